@@ -8,15 +8,18 @@ The functions mirror include/mmq.h one to one (same names without the `mmq_` pre
 
     act_bytes, act_region_offsets, quantize_act, packed_bytes, repack_weights, gemm,
     gemm_id_workspace_bytes, gemm_id, gemm_id_noalloc, gemm_id_noalloc_max_workspace_bytes,
+    group_bytes, group_region_offsets, group_rows, moe_gather, moe_combine, moe_combine_grad,
     status_string
 
-plus host-side encoders/decoders of the documented act layouts (`act_to_host`,
-`act_q8_1_pack_host` and friends for q8_1, `act_i8_pack_host` / `act_i8_to_host` for the
-per-token int8 form), used by tests and the bench to fill or read act buffers.
+plus `group_views` (the regions of a plan as tensors) and host-side encoders/decoders of the
+documented act layouts (`act_to_host`, `act_q8_1_pack_host` and friends for q8_1,
+`act_i8_pack_host` / `act_i8_to_host` for the per-token int8 form), used by tests and the bench
+to fill or read act buffers.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -72,6 +75,18 @@ def lib() -> ctypes.CDLL:
     L.mmq_gemm_id_noalloc.restype = e
     L.mmq_gemm_id_noalloc_max_workspace_bytes.argtypes = []
     L.mmq_gemm_id_noalloc_max_workspace_bytes.restype = S
+    L.mmq_group_bytes.argtypes = [I, I, I]
+    L.mmq_group_bytes.restype = S
+    L.mmq_group_region_offsets.argtypes = [I, I, I, ctypes.POINTER(S)]
+    L.mmq_group_region_offsets.restype = e
+    L.mmq_group_rows.argtypes = [P, I, I, I, P, P]
+    L.mmq_group_rows.restype = e
+    L.mmq_moe_gather.argtypes = [e, P, I, P, I, I, I, I, P, I, P]
+    L.mmq_moe_gather.restype = e
+    L.mmq_moe_combine.argtypes = [e, P, I, e, P, P, I, I, I, I, P, I, P]
+    L.mmq_moe_combine.restype = e
+    L.mmq_moe_combine_grad.argtypes = [e, P, I, P, I, e, P, P, I, I, I, I, P, I, P, P]
+    L.mmq_moe_combine_grad.restype = e
     _lib = L
     return L
 
@@ -205,6 +220,197 @@ def gemm_id_noalloc(wtype, packed, E: int, act, ids, T: int, top_k: int, N: int,
     _check("mmq_gemm_id_noalloc", lib().mmq_gemm_id_noalloc(_wt(wtype), _ptr(packed), E, _ptr(act), _ptr(ids), T,
                                                              top_k, N, K, OTYPE["f32"], _ptr(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------- rows grouped by adapter or expert
+
+# A serving step makes these calls back to back, so the host's time per call counts: sizes that
+# depend on (E, T, top_k) alone are looked up once, the checks read each tensor's shape once and
+# build their messages only when they fail.
+
+def _gpu(fn: str, *tensors) -> int:
+    """The current GPU's index, on which every tensor (None skipped) has to be."""
+    import torch
+    at = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"{fn}: every tensor must be on the current GPU, got one on {t.device}")
+    return at
+
+
+def _raw_stream(stream, at: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else int(stream.cuda_stream)
+
+
+def _ld(fn: str, name: str, t, rows: int, cols: int, dtype) -> int:
+    """The row stride of a [rows, cols] tensor of `dtype` whose columns are contiguous."""
+    if t.dtype is not dtype or t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{fn}: {name} must be {dtype} {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and cols != 1:
+        raise ValueError(f"{fn}: {name}'s columns must be contiguous, got strides {t.stride()}")
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _flat(fn: str, name: str, t, shape, dtype):
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _row_otype(fn: str, t) -> int:
+    import torch
+    if t.dtype is torch.float32:
+        return 0
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{fn}: rows must be float32 or bfloat16, got {t.dtype}")
+    return 1
+
+
+def _plan_of(fn: str, plan, E: int, T: int, top_k: int):
+    import torch
+    nbytes = group_bytes(E, T, top_k)
+    if nbytes == 0:
+        raise MMQError("mmq_group_bytes", MMQ_EINVAL)
+    if plan.dtype is not torch.uint8 or plan.numel() < nbytes or not plan.is_contiguous():
+        raise ValueError(f"{fn}: plan must be the {nbytes} bytes that group_rows returns for E={E}, T={T}, top_k={top_k}")
+
+
+def _new(shape, dtype, at: int, stream):
+    """A tensor for a call's result. One made for a call on another stream than the current one
+    must outlive the call's kernels there."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=at)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+@functools.lru_cache(maxsize=4096)
+def group_bytes(E: int, T: int, top_k: int) -> int:
+    return int(lib().mmq_group_bytes(E, T, top_k))
+
+
+@functools.lru_cache(maxsize=4096)
+def group_region_offsets(E: int, T: int, top_k: int) -> tuple[int, int, int, int]:
+    arr = (ctypes.c_size_t * 4)()
+    _check("mmq_group_region_offsets", lib().mmq_group_region_offsets(E, T, top_k, arr))
+    return tuple(int(v) for v in arr)
+
+
+def group_rows(ids, E: int, out=None, stream=None):
+    """Sort the pairs' ids (CUDA int32 [T, top_k], or [T] for one id a row) by group; returns the
+    plan (uint8), shared by the calls on this batch."""
+    import torch
+    fn = "group_rows"
+    at = _gpu(fn, ids, out)
+    shape = ids.shape
+    if ids.dtype is not torch.int32 or not 1 <= len(shape) <= 2 or not ids.is_contiguous():
+        raise ValueError(f"{fn}: ids must be contiguous int32 [T] or [T, top_k], got {ids.dtype} {tuple(shape)}")
+    T, top_k = shape[0], shape[1] if len(shape) == 2 else 1
+    if out is None:
+        nbytes = group_bytes(E, T, top_k)
+        if nbytes == 0:
+            raise MMQError("mmq_group_bytes", MMQ_EINVAL)
+        out = _new(nbytes, torch.uint8, at, stream)
+    else:
+        _plan_of(fn, out, E, T, top_k)
+    _check("mmq_group_rows", lib().mmq_group_rows(ids.data_ptr(), E, T, top_k, out.data_ptr(), _raw_stream(stream, at)))
+    return out
+
+
+def group_views(plan, E: int, T: int, top_k: int = 1):
+    """The plan's regions as int32 tensors sharing its memory: offs [E+1], order [P], pos [P],
+    units [U, 4]."""
+    import torch
+    _plan_of("group_views", plan, E, T, top_k)
+    P = T * top_k
+    U = P // 64 + min(E + 1, P)
+    _, order, pos, units = group_region_offsets(E, T, top_k)
+    w = plan.view(torch.int32)
+    return (w.as_strided((E + 1,), (1,)), w.as_strided((P,), (1,), w.storage_offset() + order // 4),
+            w.as_strided((P,), (1,), w.storage_offset() + pos // 4),
+            w.as_strided((U, 4), (4, 1), w.storage_offset() + units // 4))
+
+
+def moe_gather(x, plan, E: int, top_k: int, out=None, stream=None):
+    """Token rows x (CUDA float32 or bfloat16 [T, N]) in expert order: [T * top_k, N]."""
+    fn = "moe_gather"
+    at = _gpu(fn, x, plan, out)
+    o = _row_otype(fn, x)
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T, N], got {tuple(x.shape)}")
+    T, N = x.shape
+    _plan_of(fn, plan, E, T, top_k)
+    if out is None:
+        out = _new((T * top_k, N), x.dtype, at, stream)
+    ldx = _ld(fn, "x", x, T, N, x.dtype)
+    ldr = _ld(fn, "out", out, T * top_k, N, x.dtype)
+    _check("mmq_moe_gather", lib().mmq_moe_gather(o, x.data_ptr(), ldx, plan.data_ptr(), E, T, top_k, N,
+                                                  out.data_ptr(), ldr, _raw_stream(stream, at)))
+    return out
+
+
+ROWORDER = {"pair": 0, "sorted": 1}
+
+
+def _pair_rows(fn: str, z, P: int):
+    """z [P, N], or [T, top_k, N] as gemm_id returns it, as [P, N]."""
+    if z.dim() == 3:
+        z = z.view(-1, z.shape[2])
+    if z.dim() != 2 or z.shape[0] != P:
+        raise ValueError(f"{fn}: the pairs' rows must be [T * top_k, N] or [T, top_k, N] with {P} pairs, got {tuple(z.shape)}")
+    return z
+
+
+def moe_combine(z, plan, E: int, T: int, top_k: int, weights=None, order="pair", out=None, stream=None):
+    """The experts' rows z (CUDA float32 or bfloat16 [T * top_k, N], or [T, top_k, N] as gemm_id
+    returns them) weighted and summed into tokens: [T, N]. weights: float32 [T, top_k] or None."""
+    import torch
+    fn = "moe_combine"
+    at = _gpu(fn, z, plan, weights, out)
+    o = _row_otype(fn, z)
+    _plan_of(fn, plan, E, T, top_k)
+    z = _pair_rows(fn, z, T * top_k)
+    N = z.shape[1]
+    ldz = _ld(fn, "z", z, T * top_k, N, z.dtype)
+    if weights is not None:
+        _flat(fn, "weights", weights, (T, top_k), torch.float32)
+    if out is None:
+        out = _new((T, N), z.dtype, at, stream)
+    ldy = _ld(fn, "out", out, T, N, z.dtype)
+    _check("mmq_moe_combine", lib().mmq_moe_combine(o, z.data_ptr(), ldz, ROWORDER[order], _ptr(weights),
+                                                    plan.data_ptr(), E, T, top_k, N, out.data_ptr(), ldy,
+                                                    _raw_stream(stream, at)))
+    return out
+
+
+def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=None, dw=None, stream=None):
+    """Gradients of moe_combine for the rows and the weights: dz like z, dw float32 [T, top_k]."""
+    import torch
+    fn = "moe_combine_grad"
+    at = _gpu(fn, dy, z, plan, weights, dz, dw)
+    o = _row_otype(fn, z)
+    if dy.dim() != 2:
+        raise ValueError(f"{fn}: dy must be [T, N], got {tuple(dy.shape)}")
+    T, N = dy.shape
+    P = T * top_k
+    _plan_of(fn, plan, E, T, top_k)
+    lddy = _ld(fn, "dy", dy, T, N, z.dtype)
+    if dz is None:
+        dz = _new(z.shape, z.dtype, at, stream)
+    if dw is None:
+        dw = _new((T, top_k), torch.float32, at, stream)
+    z, rows = _pair_rows(fn, z, P), _pair_rows(fn, dz, P)
+    ldz = _ld(fn, "z", z, P, N, z.dtype)
+    lddz = _ld(fn, "dz", rows, P, N, z.dtype)
+    _flat(fn, "weights", weights, (T, top_k), torch.float32)
+    _flat(fn, "dw", dw, (T, top_k), torch.float32)
+    _check("mmq_moe_combine_grad",
+           lib().mmq_moe_combine_grad(o, dy.data_ptr(), lddy, z.data_ptr(), ldz, ROWORDER[order], weights.data_ptr(),
+                                      plan.data_ptr(), E, T, top_k, N, rows.data_ptr(), lddz, dw.data_ptr(),
+                                      _raw_stream(stream, at)))
+    return dz, dw
 
 
 # -------------------------------------------------------------------------- host helpers

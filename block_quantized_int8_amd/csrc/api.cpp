@@ -1,6 +1,7 @@
 // api.cpp - the extern "C" entry points declared in include/mmq.h: argument validation on the
 // host, then a launch on the caller's stream. Nothing here allocates device memory.
 #include "mmq_internal.h"
+#include "rows.h"
 
 using namespace mmq;
 
@@ -195,6 +196,68 @@ mmq_status mmq_gemm_id_noalloc(mmq_wtype t, const void* packed, int64_t E, const
     if (e != hipSuccess) return from_hip(e);
     return from_hip(launch_gemm_id(kernel_format(t), packed, E, act, ids, T, top_k, N, K, out, ws,
                                    ID_SCRATCH_BYTES, as_stream(stream)));
+}
+
+namespace {
+bool group_ok(int64_t E, int64_t T, int64_t top_k) {
+    return E >= 1 && E <= 4096 && T >= 1 && top_k >= 1 && top_k <= E && T <= MAX_DIM / top_k;
+}
+bool row_type(mmq_otype o) { return o == MMQ_OUT_F32 || o == MMQ_OUT_BF16; }
+}  // namespace
+
+size_t mmq_group_bytes(int64_t E, int64_t T, int64_t top_k) {
+    return group_ok(E, T, top_k) ? (size_t)plan_layout(E, T * top_k).bytes : 0;
+}
+
+mmq_status mmq_group_region_offsets(int64_t E, int64_t T, int64_t top_k, size_t offsets[4]) {
+    if (!offsets || !group_ok(E, T, top_k)) return MMQ_EINVAL;
+    const PlanLayout L = plan_layout(E, T * top_k);
+    offsets[0] = (size_t)L.offs_off;
+    offsets[1] = (size_t)L.order_off;
+    offsets[2] = (size_t)L.pos_off;
+    offsets[3] = (size_t)L.units_off;
+    return MMQ_OK;
+}
+
+mmq_status mmq_group_rows(const int32_t* ids, int64_t E, int64_t T, int64_t top_k, void* plan, void* stream) {
+    if (!group_ok(E, T, top_k) || !ids || !plan) return MMQ_EINVAL;
+    if (!aligned16(ids) || !aligned16(plan)) return MMQ_EALIGN;
+    return from_hip(launch_group_rows(ids, E, T * top_k, plan, as_stream(stream)));
+}
+
+mmq_status mmq_moe_gather(mmq_otype o, const void* x, int64_t ldx, const void* plan, int64_t E, int64_t T,
+                          int64_t top_k, int64_t N, void* rows, int64_t ldr, void* stream) {
+    if (!valid_otype(o) || !group_ok(E, T, top_k) || N < 1 || N > MAX_DIM || ldx < N || ldr < N) return MMQ_EINVAL;
+    if (!x || !plan || !rows) return MMQ_EINVAL;
+    if (!row_type(o)) return MMQ_EUNSUPPORTED;
+    if (!aligned16(x) || !aligned16(plan) || !aligned16(rows)) return MMQ_EALIGN;
+    return from_hip(launch_moe_gather(o, x, ldx, plan, E, T, top_k, N, rows, ldr, as_stream(stream)));
+}
+
+mmq_status mmq_moe_combine(mmq_otype o, const void* z, int64_t ldz, mmq_roworder r, const float* w,
+                           const void* plan, int64_t E, int64_t T, int64_t top_k, int64_t N, void* y,
+                           int64_t ldy, void* stream) {
+    if (!valid_otype(o) || !group_ok(E, T, top_k) || N < 1 || N > MAX_DIM || ldz < N || ldy < N) return MMQ_EINVAL;
+    if (r != MMQ_ROWS_PAIR && r != MMQ_ROWS_SORTED) return MMQ_EINVAL;
+    if (!z || !plan || !y) return MMQ_EINVAL;
+    if (!row_type(o)) return MMQ_EUNSUPPORTED;
+    if (!aligned16(z) || !aligned16(plan) || !aligned16(y) || (w && !aligned16(w))) return MMQ_EALIGN;
+    return from_hip(launch_moe_combine(o, z, ldz, r == MMQ_ROWS_SORTED, w, plan, E, T, top_k, N, y, ldy,
+                                       as_stream(stream)));
+}
+
+mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                                mmq_roworder r, const float* w, const void* plan, int64_t E, int64_t T,
+                                int64_t top_k, int64_t N, void* dz, int64_t lddz, float* dw, void* stream) {
+    if (!valid_otype(o) || !group_ok(E, T, top_k) || N < 1 || N > MAX_DIM) return MMQ_EINVAL;
+    if (lddy < N || ldz < N || lddz < N) return MMQ_EINVAL;
+    if (r != MMQ_ROWS_PAIR && r != MMQ_ROWS_SORTED) return MMQ_EINVAL;
+    if (!dy || !z || !w || !plan || !dz || !dw) return MMQ_EINVAL;
+    if (!row_type(o)) return MMQ_EUNSUPPORTED;
+    if (!aligned16(dy) || !aligned16(z) || !aligned16(w) || !aligned16(plan) || !aligned16(dz) || !aligned16(dw))
+        return MMQ_EALIGN;
+    return from_hip(launch_moe_combine_grad(o, dy, lddy, z, ldz, r == MMQ_ROWS_SORTED, w, plan, E, T, top_k, N,
+                                            dz, lddz, dw, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,465 @@
+// rows.hip - rows grouped by the adapter or expert they use, and the expert rows' way there and
+// back: the plan (a stable counting sort on the device), the gather of token rows into expert
+// order, their weighted sum back into tokens and its gradients.
+//
+// The plan replaces nothing inside mmq_gemm_id (whose route kernel sorts for itself, in any
+// order inside an expert); it is for calls that share one grouping: the adapters' products of
+// every projection of a step, and rows that leave in expert order. Its order is stable (rising
+// pair ids inside a group), so sums over a group's rows have one order and repeat bit for bit.
+#include <algorithm>
+
+#include "mmq_internal.h"
+#include "rows.h"
+
+namespace mmq {
+namespace {
+
+// Sizes of the sort. One workgroup of GW waves takes up to GROUP_ONE pairs (each wave a
+// contiguous segment of them, so that wave order is pair order); past that, up to GROUP_MAX
+// workgroups count their segments first and a second launch places them. KEYS bounds the groups
+// (E + 1, the last being "no group") of an instance: its LDS holds one counter per wave and key.
+constexpr int64_t GROUP_ONE = 32768;
+constexpr int64_t GROUP_MAX = 256;
+
+int64_t group_blocks(int64_t P) {
+    return P <= GROUP_ONE ? 1 : std::min<int64_t>(GROUP_MAX, ceil_div(P, GROUP_ONE));
+}
+
+struct GroupArgs {
+    const int32_t* ids;
+    int P, E, seg;              // seg: pairs per workgroup
+    int32_t *offs, *order, *pos, *scratch;
+    int4* units;
+    int nunits;
+};
+
+__device__ inline int key_of(const GroupArgs& a, int p) {
+    const int e = a.ids[p];
+    return (e >= 0 && e < a.E) ? e : a.E;
+}
+
+// counts of each workgroup's segment: scratch[block][E + 1]
+template <int GW, int KEYS>
+__global__ __launch_bounds__(GW * 64) void group_count_kernel(GroupArgs a) {
+    __shared__ int cnt[KEYS];
+    const int keys = a.E + 1;
+    for (int e = threadIdx.x; e < keys; e += GW * 64) cnt[e] = 0;
+    __syncthreads();
+    const int64_t p0 = (int64_t)blockIdx.x * a.seg;
+    const int p1 = (int)min(p0 + a.seg, (int64_t)a.P);
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += GW * 64) atomicAdd(&cnt[key_of(a, (int)p)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < keys; e += GW * 64) a.scratch[(int64_t)blockIdx.x * keys + e] = cnt[e];
+}
+
+// Inclusive scan of (x, y) over the workgroup's threads.
+template <int GW>
+__device__ inline int2 block_scan(int2 v, int2* wtot) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int ox = __shfl_up(v.x, d, 64), oy = __shfl_up(v.y, d, 64);
+        if (lane >= d) {
+            v.x += ox;
+            v.y += oy;
+        }
+    }
+    if (lane == 63) wtot[wave] = v;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) {
+        v.x += wtot[w].x;
+        v.y += wtot[w].y;
+    }
+    return v;
+}
+
+// The stable sort. Every workgroup knows all counts (its own histogram if it is the only one,
+// the count kernel's otherwise); wave w of a workgroup places segment w in pair order: 64 pairs
+// at a time find the lanes of their own key by one ballot per key bit, so a pair's position is
+// the wave's running start of its key plus the lanes before it.
+template <int GW, int KEYS>
+__global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits) {
+    __shared__ int cur[GW][KEYS];
+    __shared__ int offs[KEYS + 1], uoff[KEYS + 1];
+    __shared__ int2 wtot[GW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int keys = a.E + 1, nblk = (int)gridDim.x, blk = (int)blockIdx.x;
+    for (int i = lane; i < keys; i += 64) cur[wave][i] = 0;
+    const int64_t b0 = (int64_t)blk * a.seg;
+    const int64_t b1 = min(b0 + a.seg, (int64_t)a.P);
+    const int wseg = (int)(((b1 - b0 + GW - 1) / GW + 63) & ~(int64_t)63);   // pairs per wave
+    const int64_t s0 = min(b0 + (int64_t)wave * wseg, b1), s1 = min(s0 + wseg, b1);
+    for (int64_t p = s0 + lane; p < s1; p += 64) atomicAdd(&cur[wave][key_of(a, (int)p)], 1);
+    __syncthreads();
+
+    // thread t owns keys [t*KPT, t*KPT + KPT): all pairs of a key, those of earlier workgroups,
+    // and the waves' starts
+    const int KPT = (keys + GW * 64 - 1) / (GW * 64);
+    const int e0 = min(tid * KPT, keys), e1 = min(e0 + KPT, keys);
+    int2 sum = make_int2(0, 0);
+    for (int e = e0; e < e1; ++e) {
+        int run = 0;
+        if (nblk > 1)
+            for (int b = 0; b < blk; ++b) run += a.scratch[(int64_t)b * keys + e];
+        for (int w = 0; w < GW; ++w) {
+            const int c = cur[w][e];
+            cur[w][e] = run;
+            run += c;
+        }
+        if (nblk > 1)
+            for (int b = blk + 1; b < nblk; ++b) run += a.scratch[(int64_t)b * keys + e];
+        offs[e] = run;                                       // all pairs of key e
+        sum.x += run;
+        sum.y += (run + GROUP_UNIT - 1) / GROUP_UNIT;
+    }
+    const int2 inc = block_scan<GW>(sum, wtot);
+    int px = inc.x - sum.x, py = inc.y - sum.y;
+    for (int e = e0; e < e1; ++e) {
+        const int c = offs[e];
+        for (int w = 0; w < GW; ++w) cur[w][e] += px;
+        offs[e] = px;
+        uoff[e] = py;
+        if (blk == 0) a.offs[e] = px;
+        px += c;
+        py += (c + GROUP_UNIT - 1) / GROUP_UNIT;
+    }
+    if (tid == GW * 64 - 1) {
+        offs[keys] = px;
+        uoff[keys] = py;
+    }
+    __syncthreads();
+
+    for (int u = blk * GW * 64 + tid; u < a.nunits; u += nblk * GW * 64) {
+        int4 v = make_int4(0, 0, 0, 0);
+        if (u < uoff[keys]) {
+            int lo = 0, hi = keys;                           // the last key with uoff <= u
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (uoff[mid] <= u) lo = mid; else hi = mid;
+            }
+            v.x = lo;
+            v.y = offs[lo] + (u - uoff[lo]) * GROUP_UNIT;
+            v.z = min(GROUP_UNIT, offs[lo + 1] - v.y);
+        }
+        a.units[u] = v;
+    }
+
+    for (int64_t p = s0 + lane; p - lane < s1; p += 64) {
+        const bool live = p < s1;
+        const int key = live ? key_of(a, (int)p) : 0;
+        uint64_t same = __ballot(live);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot((key >> b) & 1);
+            same &= ((key >> b) & 1) ? m : ~m;
+        }
+        const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+        if (live) {
+            const int at = cur[wave][key] + before;
+            a.order[at] = (int)p;
+            a.pos[p] = key < a.E ? at : -1;
+            // the key's first lane moves its start past the wave's pairs, after every lane's read
+            if (before == 0) cur[wave][key] = at + __popcll(same);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ token rows
+// Rows move in 16-byte pieces, also where a row's size or stride leaves them unaligned (global
+// accesses need no alignment; the piece's type says that it has only its values'); a row's last
+// piece, if it is shorter, goes value by value.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <typename T> struct Piece {
+    static constexpr int V = 16 / (int)sizeof(T);
+    u32x4 r;
+    __device__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, (uint32_t)r[i]);
+        else return __builtin_bit_cast(float, i & 1 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
+    }
+    // from V values: f32 as they are, bf16 rounded to nearest even
+    __device__ void set(const float* v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) r[i] = __builtin_bit_cast(uint32_t, v[i]);
+            else r[i] = (uint32_t)bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
+        }
+    }
+    __device__ T bits(int i) const {
+        if constexpr (sizeof(T) == 4) return (T)r[i];
+        else return (T)(r[i / 2] >> (16 * (i & 1)));
+    }
+};
+
+// T: uint32_t (f32) or uint16_t (bf16); n: the row's values from p on
+template <typename T>
+__device__ inline Piece<T> load_piece(const void* row, int64_t at, int n) {
+    const T* p = static_cast<const T*>(row) + at;
+    Piece<T> q;
+    if (n >= Piece<T>::V) {
+        q.r = *reinterpret_cast<const u32x4_any*>(p);
+        return q;
+    }
+    q.r = 0;
+#pragma unroll
+    for (int i = 0; i < Piece<T>::V; ++i)
+        if (i < n) {
+            if constexpr (sizeof(T) == 4) q.r[i] = p[i];
+            else q.r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+        }
+    return q;
+}
+
+template <typename T>
+__device__ inline void store_piece(void* row, int64_t at, const Piece<T>& q, int n) {
+    T* p = static_cast<T*>(row) + at;
+    if (n >= Piece<T>::V) {
+        *reinterpret_cast<u32x4_any*>(p) = q.r;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < Piece<T>::V; ++i)
+        if (i < n) p[i] = q.bits(i);
+}
+
+struct RowArgs {
+    const void *x, *z, *dy;
+    void *y, *dz;
+    const float* w;
+    float* dw;
+    const int32_t* pos;
+    int64_t ldx, ldz, ldy, lddz;
+    int T, top_k, N;
+    int sorted;                 // z / dz rows: 1 by sorted position, 0 by pair
+};
+
+constexpr int ROW_THREADS = 256;
+
+// the row of z that holds pair p, -1 if it has none
+__device__ inline int pair_row(const RowArgs& a, int p) {
+    const int r = a.pos[p];
+    return r < 0 ? -1 : a.sorted ? r : p;
+}
+
+// A token's row is read once and written to each of its pairs' places.
+template <typename T>
+__global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowArgs a) {
+    const int n = ((int)blockIdx.x * ROW_THREADS + (int)threadIdx.x) * Piece<T>::V;
+    if (n >= a.N) return;
+    for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
+        const Piece<T> v = load_piece<T>(a.x, (int64_t)t * a.ldx + n, a.N - n);
+        for (int j = 0; j < a.top_k; ++j) {
+            const int r = a.pos[t * a.top_k + j];
+            if (r >= 0) store_piece<T>(a.y, (int64_t)r * a.ldy + n, v, a.N - n);
+        }
+    }
+}
+
+// y[t] = sum over j of w[t][j] z[row(t, j)]: f32 sums in rising j, one rounding at the end.
+template <typename T>
+__global__ __launch_bounds__(ROW_THREADS) void combine_kernel(RowArgs a) {
+    constexpr int V = Piece<T>::V, J = 8;      // J rows in flight
+    const int n = ((int)blockIdx.x * ROW_THREADS + (int)threadIdx.x) * V;
+    if (n >= a.N) return;
+    for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = 0.f;
+        for (int j0 = 0; j0 < a.top_k; j0 += J) {
+            Piece<T> z[J];
+            float w[J];
+            bool has[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int p = t * a.top_k + j0 + j;
+                const int r = j0 + j < a.top_k ? pair_row(a, p) : -1;
+                has[j] = r >= 0;
+                if (has[j]) {
+                    w[j] = a.w ? a.w[p] : 1.f;
+                    z[j] = load_piece<T>(a.z, (int64_t)r * a.ldz + n, a.N - n);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (has[j]) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s[i] = fmaf(w[j], z[j].get(i), s[i]);
+                }
+        }
+        Piece<T> o;
+        o.set(s);
+        store_piece<T>(a.y, (int64_t)t * a.ldy + n, o, a.N - n);
+    }
+}
+
+// dz[row] = w dy[t] and dw = <dy[t], z[row]> of one pair: W waves each (the dot is summed per
+// lane, then over lanes and waves in a fixed order).
+template <typename T, int W>
+__global__ __launch_bounds__(ROW_THREADS) void combine_grad_kernel(RowArgs a) {
+    constexpr int V = Piece<T>::V, PW = ROW_THREADS / 64 / W;   // pairs per workgroup
+    __shared__ float red[ROW_THREADS / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int P = a.T * a.top_k;
+    for (int p0 = (int)blockIdx.x * PW; p0 < P; p0 += (int)gridDim.x * PW) {
+        const int p = p0 + wave / W;
+        const int r = p < P ? pair_row(a, p) : -1;
+        float dot = 0.f;
+        if (r >= 0) {
+            const float w = a.w[p];
+            const int64_t dy = (int64_t)(p / a.top_k) * a.ldy, z = (int64_t)r * a.ldz, dz = (int64_t)r * a.lddz;
+            for (int n = ((wave % W) * 64 + lane) * V; n < a.N; n += W * 64 * V) {
+                const Piece<T> g = load_piece<T>(a.dy, dy + n, a.N - n), v = load_piece<T>(a.z, z + n, a.N - n);
+                float d[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dot = fmaf(g.get(i), v.get(i), dot);
+                    d[i] = w * g.get(i);
+                }
+                Piece<T> o;
+                o.set(d);
+                store_piece<T>(a.dz, dz + n, o, a.N - n);
+            }
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
+        if constexpr (W > 1) {
+            if (lane == 0) red[wave] = dot;
+            __syncthreads();
+            dot = 0.f;
+            for (int i = 0; i < W; ++i) dot += red[wave / W * W + i];
+            __syncthreads();
+        }
+        if (p < P && wave % W == 0 && lane == 0) a.dw[p] = dot;
+    }
+}
+
+constexpr int64_t GRID_MAX = int64_t(1) << 20;      // workgroups of a launch; they loop past it
+constexpr int GRID_Y = 65535;                        // tokens of a launch's grid; it loops past them
+
+}  // namespace
+
+PlanLayout plan_layout(int64_t E, int64_t P) {
+    PlanLayout L;
+    L.nunits = P / GROUP_UNIT + std::min<int64_t>(E + 1, P);
+    L.offs_off = 0;
+    L.order_off = round_up((E + 1) * 4, REGION_ALIGN);
+    L.pos_off = L.order_off + round_up(P * 4, REGION_ALIGN);
+    L.units_off = L.pos_off + round_up(P * 4, REGION_ALIGN);
+    L.scratch_off = L.units_off + round_up(L.nunits * 16, REGION_ALIGN);
+    const int64_t blocks = group_blocks(P);
+    L.bytes = L.scratch_off + (blocks > 1 ? round_up(blocks * (E + 1) * 4, REGION_ALIGN) : 0);
+    return L;
+}
+
+hipError_t launch_group_rows(const int32_t* ids, int64_t E, int64_t P, void* plan, hipStream_t s) {
+    const PlanLayout L = plan_layout(E, P);
+    uint8_t* base = static_cast<uint8_t*>(plan);
+    GroupArgs a;
+    a.ids = ids;
+    a.P = (int)P;
+    a.E = (int)E;
+    const int64_t blocks = group_blocks(P);
+    a.seg = (int)ceil_div(P, blocks);
+    a.offs = reinterpret_cast<int32_t*>(base + L.offs_off);
+    a.order = reinterpret_cast<int32_t*>(base + L.order_off);
+    a.pos = reinterpret_cast<int32_t*>(base + L.pos_off);
+    a.units = reinterpret_cast<int4*>(base + L.units_off);
+    a.scratch = reinterpret_cast<int32_t*>(base + L.scratch_off);
+    a.nunits = (int)L.nunits;
+    int bits = 1;
+    while ((int64_t(1) << bits) < E + 1) ++bits;
+    // 16 waves while their counters fit in LDS (1024 keys: 64 KB), else 4 (4097 keys: 64 KB)
+    if (E + 1 <= 1024) {
+        if (blocks > 1)
+            hipLaunchKernelGGL((group_count_kernel<16, 1024>), dim3(blocks), dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((group_kernel<16, 1024>), dim3(blocks), dim3(1024), 0, s, a, bits);
+    } else {
+        if (blocks > 1)
+            hipLaunchKernelGGL((group_count_kernel<4, 4097>), dim3(blocks), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((group_kernel<4, 4097>), dim3(blocks), dim3(256), 0, s, a, bits);
+    }
+    return hipGetLastError();
+}
+
+namespace {
+// workgroups along a row (of T's values) x tokens
+template <typename T> dim3 row_grid(const RowArgs& a) {
+    return dim3((unsigned)ceil_div(a.N, ROW_THREADS * Piece<T>::V), (unsigned)std::min(a.T, GRID_Y));
+}
+}  // namespace
+
+hipError_t launch_moe_gather(mmq_otype o, const void* x, int64_t ldx, const void* plan, int64_t E,
+                             int64_t T, int64_t top_k, int64_t N, void* rows, int64_t ldr, hipStream_t s) {
+    const PlanLayout L = plan_layout(E, T * top_k);
+    RowArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.y = rows;
+    a.ldy = ldr;
+    a.pos = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan) + L.pos_off);
+    a.T = (int)T;
+    a.top_k = (int)top_k;
+    a.N = (int)N;
+    if (o == MMQ_OUT_F32)
+        hipLaunchKernelGGL(gather_kernel<uint32_t>, row_grid<uint32_t>(a), dim3(ROW_THREADS), 0, s, a);
+    else
+        hipLaunchKernelGGL(gather_kernel<uint16_t>, row_grid<uint16_t>(a), dim3(ROW_THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(mmq_otype o, const void* z, int64_t ldz, bool sorted, const float* w,
+                              const void* plan, int64_t E, int64_t T, int64_t top_k, int64_t N, void* y,
+                              int64_t ldy, hipStream_t s) {
+    const PlanLayout L = plan_layout(E, T * top_k);
+    RowArgs a = {};
+    a.z = z;
+    a.ldz = ldz;
+    a.sorted = sorted;
+    a.w = w;
+    a.y = y;
+    a.ldy = ldy;
+    a.pos = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan) + L.pos_off);
+    a.T = (int)T;
+    a.top_k = (int)top_k;
+    a.N = (int)N;
+    if (o == MMQ_OUT_F32)
+        hipLaunchKernelGGL(combine_kernel<uint32_t>, row_grid<uint32_t>(a), dim3(ROW_THREADS), 0, s, a);
+    else
+        hipLaunchKernelGGL(combine_kernel<uint16_t>, row_grid<uint16_t>(a), dim3(ROW_THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                                   bool sorted, const float* w, const void* plan, int64_t E, int64_t T,
+                                   int64_t top_k, int64_t N, void* dz, int64_t lddz, float* dw, hipStream_t s) {
+    const int64_t P = T * top_k;
+    const PlanLayout L = plan_layout(E, P);
+    RowArgs a = {};
+    a.dy = dy;
+    a.ldy = lddy;
+    a.z = z;
+    a.ldz = ldz;
+    a.sorted = sorted;
+    a.w = w;
+    a.dz = dz;
+    a.lddz = lddz;
+    a.dw = dw;
+    a.pos = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan) + L.pos_off);
+    a.T = (int)T;
+    a.top_k = (int)top_k;
+    a.N = (int)N;
+    constexpr int W = ROW_THREADS / 64;
+    // a wave per pair, or all four of a workgroup while that leaves the chip's waves idle
+    const bool wide = P < 4096;
+    const dim3 grid((unsigned)std::min<int64_t>(wide ? P : ceil_div(P, W), GRID_MAX));
+    if (o == MMQ_OUT_F32) {
+        if (wide) hipLaunchKernelGGL((combine_grad_kernel<uint32_t, W>), grid, dim3(ROW_THREADS), 0, s, a);
+        else hipLaunchKernelGGL((combine_grad_kernel<uint32_t, 1>), grid, dim3(ROW_THREADS), 0, s, a);
+    } else {
+        if (wide) hipLaunchKernelGGL((combine_grad_kernel<uint16_t, W>), grid, dim3(ROW_THREADS), 0, s, a);
+        else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 1>), grid, dim3(ROW_THREADS), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mmq

@@ -252,6 +252,69 @@ mmq_status mmq_gemm_id_noalloc(mmq_wtype t, const void* packed, int64_t E, const
 /* Size of mmq_gemm_id_noalloc's static workspace, in bytes (host). */
 size_t mmq_gemm_id_noalloc_max_workspace_bytes(void);
 
+/* ---------------------------------------------------------------------------------------
+ * Rows that carry the index of a weight set: an adapter (mmq_lora) or an expert. A batch's
+ * P = T * top_k pairs (pair p = t * top_k + j, its index ids[p]) are sorted once into a plan,
+ * which every call on that batch shares (all projections of all layers).
+ *
+ * Plan buffer (int32 words, regions on 256-byte boundaries in this order):
+ *   region 0  offs  [E + 1]: group e holds the sorted positions offs[e] .. offs[e + 1] - 1
+ *   region 1  order [P]: the pair at each sorted position, by rising group and inside a group by
+ *             rising pair; the pairs without a group (an id outside [0, E)) follow offs[E],
+ *             rising
+ *   region 2  pos   [P]: the sorted position of pair p, -1 for a pair without a group
+ *   region 3  units [U][4], U = P / 64 + min(E + 1, P): up to 64 consecutive positions of one
+ *             group each, as (group, first position, positions, 0), in sorted order; the pairs
+ *             without a group are group E; unused entries hold zeros
+ *   region 4  the sort's scratch (its contents mean nothing afterwards)
+ * --------------------------------------------------------------------------------------- */
+
+/* Total bytes of a plan; 0 if the arguments are invalid: 1 <= E <= 4096, 1 <= top_k <= E,
+ * T >= 1, T * top_k <= 2^24. (host) */
+size_t mmq_group_bytes(int64_t E, int64_t T, int64_t top_k);
+
+/* Byte offsets of the plan's regions 0..3, written to offsets[0..3] (host). MMQ_EINVAL for
+ * invalid arguments. */
+mmq_status mmq_group_region_offsets(int64_t E, int64_t T, int64_t top_k, size_t offsets[4]);
+
+/* Sort the pairs' ids [T][top_k] (device, int32) into `plan` (device, mmq_group_bytes bytes).
+ * Every word of regions 0..3 is written (not the gaps between them). The sort is stable, so the
+ * plan depends on the ids alone. */
+mmq_status mmq_group_rows(const int32_t* ids, int64_t E, int64_t T, int64_t top_k, void* plan,
+                          void* stream);
+
+/* Which row of a [T * top_k] row buffer holds pair p: row p (the order of mmq_gemm_id's output)
+ * or row pos[p] (expert order, as mmq_moe_gather writes it). */
+typedef enum { MMQ_ROWS_PAIR = 0, MMQ_ROWS_SORTED = 1 } mmq_roworder;
+
+/* The three calls below move rows of N values, f32 (MMQ_OUT_F32) or bf16 (MMQ_OUT_BF16; any
+ * other type is MMQ_EUNSUPPORTED). `plan` is a plan of the same E, T and top_k. Row strides ld*
+ * are in elements, >= N and otherwise free (a stride that is no multiple of 16 bytes is
+ * allowed); columns past N are neither read nor written. 1 <= N <= 2^24. Outputs must not
+ * overlap inputs. */
+
+/* Tokens sorted by expert: rows[pos[p]] = x[p / top_k] for every pair with a group; the rows
+ * from offs[E] on are left untouched. x is [T][ldx], rows [T * top_k][ldr] (device). Its
+ * gradient is mmq_moe_combine of the rows' gradients with w = NULL and MMQ_ROWS_SORTED. */
+mmq_status mmq_moe_gather(mmq_otype o, const void* x, int64_t ldx, const void* plan, int64_t E,
+                          int64_t T, int64_t top_k, int64_t N, void* rows, int64_t ldr, void* stream);
+
+/* And back, with weights applied: y[t] = sum over j of w[t][j] * z[row of pair (t, j)], summed
+ * in f32 in rising j and rounded once. A pair without a group counts nothing and its row is not
+ * read; a token without any such pair gets zeros. z is [T * top_k][ldz] in row order `r`, w f32
+ * [T][top_k] or NULL (every weight 1), y [T][ldy] (device). */
+mmq_status mmq_moe_combine(mmq_otype o, const void* z, int64_t ldz, mmq_roworder r, const float* w,
+                           const void* plan, int64_t E, int64_t T, int64_t top_k, int64_t N, void* y,
+                           int64_t ldy, void* stream);
+
+/* Gradients of mmq_moe_combine: dz[row of pair (t, j)] = w[t][j] * dy[t], and
+ * dw[t][j] = sum over n of dy[t][n] * z[row of pair (t, j)][n] in f32 (in a fixed order). For a
+ * pair without a group dw is 0 and its row of z is not read; no row of dz but those of pairs with
+ * a group is written. dy is [T][lddy], dz [T * top_k][lddz] in row order `r`, dw f32 [T][top_k]. */
+mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                                mmq_roworder r, const float* w, const void* plan, int64_t E, int64_t T,
+                                int64_t top_k, int64_t N, void* dz, int64_t lddz, float* dw, void* stream);
+
 /* Static, human-readable name of a status code (host). */
 const char* mmq_status_string(mmq_status s);
 

@@ -1,0 +1,37 @@
+"""Plain numpy models, in 64 bits, of the calls on rows grouped by adapter or expert."""
+import numpy as np
+
+
+def plan(ids, E):
+    """(offs, order, pos, units) of ids [T, top_k] or [T], as mmq.h defines the plan's regions."""
+    flat = np.asarray(ids).reshape(-1)
+    P = flat.size
+    key = np.where((flat >= 0) & (flat < E), flat, E).astype(np.int64)
+    order = np.argsort(key, kind="stable")
+    count = np.bincount(key, minlength=E + 1)
+    offs = np.concatenate([[0], np.cumsum(count)])
+    pos = np.full(P, -1, np.int64)
+    n = int(offs[E])
+    pos[order[:n]] = np.arange(n)
+    units = []
+    for g in range(E + 1):
+        for first in range(int(offs[g]), int(offs[g + 1]), 64):
+            units.append((g, first, min(64, int(offs[g + 1]) - first), 0))
+    full = np.zeros((P // 64 + min(E + 1, P), 4), np.int64)
+    if units:
+        full[:len(units)] = units
+    return offs[:E + 1], order, pos, full
+
+
+def row_of(ids, E, order):
+    """The row of each pair ([T, top_k]) in a row buffer of `order`, -1 for a pair without one."""
+    ids = np.asarray(ids)
+    pos = plan(ids, E)[2]
+    row = pos if order == "sorted" else np.where(pos >= 0, np.arange(ids.size), -1)
+    return row.reshape(ids.shape)
+
+
+def bf16(x):
+    """x rounded to bf16 (nearest even), as f32."""
+    u = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    return (((u + 0x7FFF + ((u >> 16) & 1)) >> 16) << 16).astype(np.uint32).view(np.float32)

@@ -1,0 +1,242 @@
+"""Rows grouped by expert on the GPU, through the public binding: the plan against a numpy sort,
+the gather bit for bit, the combination and its gradients against 64-bit sums.
+
+Tolerances. An f32 sum of k products, fused multiply-adds in any order, is off by at most
+k * 2^-24 * sum |terms| (first order; 1.01 covers the rest); a value rounded once to bf16 by at
+most 2^-8 of itself, on top."""
+import numpy as np
+import pytest
+
+import rowmodel
+
+pytestmark = pytest.mark.gpu
+
+U24, U8 = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    import block_quantized_int8_amd as mmq
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mmq.lib()
+    return torch, mmq
+
+
+def _ids(T, top_k, E, away, seed, wild=False):
+    r = np.random.default_rng([seed, T, top_k, E])
+    ids = np.argsort(r.random((T, E)), axis=1)[:, :top_k].astype(np.int32) if E <= 512 else \
+        r.integers(0, E, (T, top_k)).astype(np.int32)
+    if wild:                                # the same expert twice, and ids far outside the range
+        ids[:, -1] = ids[:, 0]
+        ids[r.random(ids.shape) < 0.1] = np.iinfo(np.int32).max
+        ids[r.random(ids.shape) < 0.1] = np.iinfo(np.int32).min
+        ids[r.random(ids.shape) < 0.1] = E
+    ids[r.random(ids.shape) < away] = -1
+    return ids
+
+
+PLANS = [(1, 1, 1, 0.0), (1, 1, 1, 1.0), (7, 1, 3, 0.3), (64, 1, 1, 0.0), (65, 1, 1, 0.0), (10, 8, 64, 0.0),
+         (513, 3, 5, 0.5), (300, 17, 33, 0.1), (1025, 2, 1023, 0.0), (777, 2, 1024, 0.2), (900, 5, 4096, 0.1),
+         (32768, 1, 9, 0.1), (32769, 1, 9, 0.1), (20001, 4, 130, 0.0), (70000, 1, 1, 0.0), (11003, 3, 2000, 0.3)]
+
+
+@pytest.mark.parametrize("T,top_k,E,away", PLANS)
+def test_plan_is_the_stable_sort(env, T, top_k, E, away):
+    torch, mmq = env
+    print(f"[case] plan T={T} top_k={top_k} E={E} away={away}", flush=True)
+    ids = _ids(T, top_k, E, away, 1, wild=T % 3 == 0)
+    plan = torch.full((mmq.group_bytes(E, T, top_k),), 0xA5, dtype=torch.uint8, device="cuda")
+    mmq.group_rows(torch.from_numpy(ids).cuda(), E, out=plan)
+    got = [v.cpu().numpy() for v in mmq.group_views(plan, E, T, top_k)]
+    for name, g, w in zip(("offs", "order", "pos", "units"), got, rowmodel.plan(ids, E)):
+        assert np.array_equal(g, w), name
+
+
+def _dtype(torch, name):
+    return {"f32": torch.float32, "bf16": torch.bfloat16}[name]
+
+
+def _host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _strided(torch, rows, N, ld, dt, fill, seed):
+    """[rows, N] inside a [rows, ld] buffer, random values over a filled frame."""
+    buf = torch.full((rows, ld), fill, dtype=dt, device="cuda")
+    g = torch.Generator().manual_seed(seed)
+    buf[:, :N] = torch.randn((rows, N), generator=g).to(dt).cuda()
+    return buf, buf[:, :N]
+
+
+ROWS = [("f32", 1, 1, 1, 1, 1, 0.0), ("bf16", 1, 1, 1, 1, 1, 0.0), ("bf16", 5, 2, 3, 7, 7, 0.2),
+        ("f32", 3, 3, 4, 3, 5, 0.3), ("bf16", 9, 4, 8, 1001, 1001, 0.25), ("f32", 33, 8, 64, 1030, 1031, 0.0),
+        ("bf16", 40, 9, 16, 2052, 2060, 0.5), ("f32", 20, 17, 33, 260, 260, 0.1), ("f32", 130, 4, 8, 4096, 4096, 1.0),
+        ("bf16", 1100, 4, 8, 520, 521, 0.5), ("f32", 1030, 5, 8, 90, 91, 0.1), ("f32", 66000, 1, 2, 5, 5, 0.1)]
+
+
+@pytest.mark.parametrize("dt,T,top_k,E,N,ld,away", ROWS)
+def test_gather(env, dt, T, top_k, E, N, ld, away):
+    torch, mmq = env
+    print(f"[case] gather {dt} T={T} top_k={top_k} E={E} N={N} ld={ld}", flush=True)
+    ids = _ids(T, top_k, E, away, 2, wild=top_k > 2)
+    _, x = _strided(torch, T, N, ld, _dtype(torch, dt), 3.0, 5)
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    buf = torch.full((T * top_k, ld + 3), -7.0, dtype=x.dtype, device="cuda")
+    mmq.moe_gather(x, plan, E, top_k, out=buf[:, :N])
+    want = np.full((T * top_k, ld + 3), -7.0)
+    row = rowmodel.row_of(ids, E, "sorted")
+    t, j = np.nonzero(row >= 0)
+    want[row[t, j], :N] = _host(x)[t]
+    assert np.array_equal(_host(buf), want)
+
+
+@pytest.mark.parametrize("order", ["pair", "sorted"])
+@pytest.mark.parametrize("dt,T,top_k,E,N,ld,away", ROWS)
+def test_combine(env, dt, T, top_k, E, N, ld, away, order):
+    torch, mmq = env
+    print(f"[case] combine {dt} {order} T={T} top_k={top_k} E={E} N={N} ld={ld}", flush=True)
+    ids = _ids(T, top_k, E, away, 3, wild=top_k > 2)
+    row = rowmodel.row_of(ids, E, order)
+    zb, z = _strided(torch, T * top_k, N, ld, _dtype(torch, dt), 3.0, 6)
+    used = np.zeros(T * top_k, bool)
+    used[row[row >= 0]] = True
+    z[torch.from_numpy(~used).cuda()] = float("nan")          # rows of no pair: never read
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    w = np.random.default_rng(4).standard_normal((T, top_k)).astype(np.float32)
+    w[row < 0] = np.nan                                       # nor their weights' values used
+    zh = np.where(used[:, None], _host(z), 0.0)
+    for weights in (w, None):
+        wh = np.where(row >= 0, 1.0 if weights is None else weights, 0.0).astype(np.float64)
+        terms = wh[:, :, None] * zh[np.maximum(row, 0)]
+        want, bound = terms.sum(1), np.abs(terms).sum(1) * top_k * U24 * 1.01
+        if dt == "bf16":
+            bound += (np.abs(want) + bound) * U8
+        buf = torch.full((T, ld + 1), -7.0, dtype=z.dtype, device="cuda")
+        mmq.moe_combine(z, plan, E, T, top_k, weights=None if weights is None else torch.from_numpy(w).cuda(),
+                        order=order, out=buf[:, :N])
+        got = _host(buf)
+        assert np.all(got[:, N:] == -7.0)
+        assert np.all(np.abs(got[:, :N] - want) <= bound)
+        assert np.all(got[(row < 0).all(1), :N] == 0.0)
+
+
+@pytest.mark.parametrize("order", ["pair", "sorted"])
+@pytest.mark.parametrize("dt,T,top_k,E,N,ld,away", ROWS)
+def test_combine_grad(env, dt, T, top_k, E, N, ld, away, order):
+    torch, mmq = env
+    print(f"[case] combine_grad {dt} {order} T={T} top_k={top_k} E={E} N={N} ld={ld}", flush=True)
+    ids = _ids(T, top_k, E, away, 7, wild=top_k > 2)
+    row = rowmodel.row_of(ids, E, order)
+    _, z = _strided(torch, T * top_k, N, ld, _dtype(torch, dt), 3.0, 8)
+    used = np.zeros(T * top_k, bool)
+    used[row[row >= 0]] = True
+    z[torch.from_numpy(~used).cuda()] = float("nan")
+    _, dy = _strided(torch, T, N, ld + 2, _dtype(torch, dt), 3.0, 9)
+    w = np.random.default_rng(5).standard_normal((T, top_k)).astype(np.float32)
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    buf = torch.full((T * top_k, ld + 1), -7.0, dtype=z.dtype, device="cuda")
+    dz, dw = mmq.moe_combine_grad(dy, z, plan, E, top_k, torch.from_numpy(w).cuda(), order=order, dz=buf[:, :N])
+    got, dyh, zh = _host(buf), _host(dy), np.where(used[:, None], _host(z), 0.0)
+    t, j = np.nonzero(row >= 0)
+    want = np.full((T * top_k, ld + 1), -7.0)
+    want[row[t, j], :N] = w[t, j, None].astype(np.float64) * dyh[t]
+    off = np.abs(got - want)
+    assert np.all(off[~used] == 0) and np.all(off[:, N:] == 0)
+    step = U24 if dt == "f32" else U24 + U8 * (1 + U24)
+    assert np.all(off <= np.abs(want) * step)
+    terms = np.zeros((T, top_k, N))
+    terms[t, j] = dyh[t] * zh[row[t, j]]
+    # each lane sums its share of N, then lanes and waves join
+    bound = np.abs(terms).sum(2) * (N + 10) * U24 * 1.01
+    g = dw.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(g - terms.sum(2)) <= bound)
+    assert np.all(g[row < 0] == 0)
+
+
+def test_combine_grad_against_differences(env):
+    """The gradients against central differences of the forward call's loss <y, c>, which is linear
+    in z and in w, so that a difference of any step is the derivative up to rounding."""
+    torch, mmq = env
+    T, top_k, E, N = 6, 3, 4, 40
+    ids = _ids(T, top_k, E, 0.2, 11)
+    row = rowmodel.row_of(ids, E, "pair")
+    g = torch.Generator().manual_seed(3)
+    z, c = torch.randn((T * top_k, N), generator=g).cuda(), torch.randn((T, N), generator=g).cuda()
+    w = torch.randn((T, top_k), generator=g).cuda()
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    dz, dw = mmq.moe_combine_grad(c, z, plan, E, top_k, w, dz=torch.zeros_like(z))
+    loss = lambda zz, ww: (mmq.moe_combine(zz, plan, E, T, top_k, weights=ww).double() * c.double()).sum().item()  # noqa: E731
+    scale = (w[:, :, None].abs() * z.view(T, top_k, N).abs() * c[:, None].abs()).sum().item()
+    for t, j, n in ((0, 0, 0), (3, 1, 17), (5, 2, 39), (2, 2, 5)):
+        p = t * top_k + j
+        zp, zm, wp, wm = z.clone(), z.clone(), w.clone(), w.clone()
+        zp[p, n] += 1
+        zm[p, n] -= 1
+        wp[t, j] += 1
+        wm[t, j] -= 1
+        # both losses are sums within 4 * 2^-24 of their terms' magnitudes (at most `scale` + the step's)
+        tol = 2 * 4 * U24 * (scale + abs(float(c[t].abs().sum())) * 8)
+        live = row[t, j] >= 0
+        assert abs((loss(zp, w) - loss(zm, w)) / 2 - (dz[p, n].item() if live else 0.0)) <= tol
+        assert abs((loss(z, wp) - loss(z, wm)) / 2 - dw[t, j].item()) <= tol
+
+
+def test_row_calls_in_a_graph_and_on_a_stream(env):
+    """Plan, gather, combination and gradients captured once and replayed with new ids and rows;
+    each replay equals the eager calls, made on another stream, bit for bit."""
+    torch, mmq = env
+    T, top_k, E, N = 90, 4, 12, 333
+    ids, x = torch.zeros((T, top_k), dtype=torch.int32, device="cuda"), torch.zeros((T, N), device="cuda")
+    w, dy = torch.zeros((T, top_k), device="cuda"), torch.zeros((T, N), device="cuda")
+    res = {}
+
+    def path(stream=None):
+        plan = mmq.group_rows(ids, E, stream=stream)
+        rows = mmq.moe_gather(x, plan, E, top_k, stream=stream)
+        y = mmq.moe_combine(rows, plan, E, T, top_k, weights=w, order="sorted", stream=stream)
+        dz, dw = mmq.moe_combine_grad(dy, rows, plan, E, top_k, w, order="sorted", stream=stream)
+        dx = mmq.moe_combine(dz, plan, E, T, top_k, order="sorted", stream=stream)
+        return y, dw, dx
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        path()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res["out"] = path()
+    for rep in range(4):
+        gen = torch.Generator().manual_seed(rep)
+        ids.copy_(torch.from_numpy(_ids(T, top_k, E, 0.2, 20 + rep)))
+        x.copy_(torch.randn((T, N), generator=gen))
+        w.copy_(torch.randn((T, top_k), generator=gen))
+        dy.copy_(torch.randn((T, N), generator=gen))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        other = torch.cuda.Stream()
+        eager = path(other)                       # enqueued on `other`, whatever the current stream is
+        other.synchronize()
+        for a, b in zip(res["out"], eager):
+            assert torch.equal(a, b), rep
+
+
+def test_plan_must_fit(env):
+    torch, mmq = env
+    ids = torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    plan = mmq.group_rows(ids, 4)
+    with pytest.raises(ValueError, match="plan"):
+        mmq.moe_gather(torch.zeros((4000, 8), device="cuda"), plan, 4, 2)
+    with pytest.raises(ValueError, match="ids"):
+        mmq.group_rows(ids.long(), 4)
+    with pytest.raises(ValueError, match="ids"):
+        mmq.group_rows(ids[:, :1], 4)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        mmq.moe_gather(torch.zeros((8, 8), device="cuda", dtype=torch.float16), plan, 4, 2)
+    with pytest.raises(ValueError, match="weights"):
+        mmq.moe_combine(torch.zeros((16, 8), device="cuda"), plan, 4, 8, 2, weights=torch.zeros((16, 1), device="cuda"))
+    with pytest.raises(mmq.MMQError):
+        mmq.group_rows(ids, 1)                     # top_k > E
