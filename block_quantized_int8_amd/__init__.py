@@ -9,7 +9,7 @@ The functions mirror include/mmq.h one to one (same names without the `mmq_` pre
     act_bytes, act_region_offsets, quantize_act, packed_bytes, repack_weights, gemm,
     gemm_id_workspace_bytes, gemm_id, gemm_id_noalloc, gemm_id_noalloc_max_workspace_bytes,
     group_bytes, group_region_offsets, group_rows, moe_gather, moe_combine, moe_combine_grad,
-    status_string
+    lora_workspace_bytes, lora, status_string
 
 plus `group_views` (the regions of a plan as tensors) and host-side encoders/decoders of the
 documented act layouts (`act_to_host`, `act_q8_1_pack_host` and friends for q8_1,
@@ -87,6 +87,10 @@ def lib() -> ctypes.CDLL:
     L.mmq_moe_combine.restype = e
     L.mmq_moe_combine_grad.argtypes = [e, P, I, P, I, e, P, P, I, I, I, I, P, I, P, P]
     L.mmq_moe_combine_grad.restype = e
+    L.mmq_lora_workspace_bytes.argtypes = [I, I, I, I]
+    L.mmq_lora_workspace_bytes.restype = S
+    L.mmq_lora.argtypes = [e, P, e, P, P, P, I, I, P, I, I, I, P, I, P, I, P, P, S, P]
+    L.mmq_lora.restype = e
     _lib = L
     return L
 
@@ -411,6 +415,72 @@ def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=
                                       plan.data_ptr(), E, T, top_k, N, rows.data_ptr(), lddz, dw.data_ptr(),
                                       _raw_stream(stream, at)))
     return dz, dw
+
+
+# ---------------------------------------------------- adapters beside a shared projection
+
+ADTYPE = {"bf16": 0, "f16": 1}
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_workspace_bytes(E: int, M: int, K: int, R: int) -> int:
+    return int(lib().mmq_lora_workspace_bytes(E, M, K, R))
+
+
+@functools.lru_cache(maxsize=4096)
+def _act_need(atype: int, M: int, K: int) -> int:
+    return int(lib().mmq_act_bytes(atype, M, K))
+
+
+def _adapters(fn: str, act, A, B, scale, plan, M: int, at_: int):
+    """Checks what both adapter calls read; returns (adapter type, E, R, K, N)."""
+    import torch
+    if A.dtype is torch.bfloat16:
+        d = 0
+    elif A.dtype is torch.float16:
+        d = 1
+    else:
+        raise ValueError(f"{fn}: adapters must be bfloat16 or float16, got {A.dtype}")
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError(f"{fn}: A must be [E, R, K] and B [E, N, R], got {tuple(A.shape)} and {tuple(B.shape)}")
+    E, R, K = A.shape
+    N = B.shape[1]
+    _flat(fn, "A", A, (E, R, K), A.dtype)
+    _flat(fn, "B", B, (E, N, R), A.dtype)
+    _flat(fn, "scale", scale, (E,), torch.float32)
+    _plan_of(fn, plan, E, M, 1)
+    need = _act_need(at_, M, K)
+    if act.dtype is not torch.uint8 or act.numel() < max(need, 1) or not act.is_contiguous():
+        raise ValueError(f"{fn}: act must be the {need} bytes that quantize_act returns for M={M}, K={K}")
+    return d, E, R, K, N
+
+
+def lora(act, A, B, scale, plan, M: int, atype="q8_1", base=None, out=None, v=None, workspace=None, stream=None):
+    """Adds the rows' low-rank adapters to a projection's output: out = base + scale (x^ A^T) B^T,
+    with A [E, R, K], B [E, N, R] (bfloat16 or float16), scale float32 [E] and the plan of the
+    rows' adapters (group_rows of int32 [M]). base, out: [M, N] float32 (q8_1) or bfloat16
+    (i8_token); out=base adds in place, base=None starts from zeros. Returns (out, v), v = x^ A^T
+    float32 [M, R] being what lora_grad needs."""
+    import torch
+    fn = "lora"
+    at = _gpu(fn, act, A, B, scale, plan, base, out, v, workspace)
+    at_ = _at(atype)
+    d, E, R, K, N = _adapters(fn, act, A, B, scale, plan, M, at_)
+    dt = torch.float32 if at_ == 0 else torch.bfloat16
+    if out is None:
+        out = _new((M, N), dt, at, stream)
+    if v is None:
+        v = _new((M, R), torch.float32, at, stream)
+    else:
+        _flat(fn, "v", v, (M, R), torch.float32)
+    if workspace is None:
+        workspace = _new(lora_workspace_bytes(E, M, K, R), torch.uint8, at, stream)
+    ldo = _ld(fn, "out", out, M, N, dt)
+    ldb = _ld(fn, "base", base, M, N, dt) if base is not None else 0
+    _check("mmq_lora", lib().mmq_lora(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
+                                      plan.data_ptr(), M, N, K, _ptr(base), ldb, out.data_ptr(), ldo, v.data_ptr(),
+                                      workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, at)))
+    return out, v
 
 
 # -------------------------------------------------------------------------- host helpers

@@ -2,6 +2,7 @@
 // host, then a launch on the caller's stream. Nothing here allocates device memory.
 #include "mmq_internal.h"
 #include "rows.h"
+#include "lora.h"
 
 using namespace mmq;
 
@@ -258,6 +259,33 @@ mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const
         return MMQ_EALIGN;
     return from_hip(launch_moe_combine_grad(o, dy, lddy, z, ldz, r == MMQ_ROWS_SORTED, w, plan, E, T, top_k, N,
                                             dz, lddz, dw, as_stream(stream)));
+}
+
+namespace {
+bool lora_sizes_ok(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    return sizes_ok(M, N, K) && K % QK == 0 && R >= 8 && R <= LORA_MAX_R && R % 8 == 0 && group_ok(E, M, 1) &&
+           lora_grid_ok(E, M, N, K);
+}
+}  // namespace
+
+size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R) {
+    return lora_sizes_ok(E, M, 1, K, R) ? lora_workspace_bytes(E, M, K, R) : 0;
+}
+
+mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B, const float* scale,
+                    int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const void* base,
+                    int64_t ldb, void* out, int64_t ldo, float* v, void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_atype(a) || (d != MMQ_ADAPTER_BF16 && d != MMQ_ADAPTER_F16)) return MMQ_EINVAL;
+    if (!lora_sizes_ok(E, M, N, K, R) || ldo < N || (base && ldb < N)) return MMQ_EINVAL;
+    if (!act || !A || !B || !scale || !plan || !out || !v) return MMQ_EINVAL;
+    if (base == out && ldb != ldo) return MMQ_EINVAL;
+    if (!aligned16(act) || !aligned16(A) || !aligned16(B) || !aligned16(scale) || !aligned16(plan) ||
+        (base && !aligned16(base)) || !aligned16(out) || !aligned16(v))
+        return MMQ_EALIGN;
+    if (!workspace || ws_bytes < lora_workspace_bytes(E, M, K, R)) return MMQ_EWORKSPACE;
+    if (!aligned16(workspace)) return MMQ_EALIGN;
+    return from_hip(launch_lora(a, d == MMQ_ADAPTER_F16, act, A, B, scale, E, R, plan, M, N, K, base, ldb, out, ldo,
+                                v, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -315,6 +315,48 @@ mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const
                                 mmq_roworder r, const float* w, const void* plan, int64_t E, int64_t T,
                                 int64_t top_k, int64_t N, void* dz, int64_t lddz, float* dw, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection. Row m of the batch uses
+ * adapter e = ids[m] (the ids that `plan` was made from, with top_k = 1); adapter e is the pair
+ * A[e] [R][K], B[e] [N][R] with a scale, in bf16 or f16:
+ *
+ *     v[m][r]   = sum_k x^[m][k] * A[e][r][k]
+ *     out[m][n] = base[m][n] + scale[e] * sum_r v[m][r] * B[e][n][r]
+ *
+ * x^ are the values that the act buffer stands for: xs * xq (MMQ_ACT_Q8_1) or sa * a
+ * (MMQ_ACT_I8_TOKEN), so the adapters see the same quantised activations as the projection.
+ * A row without an adapter gets v = 0 and out = base. Products and sums are f32-exact products
+ * with f32 sums (no operand is rounded); `out` is rounded once to its type. Results repeat bit
+ * for bit. Adapters, scales and `base` must be finite.
+ * --------------------------------------------------------------------------------------- */
+typedef enum { MMQ_ADAPTER_BF16 = 0, MMQ_ADAPTER_F16 = 1 } mmq_adtype;
+
+/* Workspace bytes of mmq_lora for E adapters of rank R and M rows; 0 if the arguments are invalid
+ * (see mmq_lora). (host) */
+size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
+
+/* The forward call.
+ *  act   (device) of M rows and K columns, as mmq_quantize_act(a, ...) writes it
+ *  A, B  (device) [E][R][K] and [E][N][R] of type d; adapters of a smaller rank are padded with
+ *        zeros
+ *  scale (device) f32 [E]
+ *  plan  (device) mmq_group_rows of the rows' adapters: E groups, T = M, top_k = 1
+ *  base  (device) [M][ldb], or NULL for zeros; may be `out` itself with ldb = ldo (mmq_gemm's
+ *        output, added to in place), and must not overlap it otherwise
+ *  out   (device) [M][ldo]: f32 with MMQ_ACT_Q8_1, bf16 with MMQ_ACT_I8_TOKEN, as mmq_gemm
+ *        writes for these activations (base has the same type). Columns past N are left
+ *        untouched.
+ *  v     (device) f32 [M][R], written whole: the backward call needs it
+ *  workspace (device) >= mmq_lora_workspace_bytes(E, M, K, R) bytes; needs no initialisation. Two
+ *        calls that overlap in time must not share one.
+ * R is a multiple of 8, at most 256; K a multiple of 32; 1 <= E <= 4096. The strides are in
+ * elements, >= N, and need no alignment. MMQ_EINVAL also where ceil(N/256) or ceil(K/256)
+ * workgroups for each of the plan's units reach 2^24. */
+mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B,
+                    const float* scale, int64_t E, int64_t R, const void* plan, int64_t M, int64_t N,
+                    int64_t K, const void* base, int64_t ldb, void* out, int64_t ldo, float* v,
+                    void* workspace, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code (host). */
 const char* mmq_status_string(mmq_status s);
 

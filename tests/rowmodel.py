@@ -35,3 +35,40 @@ def bf16(x):
     """x rounded to bf16 (nearest even), as f32."""
     u = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
     return (((u + 0x7FFF + ((u >> 16) & 1)) >> 16) << 16).astype(np.uint32).view(np.float32)
+
+
+# ------------------------------------------------------------------------------ adapters
+
+def act_values(kind, q, s):
+    """x^ [M, K] in 64 bits from int8 values q [M, K] and the scales ([M, K/32], or [M])."""
+    s = np.asarray(s, np.float64)
+    per = np.repeat(s, 32, axis=1) if kind == "q8_1" else s[:, None]
+    return q.astype(np.float64) * per
+
+
+def lora(x, A, B, scale, ids, base):
+    """(out, v) and the sums of the terms' magnitudes (out, v) behind them."""
+    M, R = x.shape[0], A.shape[1]
+    out, v = np.array(base, np.float64), np.zeros((M, R))
+    mag_out, mag_v = np.abs(out), np.zeros((M, R))
+    for e in range(A.shape[0]):
+        at = np.nonzero(ids == e)[0]
+        v[at] = x[at] @ A[e].T
+        mag_v[at] = np.abs(x[at]) @ np.abs(A[e]).T
+        out[at] += scale[e] * (v[at] @ B[e].T)
+        mag_out[at] += abs(scale[e]) * (mag_v[at] @ np.abs(B[e]).T)
+    return out, v, mag_out, mag_v
+
+
+def lora_grad(x, A, B, scale, ids, v, dy, dx_base):
+    """(dx, dA, dB) and the sums of the terms' magnitudes behind each."""
+    res = [np.array(dx_base, np.float64), np.zeros(A.shape), np.zeros(B.shape)]
+    mag = [np.abs(res[0]), np.zeros(A.shape), np.zeros(B.shape)]
+    for e in range(A.shape[0]):
+        at = np.nonzero(ids == e)[0]
+        for to, f in ((res, lambda a: a), (mag, np.abs)):
+            u = f(scale[e]) * (f(dy[at]) @ f(B[e]))
+            to[0][at] += u @ f(A[e])
+            to[1][e] = u.T @ f(x[at])
+            to[2][e] = f(scale[e]) * (f(dy[at]).T @ f(v[at]))
+    return res, mag

@@ -1,0 +1,247 @@
+"""Low-rank adapters beside a shared projection on the GPU, through the public binding, against
+64-bit sums.
+
+Tolerances. Every product of operands is exact in f32; a sum of n terms made by the matrix core
+and by fused multiply-adds, each addition cut off or rounded (off by at most 2^-23 of the running
+sum), is off by at most n * 2^-23 * sum |terms|. v is such a sum over K; out adds the R products
+of v (three or five terms each, the pairs left out below 2^-23 of the product) to that error, and
+is rounded once to its type (2^-24 or 2^-8). On inputs whose every partial sum is an integer below
+2^24 nothing rounds, and the results have to be equal."""
+import numpy as np
+import pytest
+
+import gen
+import rowmodel
+
+pytestmark = pytest.mark.gpu
+
+U23, U24, U8 = 2.0 ** -23, 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    import block_quantized_int8_amd as mmq
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mmq.lib()
+    return torch, mmq
+
+
+def row_ids(M, E, how, seed):
+    r = np.random.default_rng([seed, M, E])
+    if how == "none":
+        return np.full(M, -1, np.int32)
+    if how == "one":                              # one request
+        return np.full(M, E - 1, np.int32)
+    if how == "mixed":
+        ids = r.integers(0, E, M).astype(np.int32)
+        if M > 1:
+            ids[r.random(M) < 0.15] = r.choice([-1, E, 1 << 30, -(1 << 31)])
+        return ids
+    cuts = np.sort(r.integers(0, M, E))           # runs of requests, some empty; a run without adapter
+    ids = np.searchsorted(cuts, np.arange(M), side="right").astype(np.int32)
+    return np.where(ids == E, -1, ids).astype(np.int32)
+
+
+def adapters(torch, kind, E, R, K, N, seed):
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float16
+    A = (torch.randn((E, R, K), generator=g) * K ** -0.5).to(dt)
+    B = (torch.randn((E, N, R), generator=g) * 0.1).to(dt)
+    scale = 0.25 + torch.rand((E,), generator=g)
+    return A, B, scale
+
+
+def activations(mmq, kind, M, K, seed):
+    """An act buffer (host bytes) and the 64-bit values it stands for."""
+    x = gen.act_f32(M, K, seed=seed, cfg=140, outlier_rate=1e-2)
+    amax = np.abs(x.reshape(M, K // 32, 32)).max(2) if kind == "q8_1" else np.abs(x).max(1)
+    s = (amax / np.float32(127)).astype(np.float32)
+    per = np.repeat(s, 32, axis=1) if kind == "q8_1" else s[:, None]
+    q = np.clip(np.rint(x / per), -128, 127).astype(np.int8)
+    if kind == "q8_1":
+        s = s.astype(np.float16).astype(np.float32)
+        return mmq.act_q8_1_pack_host(q, s), rowmodel.act_values(kind, q, s)
+    return mmq.act_i8_pack_host(q, s), rowmodel.act_values(kind, q, s)
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+CASES = [
+    ("q8_1", "bf16", 1, 1, 32, 8, 1, "one"), ("i8_token", "f16", 1, 3, 32, 8, 1, "one"),
+    ("q8_1", "f16", 1, 4096, 4096, 16, 8, "one"), ("q8_1", "bf16", 2, 257, 96, 16, 3, "mixed"),
+    ("i8_token", "bf16", 5, 255, 64, 24, 2, "mixed"), ("q8_1", "f16", 16, 64, 416, 32, 5, "mixed"),
+    ("q8_1", "bf16", 17, 1003, 1024, 40, 1, "one"), ("i8_token", "f16", 63, 129, 320, 64, 4, "runs"),
+    ("q8_1", "bf16", 64, 512, 288, 64, 64, "mixed"), ("q8_1", "f16", 65, 130, 1056, 72, 2, "runs"),
+    ("i8_token", "bf16", 130, 70, 544, 128, 3, "runs"), ("q8_1", "bf16", 200, 301, 512, 256, 2, "runs"),
+    ("q8_1", "f16", 333, 99, 800, 8, 70, "mixed"), ("i8_token", "f16", 301, 777, 96, 16, 1, "one"),
+    ("q8_1", "bf16", 40, 50, 64, 16, 3, "none"), ("q8_1", "bf16", 700, 260, 128, 48, 4, "runs"),
+    ("i8_token", "bf16", 100, 33, 11008, 8, 2, "runs"), ("q8_1", "bf16", 90, 65, 64, 8, 4096, "mixed"),
+]
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E,how", CASES)
+def test_forward(env, act, kind, M, N, K, R, E, how):
+    torch, mmq = env
+    print(f"[case] lora {act} {kind} M={M} N={N} K={K} R={R} E={E} {how}", flush=True)
+    ids = row_ids(M, E, how, 1)
+    buf, x = activations(mmq, act, M, K, 2)
+    A, B, scale = adapters(torch, kind, E, R, K, N, 3)
+    io = torch.float32 if act == "q8_1" else torch.bfloat16
+    frame = torch.full((M, N + 3), -7.0, dtype=io, device="cuda")
+    frame[:, :N] = torch.randn((M, N), generator=torch.Generator().manual_seed(4)).to(io).cuda()
+    base = frame[:, :N].clone()
+    dev = [t.cuda() for t in (torch.from_numpy(buf), A, B, scale)]
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    v = torch.full((M, R), float("nan"), device="cuda")
+    out, v = mmq.lora(*dev, plan, M, atype=act, base=frame[:, :N], out=frame[:, :N], v=v)     # in place
+    want, wv, mag, mag_v = rowmodel.lora(x, host(A), host(B), host(scale), ids, host(base))
+    got, gv = host(frame), host(v)
+    assert np.all(got[:, N:] == -7.0)
+    assert np.all(np.abs(gv - wv) <= (K + 8) * U23 * mag_v * 1.01)
+    tol = (K + 8 + 5 * R + 8) * U23 * mag * 1.01
+    tol += (np.abs(want) + tol) * (U24 if act == "q8_1" else U8)
+    assert np.all(np.abs(got[:, :N] - want) <= tol)
+    none = (ids < 0) | (ids >= E)
+    assert np.all(gv[none] == 0)
+    assert torch.equal(frame[:, :N].cpu()[torch.from_numpy(none)], base.cpu()[torch.from_numpy(none)])
+    # much nearer than the bounds where the terms have both signs: as near as f32 sums are
+    if act == "q8_1" and how != "none":
+        assert np.linalg.norm(gv - wv) <= 1e-6 * np.linalg.norm(wv)
+    # out of place, twice: the same bits
+    for _ in range(2):
+        out2, v2 = mmq.lora(*dev, plan, M, atype=act, base=base)
+        assert torch.equal(out2, frame[:, :N]) and torch.equal(v2, v)
+    # no base: zeros
+    out0, _ = mmq.lora(*dev, plan, M, atype=act)
+    want0 = want - host(base)
+    tol0 = (K + 8 + 5 * R + 8) * U23 * mag * 1.01
+    tol0 += (np.abs(want0) + tol0) * (U24 if act == "q8_1" else U8)
+    assert np.all(np.abs(host(out0) - want0) <= tol0)
+    assert np.all(host(out0)[none] == 0)
+
+
+def integer_case(mmq, act, kind, M, N, K, R, E, seed):
+    """Inputs of small integers (times powers of two) whose sums need up to 24 bits."""
+    r = np.random.default_rng(seed)
+    q = r.integers(-127, 128, (M, K)).astype(np.int8)
+    if act == "q8_1":
+        s = (2.0 ** r.integers(0, 2, (M, K // 32))).astype(np.float32)
+        buf = mmq.act_q8_1_pack_host(q, s)
+    else:
+        s = (2.0 ** r.integers(0, 2, M)).astype(np.float32)
+        buf = mmq.act_i8_pack_host(q, s)
+    top = 255 if kind == "bf16" else 2047                     # 8 and 11 significand bits
+    A = r.integers(-top, top + 1, (E, R, K)) * (r.random((E, R, K)) < (24 if kind == "bf16" else 4) / max(K, 64))
+    B = r.integers(-2, 3, (E, N, R)) * (r.random((E, N, R)) < 2 / R)
+    return buf, rowmodel.act_values(act, q, s), A.astype(np.float32), B.astype(np.float32)
+
+
+@pytest.mark.parametrize("act", ["q8_1", "i8_token"])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,R,E", [(1, 70, 64, 8, 1), (33, 100, 256, 16, 3), (150, 300, 512, 64, 2), (70, 65, 96, 136, 2)])
+def test_forward_exact_on_integers(env, act, kind, M, N, K, R, E):
+    torch, mmq = env
+    print(f"[case] lora integers {act} {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    buf, x, A, B = integer_case(mmq, act, kind, M, N, K, R, E, [M, N, K])
+    ids = row_ids(M, E, "mixed", 5)
+    scale = 2.0 ** (np.arange(E) % 2) / 2
+    base = np.random.default_rng(6).integers(-64, 65, (M, N)).astype(np.float32)
+    want, wv, mag, mag_v = rowmodel.lora(x, A, B, scale, ids, base)
+    assert mag_v.max() < 2 ** 24 and (2 * mag).max() < 2 ** 25      # halves of integers below 2^24
+    if mag_v.max() > 2 ** 17:
+        assert np.any(np.abs(wv) > 2 ** 16)                         # more bits than two terms hold
+    dt, io = (torch.bfloat16 if kind == "bf16" else torch.float16), (torch.float32 if act == "q8_1" else torch.bfloat16)
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    out, v = mmq.lora(torch.from_numpy(buf).cuda(), torch.from_numpy(A).to(dt).cuda(), torch.from_numpy(B).to(dt).cuda(),
+                      torch.from_numpy(scale.astype(np.float32)).cuda(), plan, M, atype=act,
+                      base=torch.from_numpy(base).to(io).cuda())
+    assert np.array_equal(host(v), wv)
+    want = want if act == "q8_1" else rowmodel.bf16(want).astype(np.float64)
+    assert np.array_equal(host(out), want)
+
+
+def test_beside_the_projection(env):
+    """The run that it is made for: quantise, plan, the shared projection, the adapters on its
+    output in place; against the oracle's projection plus the 64-bit adapters."""
+    torch, mmq = env
+    import oracle
+    M, N, K, R, E = 150, 384, 512, 16, 5
+    raw = gen.weights("q4_0", N, K, seed=3, cfg=141)
+    xh = gen.act_f32(M, K, seed=4, cfg=141)
+    ids = row_ids(M, E, "runs", 6)
+    A, B, scale = adapters(torch, "bf16", E, R, K, N, 7)
+    packed = mmq.repack_weights("q4_0", torch.from_numpy(raw).cuda(), N, K)
+    act = mmq.quantize_act(torch.from_numpy(xh).cuda())
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    out = mmq.gemm("q4_0", packed, act, M, N, K)
+    mmq.lora(act, A.cuda(), B.cuda(), scale.cuda(), plan, M, base=out, out=out)
+    oracle.build()
+    rq, rs, _ = oracle.quantize_q8_1(xh)
+    ref = oracle.gemm_f64("q4_0", raw, N, K, rq, rs)
+    want = rowmodel.lora(rowmodel.act_values("q8_1", rq, rs), host(A), host(B), host(scale), ids, ref)[0]
+    assert np.max(np.abs(host(out) - want)) <= 1e-3 * np.max(np.abs(want))
+
+
+def test_graph_and_streams(env):
+    """Captured once, replayed with other activations, adapters' rows and bases; every replay equals
+    the eager call on another stream, and two plans' calls interleaved on two streams do too."""
+    torch, mmq = env
+    M, N, K, R, E = 77, 300, 256, 32, 6
+    A, B, scale = (t.cuda() for t in adapters(torch, "f16", E, R, K, N, 8))
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    base = torch.zeros((M, N), device="cuda")
+    act = torch.zeros(mmq.act_bytes("q8_1", M, K), dtype=torch.uint8, device="cuda")
+    got = {}
+
+    def path(stream=None):
+        return mmq.lora(act, A, B, scale, mmq.group_rows(ids, E, stream=stream), M, base=base, stream=stream)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        path()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got["out"] = path()
+    for rep in range(4):
+        act.copy_(torch.from_numpy(activations(mmq, "q8_1", M, K, 30 + rep)[0]))
+        ids.copy_(torch.from_numpy(row_ids(M, E, ["mixed", "runs", "one", "none"][rep], rep)))
+        base.normal_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        pairs = [path(s) for s in (s1, s2, s1, s2)]
+        torch.cuda.synchronize()
+        for out, v in pairs:
+            assert torch.equal(out, got["out"][0]) and torch.equal(v, got["out"][1]), rep
+
+
+def test_binding_refusals(env):
+    torch, mmq = env
+    M, N, K, R, E = 4, 64, 64, 8, 2
+    A, B, scale = (t.cuda() for t in adapters(torch, "bf16", E, R, K, N, 1))
+    act = torch.zeros(mmq.act_bytes("q8_1", M, K), dtype=torch.uint8, device="cuda")
+    plan = mmq.group_rows(torch.zeros(M, dtype=torch.int32, device="cuda"), E)
+    for bad, match in (((act[:-256], A, B, scale, plan, M), "act"), ((act, A.float(), B, scale, plan, M), "adapters"),
+                       ((act, A, B.half(), scale, plan, M), "B must"), ((act, A, B[:1], scale, plan, M), "B must"),
+                       ((act, A, B, scale[:1], plan, M), "scale"), ((act, A, B, scale.double(), plan, M), "scale"),
+                       ((act, A, B, scale, plan, 400), "plan"), ((act.cpu(), A, B, scale, plan, M), "GPU"),
+                       ((act, A.transpose(1, 2), B, scale, plan, M), "must")):
+        with pytest.raises(ValueError, match=match):
+            mmq.lora(*bad)
+    with pytest.raises(ValueError, match="base"):
+        mmq.lora(act, A, B, scale, plan, M, base=torch.zeros((M, N), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="out"):
+        mmq.lora(act, A, B, scale, plan, M, out=torch.zeros((M, N + 1), device="cuda"))
+    with pytest.raises(mmq.MMQError) as err:
+        mmq.lora(act, A, B, scale, plan, M, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert err.value.code == mmq.MMQ_EWORKSPACE
+    with pytest.raises(mmq.MMQError) as err:                       # a rank that is no multiple of 8
+        mmq.lora(act, A[:, :7].contiguous(), B[:, :, :7].contiguous(), scale, plan, M)
+    assert err.value.code == mmq.MMQ_EINVAL
