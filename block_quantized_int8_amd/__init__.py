@@ -9,7 +9,7 @@ The functions mirror include/mmq.h one to one (same names without the `mmq_` pre
     act_bytes, act_region_offsets, quantize_act, packed_bytes, repack_weights, gemm,
     gemm_id_workspace_bytes, gemm_id, gemm_id_noalloc, gemm_id_noalloc_max_workspace_bytes,
     group_bytes, group_region_offsets, group_rows, moe_gather, moe_combine, moe_combine_grad,
-    lora_workspace_bytes, lora, status_string
+    lora_workspace_bytes, lora, lora_grad_workspace_bytes, lora_grad, status_string
 
 plus `group_views` (the regions of a plan as tensors) and host-side encoders/decoders of the
 documented act layouts (`act_to_host`, `act_q8_1_pack_host` and friends for q8_1,
@@ -91,6 +91,10 @@ def lib() -> ctypes.CDLL:
     L.mmq_lora_workspace_bytes.restype = S
     L.mmq_lora.argtypes = [e, P, e, P, P, P, I, I, P, I, I, I, P, I, P, I, P, P, S, P]
     L.mmq_lora.restype = e
+    L.mmq_lora_grad_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.mmq_lora_grad_workspace_bytes.restype = S
+    L.mmq_lora_grad.argtypes = [e, P, e, P, P, P, I, I, P, I, I, I, P, P, I, P, I, P, I, P, P, P, S, P]
+    L.mmq_lora_grad.restype = e
     _lib = L
     return L
 
@@ -481,6 +485,50 @@ def lora(act, A, B, scale, plan, M: int, atype="q8_1", base=None, out=None, v=No
                                       plan.data_ptr(), M, N, K, _ptr(base), ldb, out.data_ptr(), ldo, v.data_ptr(),
                                       workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, at)))
     return out, v
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_grad_workspace_bytes(E: int, M: int, N: int, K: int, R: int) -> int:
+    return int(lib().mmq_lora_grad_workspace_bytes(E, M, N, K, R))
+
+
+def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None, dA=None, dB=None,
+              want_dx: bool = True, workspace=None, stream=None):
+    """Gradients of lora from its 8-bit activations: dy [M, N] float32 (q8_1) or bfloat16
+    (i8_token), v as lora returned it, the other inputs as given to it. Returns (dx, dA, dB) in
+    float32: dx [M, K] = dx_base + the adapters' part (dx=dx_base adds in place; None with
+    want_dx=False), dA and dB like A and B."""
+    import torch
+    fn = "lora_grad"
+    at = _gpu(fn, act, A, B, scale, plan, v, dy, dx_base, dx, dA, dB, workspace)
+    at_ = _at(atype)
+    if dy.dim() != 2:
+        raise ValueError(f"{fn}: dy must be [M, N], got {tuple(dy.shape)}")
+    M = dy.shape[0]
+    d, E, R, K, N = _adapters(fn, act, A, B, scale, plan, M, at_)
+    f32 = torch.float32
+    lddy = _ld(fn, "dy", dy, M, N, f32 if at_ == 0 else torch.bfloat16)
+    _flat(fn, "v", v, (M, R), f32)
+    if want_dx and dx is None:
+        dx = _new((M, K), f32, at, stream)
+    if dA is None:
+        dA = _new((E, R, K), f32, at, stream)
+    else:
+        _flat(fn, "dA", dA, (E, R, K), f32)
+    if dB is None:
+        dB = _new((E, N, R), f32, at, stream)
+    else:
+        _flat(fn, "dB", dB, (E, N, R), f32)
+    lddx = _ld(fn, "dx", dx, M, K, f32) if dx is not None else 0
+    ldxb = _ld(fn, "dx_base", dx_base, M, K, f32) if dx_base is not None else 0
+    if workspace is None:
+        workspace = _new(lora_grad_workspace_bytes(E, M, N, K, R), torch.uint8, at, stream)
+    _check("mmq_lora_grad",
+           lib().mmq_lora_grad(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
+                               plan.data_ptr(), M, N, K, v.data_ptr(), dy.data_ptr(), lddy, _ptr(dx_base), ldxb,
+                               _ptr(dx), lddx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, at)))
+    return dx, dA, dB
 
 
 # -------------------------------------------------------------------------- host helpers

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmmq.so")
 SOURCES = ["api.cpp", "quantize.hip", "repack.hip", "gemm_block.hip", "gemm_w8a8.hip", "gemm_id.hip",
-           "gemm_mmvq.hip", "rows.hip", "lora.hip"]
+           "gemm_mmvq.hip", "rows.hip", "lora.hip", "lora_grad.hip"]
 ARCH = os.environ.get("MMQ_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -288,4 +288,34 @@ mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, c
                                 v, workspace, as_stream(stream)));
 }
 
+namespace {
+bool lora_grad_sizes_ok(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    return lora_sizes_ok(E, M, N, K, R) && E * ceil_div(N, 64) < (int64_t(1) << 24) &&
+           E * ceil_div(K, 64) < (int64_t(1) << 24);
+}
+}  // namespace
+
+size_t mmq_lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    return lora_grad_sizes_ok(E, M, N, K, R) ? lora_grad_workspace_bytes(E, M, N, R) : 0;
+}
+
+mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B, const float* scale,
+                         int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const float* v,
+                         const void* dy, int64_t lddy, const float* dx_base, int64_t ldxb, float* dx, int64_t lddx,
+                         float* dA, float* dB, void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_atype(a) || (d != MMQ_ADAPTER_BF16 && d != MMQ_ADAPTER_F16)) return MMQ_EINVAL;
+    if (!lora_grad_sizes_ok(E, M, N, K, R) || lddy < N) return MMQ_EINVAL;
+    if (!act || !A || !B || !scale || !plan || !v || !dy || !dA || !dB) return MMQ_EINVAL;
+    if (dx && (lddx < K || (dx_base && ldxb < K))) return MMQ_EINVAL;
+    if (dx && dx_base == dx && ldxb != lddx) return MMQ_EINVAL;
+    if (!aligned16(act) || !aligned16(A) || !aligned16(B) || !aligned16(scale) || !aligned16(plan) || !aligned16(v) ||
+        !aligned16(dy) || (dx_base && !aligned16(dx_base)) || (dx && !aligned16(dx)) || !aligned16(dA) ||
+        !aligned16(dB))
+        return MMQ_EALIGN;
+    if (!workspace || ws_bytes < lora_grad_workspace_bytes(E, M, N, R)) return MMQ_EWORKSPACE;
+    if (!aligned16(workspace)) return MMQ_EALIGN;
+    return from_hip(launch_lora_grad(a, d == MMQ_ADAPTER_F16, act, A, B, scale, E, R, plan, M, N, K, v, dy, lddy,
+                                     dx_base, ldxb, dx, lddx, dA, dB, workspace, as_stream(stream)));
+}
+
 }  // extern "C"

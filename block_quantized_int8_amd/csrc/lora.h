@@ -100,6 +100,56 @@ template <bool F16> __device__ inline u32x4 int8_operand(u32x2 q) {
     return r;
 }
 
+// Four values of a row of the output's type from column n on, as f32 (columns past N read 0).
+template <bool BF16> __device__ inline f32x4 load4(const void* p, int64_t at, int left) {
+    f32x4 r = 0;
+    if constexpr (BF16) {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+        if (left >= 4) {
+            const u32x2 w = *reinterpret_cast<const u32x2_any*>(q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = as_f(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < left) r[j] = as_f((uint32_t)q[j] << 16);
+        }
+    } else {
+        const float* q = static_cast<const float*>(p) + at;
+        if (left >= 4) r = *reinterpret_cast<const f32x4_any*>(q);
+        else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < left) r[j] = q[j];
+        }
+    }
+    return r;
+}
+
+template <bool BF16> __device__ inline void store4(void* p, int64_t at, f32x4 v, int left) {
+    if constexpr (BF16) {
+        uint16_t* q = static_cast<uint16_t*>(p) + at;
+        if (left >= 4) {
+            u32x2 w;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) w[j] = (uint32_t)bf16_rne(v[2 * j]) | ((uint32_t)bf16_rne(v[2 * j + 1]) << 16);
+            *reinterpret_cast<u32x2_any*>(q) = w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < left) q[j] = bf16_rne(v[j]);
+        }
+    } else {
+        float* q = static_cast<float*>(p) + at;
+        if (left >= 4) *reinterpret_cast<f32x4_any*>(q) = v;
+        else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < left) q[j] = v[j];
+        }
+    }
+}
+
 struct LoraArgs {
     const int8_t* xq;           // act region 0
     const uint32_t* xs2;        // q8_1 region 1 (xs as an f16 pair)
@@ -118,14 +168,53 @@ struct LoraArgs {
     void* out;
     int64_t ldo;
     float* v;                   // [M][R]
+    // backward
+    const int32_t* offs;
+    const void* dy;
+    int64_t lddy;
+    const float* dxb;
+    int64_t lddxb;
+    float* dx;
+    int64_t lddx;
+    float *dA, *dB, *u;         // u: [M][R] by sorted position
 };
 
-// the f32 scale of row m, block b
-__device__ inline float block_scale(const uint32_t* xs2, int KBp, int m, int b) {
-    const uint32_t w = xs2[((int64_t)(m >> 5) * KBp + b) * 32 + (m & 31)];
-    return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+// The arguments both calls share.
+inline LoraArgs lora_args(mmq_atype t, const void* act, const void* A, const void* B, const float* scale, int64_t E,
+                          int64_t R, const void* plan, int64_t M, int64_t N, int64_t K) {
+    const PlanLayout L = plan_layout(E, M);
+    const uint8_t* p = static_cast<const uint8_t*>(plan);
+    const uint8_t* x = static_cast<const uint8_t*>(act);
+    LoraArgs a = {};
+    if (t == MMQ_ACT_Q8_1) {
+        const ActQ81Layout l = act_q8_1_layout(M, K);
+        a.xq = reinterpret_cast<const int8_t*>(x + l.xq_off);
+        a.xs2 = reinterpret_cast<const uint32_t*>(x + l.xs2_off);
+        a.KBp = (int)l.KBp;
+    } else {
+        const ActI8Layout l = act_i8_layout(M, K);
+        a.xq = reinterpret_cast<const int8_t*>(x + l.a_off);
+        a.sa = reinterpret_cast<const float*>(x + l.sa_off);
+        a.KBp = (int)l.KBp;
+    }
+    a.KB = (int)(K / QK);
+    a.A = static_cast<const uint16_t*>(A);
+    a.B = static_cast<const uint16_t*>(B);
+    a.scale = scale;
+    a.offs = reinterpret_cast<const int32_t*>(p + L.offs_off);
+    a.order = reinterpret_cast<const int32_t*>(p + L.order_off);
+    a.units = reinterpret_cast<const int4*>(p + L.units_off);
+    a.E = (int)E;
+    a.R = (int)R;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.nunits = (int)L.nunits;
+    return a;
 }
 
+constexpr int LT = 256;             // threads of a workgroup
+constexpr int UP_COLS = 256;        // columns of an up workgroup: 64 per wave
 constexpr int LORA_RC = 64;        // ranks of a pass
 constexpr int64_t LORA_MAX_R = 256;
 
@@ -134,5 +223,10 @@ bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
                        int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const void* base,
                        int64_t ldb, void* out, int64_t ldo, float* v, void* ws, hipStream_t s);
+size_t lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t R);
+hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
+                            int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const float* v,
+                            const void* dy, int64_t lddy, const float* dxb, int64_t lddxb, float* dx, int64_t lddx,
+                            float* dA, float* dB, void* ws, hipStream_t s);
 
 }  // namespace mmq

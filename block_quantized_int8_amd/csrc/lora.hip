@@ -16,9 +16,6 @@
 namespace mmq {
 namespace {
 
-constexpr int LT = 256;             // threads of a workgroup
-constexpr int UP_COLS = 256;        // columns of an up workgroup: 64 per wave
-
 template <int RT, bool F16, bool Q81>
 __global__ __launch_bounds__(LT) void lora_down_kernel(LoraArgs a) {
     __shared__ f32x4 red[4][4 * RT][64];
@@ -101,56 +98,6 @@ __global__ __launch_bounds__(LT) void lora_down_kernel(LoraArgs a) {
         if (at >= unit.z || r >= a.R) continue;
         if constexpr (!Q81) d *= a.sa[a.order[unit.y + at]];
         *reinterpret_cast<f32x4*>(a.part + ((int64_t)s * a.M + unit.y + at) * a.R + r) = d;
-    }
-}
-
-// Four values of a row of the output's type from column n on, as f32 (columns past N read 0).
-template <bool BF16> __device__ inline f32x4 load4(const void* p, int64_t at, int left) {
-    f32x4 r = 0;
-    if constexpr (BF16) {
-        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-        if (left >= 4) {
-            const u32x2 w = *reinterpret_cast<const u32x2_any*>(q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = as_f(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) r[j] = as_f((uint32_t)q[j] << 16);
-        }
-    } else {
-        const float* q = static_cast<const float*>(p) + at;
-        if (left >= 4) r = *reinterpret_cast<const f32x4_any*>(q);
-        else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) r[j] = q[j];
-        }
-    }
-    return r;
-}
-
-template <bool BF16> __device__ inline void store4(void* p, int64_t at, f32x4 v, int left) {
-    if constexpr (BF16) {
-        uint16_t* q = static_cast<uint16_t*>(p) + at;
-        if (left >= 4) {
-            u32x2 w;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) w[j] = (uint32_t)bf16_rne(v[2 * j]) | ((uint32_t)bf16_rne(v[2 * j + 1]) << 16);
-            *reinterpret_cast<u32x2_any*>(q) = w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) q[j] = bf16_rne(v[j]);
-        }
-    } else {
-        float* q = static_cast<float*>(p) + at;
-        if (left >= 4) *reinterpret_cast<f32x4_any*>(q) = v;
-        else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) q[j] = v[j];
-        }
     }
 }
 
@@ -276,33 +223,7 @@ bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K) {
 hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
                        int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const void* base,
                        int64_t ldb, void* out, int64_t ldo, float* v, void* ws, hipStream_t s) {
-    const PlanLayout L = plan_layout(E, M);
-    const uint8_t* p = static_cast<const uint8_t*>(plan);
-    const uint8_t* x = static_cast<const uint8_t*>(act);
-    LoraArgs a = {};
-    if (t == MMQ_ACT_Q8_1) {
-        const ActQ81Layout l = act_q8_1_layout(M, K);
-        a.xq = reinterpret_cast<const int8_t*>(x + l.xq_off);
-        a.xs2 = reinterpret_cast<const uint32_t*>(x + l.xs2_off);
-        a.KBp = (int)l.KBp;
-    } else {
-        const ActI8Layout l = act_i8_layout(M, K);
-        a.xq = reinterpret_cast<const int8_t*>(x + l.a_off);
-        a.sa = reinterpret_cast<const float*>(x + l.sa_off);
-        a.KBp = (int)l.KBp;
-    }
-    a.KB = (int)(K / QK);
-    a.A = static_cast<const uint16_t*>(A);
-    a.B = static_cast<const uint16_t*>(B);
-    a.scale = scale;
-    a.order = reinterpret_cast<const int32_t*>(p + L.order_off);
-    a.units = reinterpret_cast<const int4*>(p + L.units_off);
-    a.E = (int)E;
-    a.R = (int)R;
-    a.M = (int)M;
-    a.N = (int)N;
-    a.K = (int)K;
-    a.nunits = (int)L.nunits;
+    LoraArgs a = lora_args(t, act, A, B, scale, E, R, plan, M, N, K);
     a.part = static_cast<float*>(ws);
     a.S = (int)down_parts(E, M, K);
     a.base = base;
@@ -316,7 +237,7 @@ hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, co
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int ntiles = (int)ceil_div(N, UP_COLS);
-    const dim3 grid((unsigned)(L.nunits * ntiles));
+    const dim3 grid((unsigned)a.nunits * (unsigned)ntiles);
     if (f16) {
         if (q81) hipLaunchKernelGGL((lora_up_kernel<true, false>), grid, dim3(LT), 0, s, a, ntiles);
         else hipLaunchKernelGGL((lora_up_kernel<true, true>), grid, dim3(LT), 0, s, a, ntiles);

@@ -357,6 +357,35 @@ mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, c
                     int64_t K, const void* base, int64_t ldb, void* out, int64_t ldo, float* v,
                     void* workspace, size_t ws_bytes, void* stream);
 
+/* Workspace bytes of mmq_lora_grad; 0 if the arguments are invalid. (host) */
+size_t mmq_lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R);
+
+/* The backward call, from the 8-bit activations of the forward call (the act buffer is the
+ * checkpoint; nothing else of the activations is kept but v):
+ *
+ *     u[m][r]     = scale[e] * sum_n dy[m][n] * B[e][n][r]
+ *     dB[e][n][r] = scale[e] * sum over the rows m of adapter e of dy[m][n] * v[m][r]
+ *     dA[e][r][k] = sum over the rows m of adapter e of u[m][r] * x^[m][k]
+ *     dx[m][k]    = dx_base[m][k] + sum_r u[m][r] * A[e][r][k]
+ *
+ * dx is the gradient for the activations before quantisation (which counts as the identity).
+ * The gradient for `base` is dy itself.
+ *  act, d, A, B, scale, plan: as given to mmq_lora; v as it returned it
+ *  dy      (device) [M][lddy], f32 with MMQ_ACT_Q8_1, bf16 with MMQ_ACT_I8_TOKEN
+ *  dx_base (device) f32 [M][ldxb] (the projection's own input gradient), or NULL for zeros; may be
+ *          `dx` itself with ldxb = lddx, and must not overlap it otherwise
+ *  dx      (device) f32 [M][lddx], or NULL if it is not wanted. A row without an adapter gets
+ *          dx_base
+ *  dA, dB  (device) f32 [E][R][K] and [E][N][R], written whole (zeros for an adapter without rows)
+ *  workspace (device) >= mmq_lora_grad_workspace_bytes(E, M, N, K, R) bytes, as for mmq_lora
+ * Sizes, strides and errors as for mmq_lora; MMQ_EINVAL also where E * ceil(N/64) or
+ * E * ceil(K/64) reaches 2^24. f32 sums of exact products in a fixed order, as in mmq_lora. */
+mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B,
+                         const float* scale, int64_t E, int64_t R, const void* plan, int64_t M, int64_t N,
+                         int64_t K, const float* v, const void* dy, int64_t lddy, const float* dx_base,
+                         int64_t ldxb, float* dx, int64_t lddx, float* dA, float* dB, void* workspace,
+                         size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code (host). */
 const char* mmq_status_string(mmq_status s);
 
