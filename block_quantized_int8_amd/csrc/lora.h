@@ -52,6 +52,19 @@ __device__ inline void split3(const float* x, u32x4* t) {
     }
 }
 
+// four f32 values to three planes of bf16 terms, `plane` values apart
+__device__ inline void store_terms(uint16_t* at, int64_t plane, f32x4 d) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        u32x2 w;
+        w[0] = pack_hi(d[0], d[1]);
+        w[1] = pack_hi(d[2], d[3]);
+        *reinterpret_cast<u32x2*>(at + k * plane) = w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] -= cut(d[j]);
+    }
+}
+
 // eight f16 values (raw bits) as two bf16 operands
 __device__ inline void split_f16(u32x4 h, u32x4* t) {
     const f16x8 v = __builtin_bit_cast(f16x8, h);
@@ -61,6 +74,31 @@ __device__ inline void split_f16(u32x4 h, u32x4* t) {
         t[0][i] = pack_hi(a, b);
         t[1][i] = pack_hi(a - cut(a), b - cut(b));
     }
+}
+
+// Rows of 16-byte pieces are loaded with four consecutive lanes on a row's 64 bytes (lane 4c + g:
+// row c, piece g), one cache access for each four lanes; an operand wants lane 16g + c there. In
+// the operand's own order every lane is an access of its own (49 of them for a load of 64 lanes),
+// and the adapters' loads then bound the forward kernels: 17.5 us against 11.7 for the down
+// kernel at 2048 x 4096, rank 64. The pieces turn in a wave's own 1 KB of LDS.
+__device__ inline int piece_row(int lane) { return lane >> 2; }
+__device__ inline int piece_of(int lane) { return lane & 3; }
+__device__ inline int piece_at(int lane) { return 4 * (lane & 15) + (lane >> 4); }   // the operand's piece
+// An operand from a row-major LDS tile with the operand's k along the rows (k = 8g .. 8g+7, 16
+// columns from `tile` on): lane i of 16 gives the address of four values of row i / 4 and gets
+// column i of the four rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ inline u32x4 turned_operand(const uint16_t* tile, int ld, int lane) {
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const uint16_t* p = tile + (8 * (lane >> 4) + (lane & 15) / 4) * ld + 4 * (lane & 3);
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * ld)));
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+// LDS written by a wave's lanes is read by its other lanes (no other wave is concerned)
+__device__ inline void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // An adapter's operand: one bf16 term, or an f16 value's two.
@@ -85,6 +123,20 @@ __device__ inline f32x4 mfma_terms(const Weights<F16>& w, const u32x4* x, f32x4 
     }
     acc = mfma_bf16(w.t[0], x[1], acc);
     return mfma_bf16(w.t[0], x[0], acc);
+}
+
+// the same with the f32 values as A: their rows are the accumulator's
+template <bool F16>
+__device__ inline f32x4 terms_mfma(const u32x4* x, const Weights<F16>& w, f32x4 acc) {
+    if constexpr (F16) {
+        acc = mfma_bf16(x[1], w.t[1], acc);
+        acc = mfma_bf16(x[2], w.t[0], acc);
+        acc = mfma_bf16(x[0], w.t[1], acc);
+    } else {
+        acc = mfma_bf16(x[2], w.t[0], acc);
+    }
+    acc = mfma_bf16(x[1], w.t[0], acc);
+    return mfma_bf16(x[0], w.t[0], acc);
 }
 
 // eight int8 values as a bf16 or f16 operand (exact: 8 bits)
@@ -132,7 +184,7 @@ template <bool BF16> __device__ inline void store4(void* p, int64_t at, f32x4 v,
         if (left >= 4) {
             u32x2 w;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) w[j] = (uint32_t)bf16_rne(v[2 * j]) | ((uint32_t)bf16_rne(v[2 * j + 1]) << 16);
+            for (int j = 0; j < 2; ++j) w[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
             *reinterpret_cast<u32x2_any*>(q) = w;
         } else {
 #pragma unroll
@@ -162,6 +214,7 @@ struct LoraArgs {
     int E, R, M, N, K, nunits;
     float* part;                // partial sums [S][M][R] by sorted position
     int S;
+    uint16_t* planes;           // three bf16 terms of s_e v or u: [3][R/8][M][8] by sorted position
     // forward
     const void* base;
     int64_t ldb;
@@ -178,6 +231,12 @@ struct LoraArgs {
     int64_t lddx;
     float *dA, *dB, *u;         // u: [M][R] by sorted position
 };
+
+// The planes' values of ranks r .. of a position: eight ranks of consecutive positions lie side by
+// side, so that a matrix-core operand of 16 positions is loaded in whole cache lines.
+__device__ inline uint16_t* plane_at(const LoraArgs& a, int pos, int r) {
+    return a.planes + (((int64_t)(r >> 3) * a.M + pos) * 8 + (r & 7));
+}
 
 // The arguments both calls share.
 inline LoraArgs lora_args(mmq_atype t, const void* act, const void* A, const void* B, const float* scale, int64_t E,
@@ -217,6 +276,126 @@ constexpr int LT = 256;             // threads of a workgroup
 constexpr int UP_COLS = 256;        // columns of an up workgroup: 64 per wave
 constexpr int LORA_RC = 64;        // ranks of a pass
 constexpr int64_t LORA_MAX_R = 256;
+
+// out = base + the rows' planes (s_e v, or u) times a weight matrix, for 16 rows x 64 columns a wave:
+// waves 0-3 of a workgroup of W waves have the row tiles of a unit, each further four the next 64
+// columns. The weights of up to 64 ranks go through LDS as bf16 terms, once for the four row
+// tiles: rows of ranks for each column (B_e, TR false) or of columns for each rank (A_e, TR true).
+// Operand mapping: A = the rows' planes, B = the columns; a lane ends with four rows, of four
+// consecutive columns (TR false: column 4c + i of tile i) or of one (TR true: column 16i + c).
+template <bool TR, bool F16, int W> struct ExpandLds {
+    static constexpr int T = Weights<F16>::T, COLS = 16 * W;       // columns of the workgroup
+    static constexpr int ROWS = TR ? LORA_RC : COLS, LD = (TR ? COLS : LORA_RC) + 8;
+    uint16_t w[T][ROWS][LD];
+};
+
+template <bool TR, bool F16, bool BF16, bool TAIL, int W>
+__device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, int C, const void* base_, int64_t ldb,
+                                   void* out, int64_t ldo, int4 unit, int tile, ExpandLds<TR, F16, W>& lds) {
+    using L = ExpandLds<TR, F16, W>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4, t = wave & 3;
+    const int c0 = tile * L::COLS, n0 = c0 + 64 * (wave >> 2), n = n0 + (TR ? c : 4 * c);
+    const bool none = unit.x >= a.E, live = 16 * t < unit.z && n0 < C;
+    const uint16_t* w0 = weights + (none ? 0 : (int64_t)unit.x * C * a.R);
+
+    int m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = a.order[unit.y + min(16 * t + 4 * g + j, unit.z - 1)];
+    f32x4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = 0;
+    f32x4 base[4];
+#pragma unroll 1
+    for (int r0 = 0; r0 < a.R; r0 += LORA_RC) {
+        const int rc = min(a.R - r0, LORA_RC);
+        // pieces of eight values: eight of 64 ranks for each column, or COLS / 8 for each rank
+        constexpr int PER = TR ? L::COLS / 8 : LORA_RC / 8, PIECES = L::ROWS * PER / (64 * W);
+        u32x4 raw[PIECES];
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int idx = i * 64 * W + (int)threadIdx.x, row = idx / PER, p = 8 * (idx % PER);
+            raw[i] = 0;                                    // zeros past R and past the columns
+            if constexpr (TR) {
+                if (row < rc && c0 + p < C && !none) raw[i] = *reinterpret_cast<const u32x4*>(w0 + (int64_t)(r0 + row) * C + c0 + p);
+            } else {
+                if (p < rc && c0 + row < C && !none) raw[i] = *reinterpret_cast<const u32x4*>(w0 + (int64_t)(c0 + row) * a.R + r0 + p);
+            }
+        }
+        // the row tile's planes: row c, ranks 8g .. of both steps; zeros past the unit and past R
+        u32x4 x[2][3];
+        const int at = 16 * t + c;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 32 * k + 8 * g;
+            const bool ok = live && !none && at < unit.z && r < a.R;
+            const uint16_t* p = plane_at(a, unit.y + at, r);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                x[k][j] = 0;
+                if (ok) x[k][j] = *reinterpret_cast<const u32x4*>(p + (int64_t)j * a.M * a.R);
+            }
+        }
+        if (r0 == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                base[j] = 0;
+                if (!base_ || !live) continue;
+                if constexpr (TR) {
+                    const float* p = static_cast<const float*>(base_) + m[j] * ldb + n;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n0 + 16 * i < C) base[j][i] = p[16 * i];
+                } else {
+                    if (n < C) base[j] = load4<BF16>(base_, m[j] * ldb + n, TAIL ? C - n : 4);
+                }
+            }
+        } else {
+            __syncthreads();
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // every load is issued before the first wait
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int idx = i * 64 * W + (int)threadIdx.x, row = idx / PER, p = 8 * (idx % PER);
+            Weights<F16> w;
+            w.set(raw[i]);
+            const int to = TR ? row : (row & ~63) + 16 * (row & 3) + ((row & 63) >> 2);
+#pragma unroll
+            for (int j = 0; j < L::T; ++j) *reinterpret_cast<u32x4*>(&lds.w[j][to][p]) = w.t[j];
+        }
+        __syncthreads();
+        if (!live || none) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (32 * k >= rc) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Weights<F16> w;
+#pragma unroll
+                for (int j = 0; j < L::T; ++j)
+                    w.t[j] = TR ? turned_operand(&lds.w[j][32 * k][n0 - c0 + 16 * i], L::LD, lane)
+                                : *reinterpret_cast<const u32x4*>(&lds.w[j][n0 - c0 + 16 * i + c][32 * k + 8 * g]);
+                acc[i] = terms_mfma<F16>(x[k], w, acc[i]);
+            }
+        }
+    }
+    if (!live) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (16 * t + 4 * g + j >= unit.z) continue;
+        if constexpr (TR) {
+            float* p = static_cast<float*>(out) + m[j] * ldo + n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n0 + 16 * i < C) p[16 * i] = base[j][i] + acc[i][j];
+        } else if (n < C) {
+            f32x4 o = base[j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] += acc[i][j];
+            store4<BF16>(out, m[j] * ldo + n, o, TAIL ? C - n : 4);
+        }
+    }
+}
 
 size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
 bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K);

@@ -3,12 +3,15 @@
 // on the act buffer that the projection reads and the output that it wrote.
 //
 // Two launches over the plan's units (up to 64 rows of one adapter):
-//   1. lora_down_kernel: v, split over K into S parts so that few rows still fill the chip; a
-//      workgroup's four waves take every fourth block of its part and join in LDS. The int8
-//      values enter the matrix core as they are (exact in bf16 and f16), each block's product
-//      is scaled by its f32 scale; the per-token form accumulates on the matrix core.
-//   2. lora_up_kernel: (unit, 256 columns): sums the S parts of v in order, and adds
-//      s_e B_e v to the base.
+//   1. lora_down_kernel: v. A workgroup has 16 of a unit's rows and one of S parts of K; its
+//      eight waves take consecutive blocks of the part and join in LDS. The int8 values enter
+//      the matrix core as they are (exact in bf16 and f16), each block's product is scaled by
+//      its f32 scale; the per-token form accumulates on the matrix core.
+//   2. s_e B_e v added to the base: lora_expand_kernel where K is not split (rows enough to fill the
+//      chip), from the terms of s_e v that the first launch leaves; lora_up_kernel otherwise, which
+//      sums the S parts in order and makes the terms itself.
+// Loops over rows stay loops: a launch fetches its code cold, and with the four row tiles
+// unrolled (25 KB of code) the second launch took 13.8 us on 517 x 1536 instead of 5.4.
 #include <algorithm>
 
 #include "lora.h"
@@ -16,208 +19,305 @@
 namespace mmq {
 namespace {
 
+constexpr int DW = 8;               // waves of a down workgroup
+constexpr int MAX_PARTS = 8;
+
+// Operand mapping: A = the adapter's rows r (lane c: rank r0 + 16i + c of tile i), B = the
+// activations (lane c: row c of the 16), so a lane ends with four consecutive ranks of a row.
+// NB blocks are loaded before the first is used.
 template <int RT, bool F16, bool Q81>
-__global__ __launch_bounds__(LT) void lora_down_kernel(LoraArgs a) {
-    __shared__ f32x4 red[4][4 * RT][64];
+__global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
+    constexpr int NB = RT == 1 ? 4 : 2;
+    __shared__ u32x4 lds[DW][NB * RT][64];      // each wave's pieces; the waves' sums at the end
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int u = (int)blockIdx.x / a.S, s = (int)blockIdx.x % a.S;
-    const int4 unit = a.units[u];
-    if (unit.z == 0 || unit.x >= a.E) return;
-    const int r0 = (int)blockIdx.y * LORA_RC;
-    const int nt = (unit.z + 15) >> 4;
+    // a unit's first 16 rows come first in the grid (units of few rows have no others); the part
+    // turns with the unit, so that no XCD's L2 gets the same columns of every row of the adapters
+    // (those are a few of its channels only: 14 us against 6.5 for 64 rows of 32 adapters)
+    const int at = (int)blockIdx.x / a.S, s = ((int)blockIdx.x + at) % a.S;
+    const int sub = at / a.nunits;
+    const int4 unit = a.units[at - sub * a.nunits];
+    const int rows = min(unit.z - 16 * sub, 16);
+    if (rows <= 0 || unit.x >= a.E) return;
+    const int p0 = unit.y + 16 * sub, r0 = (int)blockIdx.y * LORA_RC;
 
-    const int8_t* xrow[4];
-    const uint32_t* srow[4];
-    int row[4];
+    const int parts = a.S * DW, per = (a.KB + parts - 1) / parts;      // blocks of a wave
+    const int b0 = (s * DW + wave) * per, b1 = min(b0 + per, a.KB);
+    // rows past the unit's last repeat it; their columns are not stored. Ranks past R likewise.
+    const int m = a.order[p0 + min(c, rows - 1)];
+    const uint16_t* A = a.A + (int64_t)unit.x * a.R * a.K;
+    uint32_t aoff[RT];                          // R * K < 2^31 values
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        // rows past the unit's last repeat it; their columns are not stored
-        const int m = a.order[unit.y + min(16 * t + c, unit.z - 1)];
-        row[t] = m;
-        xrow[t] = a.xq + (int64_t)(m >> 5) * a.KBp * 1024 + ((g >> 1) * 32 + (m & 31)) * 16 + (g & 1) * 8;
-        if constexpr (Q81) srow[t] = a.xs2 + (int64_t)(m >> 5) * a.KBp * 32 + (m & 31);
-    }
-    const uint16_t* arow[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)        // ranks past R repeat the last one; not stored either
-        arow[i] = a.A + ((int64_t)unit.x * a.R + min(r0 + 16 * i + c, a.R - 1)) * a.K + 8 * g;
+    for (int i = 0; i < RT; ++i)
+        aoff[i] = (uint32_t)min(r0 + 16 * i + piece_row(lane), a.R - 1) * (uint32_t)a.K + 8u * piece_of(lane);
+    const int64_t tile = (int64_t)(m >> 5) * a.KBp;
+    const int8_t* xrow = a.xq + tile * 1024 + ((g >> 1) * 32 + (m & 31)) * 16 + (g & 1) * 8;
+    const uint16_t* srow = reinterpret_cast<const uint16_t*>(a.xs2 + tile * 32 + (m & 31));
 
-    f32x4 acc[4][RT];
+    f32x4 acc[RT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int i = 0; i < RT; ++i) acc[i] = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; b += NB) {
+        u32x4 w[NB][RT];
+        u32x2 q[NB];
+        uint16_t xs[NB];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[t][i] = 0;
-
-    const int per = (a.KB + a.S - 1) / a.S;
-    const int b1 = min((s + 1) * per, a.KB);
-    for (int b = s * per + wave; b < b1; b += 4) {
-        u32x4 w[RT];
+        for (int i = 0; i < RT; ++i)                       // a row's bytes in a row: whole cache lines
 #pragma unroll
-        for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const u32x4*>(arow[i] + (int64_t)b * 32);
-        u32x2 q[4];
-        float xs[4];
+            for (int k = 0; k < NB; ++k)
+                w[k][i] = *reinterpret_cast<const u32x4*>(A + (aoff[i] + (uint32_t)min(b + k, b1 - 1) * 32u));
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                q[t] = *reinterpret_cast<const u32x2*>(xrow[t] + (int64_t)b * 1024);
-                if constexpr (Q81) xs[t] = (float)__builtin_bit_cast(_Float16, (uint16_t)srow[t][(int64_t)b * 32]);
-            }
+        for (int k = 0; k < NB; ++k) {
+            const uint32_t bk = (uint32_t)min(b + k, b1 - 1);
+            q[k] = *reinterpret_cast<const u32x2*>(xrow + (uint64_t)bk * 1024);
+            if constexpr (Q81) xs[k] = srow[bk * 64u];
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // every load is issued before the first use
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                const u32x4 x = int8_operand<F16>(q[t]);
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const f32x4 from = Q81 ? f32x4(0) : acc[t][i];
-                    const f32x4 d = F16 ? mfma_f16(w[i], x, from) : mfma_bf16(w[i], x, from);
-                    if constexpr (Q81) {
+            for (int i = 0; i < RT; ++i) lds[wave][k * RT + i][lane] = w[k][i];
+        wave_lds_fence();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[t][i][j] = fmaf(xs[t], d[j], acc[t][i][j]);
-                    } else {
-                        acc[t][i] = d;
-                    }
+        for (int k = 0; k < NB; ++k) {
+            if (b + k >= b1) q[k] = 0;                     // the last block's repeat adds nothing
+            const u32x4 x = int8_operand<F16>(q[k]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const u32x4 ww = lds[wave][k * RT + i][piece_at(lane)];
+                const f32x4 from = Q81 ? f32x4(0) : acc[i];
+                const f32x4 d = F16 ? mfma_f16(ww, x, from) : mfma_bf16(ww, x, from);
+                if constexpr (Q81) {
+                    const float f = (float)__builtin_bit_cast(_Float16, xs[k]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(f, d[j], acc[i][j]);
+                } else {
+                    acc[i] = d;
                 }
             }
+        }
+        wave_lds_fence();
     }
+    // the waves' sums: wave i joins and stores tile i
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        if (t < nt)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) red[wave][t * RT + i][lane] = acc[t][i];
+    for (int i = 0; i < RT; ++i) lds[wave][i][lane] = __builtin_bit_cast(u32x4, acc[i]);
     __syncthreads();
-    // wave w joins the tiles w, w + 4, ... (RT of them at most)
+    if (wave >= RT) return;
+    f32x4 d = 0;
 #pragma unroll
-    for (int k = 0; k < RT; ++k) {
-        const int tile = wave + 4 * k, t = tile / RT, i = tile % RT;
-        if (t >= nt) continue;
-        f32x4 d = red[0][tile][lane];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) d += red[w][tile][lane];
-        const int at = 16 * t + c, r = r0 + 16 * i + 4 * g;
-        if (at >= unit.z || r >= a.R) continue;
-        if constexpr (!Q81) d *= a.sa[a.order[unit.y + at]];
-        *reinterpret_cast<f32x4*>(a.part + ((int64_t)s * a.M + unit.y + at) * a.R + r) = d;
+    for (int w = 0; w < DW; ++w) d += __builtin_bit_cast(f32x4, lds[w][wave][lane]);
+    const int r = r0 + 16 * wave + 4 * g;
+    if (c >= rows || r >= a.R) return;
+    if constexpr (!Q81) d *= a.sa[m];
+    const int64_t to = (int64_t)(p0 + c) * a.R + r;
+    if (a.S > 1) {
+        *reinterpret_cast<f32x4*>(a.part + (int64_t)s * a.M * a.R + to) = d;
+    } else {
+        *reinterpret_cast<f32x4*>(a.v + (int64_t)m * a.R + r) = d;
+        store_terms(plane_at(a, p0 + c, r), (int64_t)a.M * a.R, d * a.scale[unit.x]);
     }
 }
 
-template <bool F16, bool BF16>
-__global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles) {
-    constexpr int LD = LORA_RC + 8;                         // a row's stride in LDS: rows on other banks
-    __shared__ __attribute__((aligned(16))) uint16_t vt[3][GROUP_UNIT][LD];
+template <bool F16, bool BF16, bool TAIL>
+__global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs a, int ntiles) {
+    __shared__ __attribute__((aligned(16))) ExpandLds<false, F16, 4> lds;
+    const int u = (int)blockIdx.x / ntiles, tile = (int)blockIdx.x % ntiles;
+    const int4 unit = a.units[u];
+    if (unit.z == 0) return;
+    if (unit.x >= a.E && tile == 0)                         // rows without an adapter: v = 0
+        for (int i = 8 * threadIdx.x; i < unit.z * a.R; i += 8 * LT) {
+            float* to = a.v + (int64_t)a.order[unit.y + i / a.R] * a.R + i % a.R;
+            *reinterpret_cast<f32x4*>(to) = *reinterpret_cast<f32x4*>(to + 4) = 0;
+        }
+    expand_body<false, F16, BF16, TAIL, 4>(a, a.B, a.N, a.base, a.ldb, a.out, a.ldo, unit, tile, lds);
+}
+
+// Operand mapping: A = the rows' v (lane c: row c of 16), B = the adapter's columns (lane c:
+// column n + i of tile i, n = 4c), so a lane ends with four consecutive columns of each of its four
+// rows and 16 lanes write 256 contiguous bytes. A wave has 64 columns of 16 rows (`tall`: the
+// workgroup's four waves the unit's rows; else 256 columns, rows past 16 in a loop) and works
+// alone: its loads depend on the unit, and the base on its rows, and on nothing else. RK: steps of
+// 32 ranks, their operands held; 0 for any number, loaded step by step. TAIL: N % 4 != 0.
+template <int RK, bool F16, bool BF16, bool TAIL>
+__global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int tall) {
+    constexpr int H = RK ? RK : 1;                          // steps held
+    __shared__ u32x4 turn[LT / 64][4 * H][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int u = (int)blockIdx.x / ntiles, tile = (int)blockIdx.x % ntiles;
     const int4 unit = a.units[u];
-    if (unit.z == 0) return;
     const int nt = (unit.z + 15) >> 4;
+    const int t0 = tall ? wave : 0, group = tall ? tile : 4 * tile + wave;
+    const int n0 = 64 * group, n = n0 + 4 * c, left = a.N - n;
+    if (t0 >= nt || n0 >= a.N) return;
     const bool none = unit.x >= a.E;
-    const int n0 = tile * UP_COLS + wave * 64;
+    const uint16_t* B = a.B + ((int64_t)(none ? 0 : unit.x) * a.N + n0) * a.R;
+    const uint32_t col = 4u * piece_row(lane), last = (uint32_t)(a.N - 1 - n0);
 
-    int64_t row[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) row[t] = a.order[unit.y + min(16 * t + c, unit.z - 1)];
-    f32x4 base[4][4], acc[4][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
+    // the columns' pieces of rank step k, zeros past R
+    auto pieces = [&](int k, int at) {
+        const uint32_t r = 32u * k + 8u * piece_of(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            acc[t][i] = 0;
-            base[t][i] = 0;
-            const int n = n0 + 16 * i + 4 * g;
-            if (a.base && t < nt && n < a.N) base[t][i] = load4<BF16>(a.base, row[t] * a.ldb + n, a.N - n);
+            u32x4 raw = 0;
+            if (r < (uint32_t)a.R) raw = *reinterpret_cast<const u32x4*>(B + min(col + i, last) * (uint32_t)a.R + r);
+            turn[wave][at + i][lane] = raw;
         }
-
-    for (int r0 = 0; r0 < a.R; r0 += LORA_RC) {
-        // the rows' v of these ranks: the parts in order, three bf16 terms each; zeros past the
-        // unit's rows and past R
-        if (r0) __syncthreads();
-        for (int idx = threadIdx.x; idx < nt * 16 * (LORA_RC / 4); idx += LT) {
-            const int at = idx / (LORA_RC / 4), r = 4 * (idx % (LORA_RC / 4));
-            f32x4 d = 0;
-            if (at < unit.z && r0 + r < a.R) {
-                if (!none) {
-                    const float* p = a.part + ((int64_t)unit.y + at) * a.R + r0 + r;
-                    for (int s = 0; s < a.S; ++s) d += *reinterpret_cast<const f32x4*>(p + (int64_t)s * a.M * a.R);
+    };
+    // the rows' v of rank step k (the parts in order) as three terms; zeros past the unit and R.
+    // The first columns' wave keeps it
+    auto v_of = [&](int t, int k, u32x4* x) {
+        const int at = 16 * t + c, r = 32 * k + 8 * g;
+        f32x4 d[2] = {0, 0};
+        if (at < unit.z && r < a.R) {
+            if (!none) {
+                const float* p = a.part + ((int64_t)unit.y + at) * a.R + r;
+#pragma unroll 1
+                for (int s = 0; s < a.S; s += 4) {
+                    f32x4 q[4][2];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s + j < a.S) {
+                            q[j][0] = *reinterpret_cast<const f32x4*>(p);
+                            q[j][1] = *reinterpret_cast<const f32x4*>(p + 4);
+                            p += (int64_t)a.M * a.R;
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s + j < a.S) {
+                            d[0] += q[j][0];
+                            d[1] += q[j][1];
+                        }
                 }
-                if (tile == 0) *reinterpret_cast<f32x4*>(a.v + (int64_t)a.order[unit.y + at] * a.R + r0 + r) = d;
             }
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                u32x2 w;
-                w[0] = pack_hi(d[0], d[1]);
-                w[1] = pack_hi(d[2], d[3]);
-                *reinterpret_cast<u32x2*>(&vt[k][at][r]) = w;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] -= cut(d[j]);
+            if (group == 0) {
+                float* to = a.v + (int64_t)a.order[unit.y + at] * a.R + r;
+                *reinterpret_cast<f32x4*>(to) = d[0];
+                *reinterpret_cast<f32x4*>(to + 4) = d[1];
             }
         }
-        __syncthreads();
-        if (none) continue;
+        const float f[8] = {d[0][0], d[0][1], d[0][2], d[0][3], d[1][0], d[1][1], d[1][2], d[1][3]};
+        split3(f, x);
+    };
+    int m[4];
+    auto rows_of = [&](int t) {
 #pragma unroll
-        for (int kk = 0; kk < LORA_RC; kk += 32) {
-            if (r0 + kk >= a.R) break;
-            Weights<F16> w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = min(n0 + 16 * i + c, a.N - 1), r = r0 + kk + 8 * g;
-                u32x4 raw = 0;
-                if (r < a.R) raw = *reinterpret_cast<const u32x4*>(a.B + ((int64_t)unit.x * a.N + n) * a.R + r);
-                w[i].set(raw);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (t < nt) {
-                    u32x4 x[3];
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) x[k] = *reinterpret_cast<const u32x4*>(&vt[k][16 * t + c][kk + 8 * g]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][i] = mfma_terms(w[i], x, acc[t][i]);
-                }
-        }
-    }
+        for (int j = 0; j < 4; ++j) m[j] = a.order[unit.y + min(16 * t + 4 * g + j, unit.z - 1)];
+    };
 
+    rows_of(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (RK != 0)
+        if (!none)
+#pragma unroll
+            for (int k = 0; k < RK; ++k) pieces(k, 4 * k);
     const float scale = none ? 0.f : a.scale[unit.x];
+#pragma unroll 1
+    for (int t = t0; t < nt; t += tall ? 4 : 1) {
+        f32x4 base[4], acc[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        if (t >= nt || 16 * t + c >= unit.z) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 16 * i + 4 * g;
-            if (n >= a.N) continue;
-            f32x4 o = base[t][i];
-            if (!none)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = fmaf(scale, acc[t][i][j], o[j]);
-            store4<BF16>(a.out, row[t] * a.ldo + n, o, a.N - n);
+        for (int j = 0; j < 4; ++j) {
+            acc[j] = base[j] = 0;
+            if (a.base && left > 0) base[j] = load4<BF16>(a.base, m[j] * a.ldb + n, TAIL ? left : 4);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        wave_lds_fence();
+        if constexpr (RK != 0) {
+#pragma unroll
+            for (int k = 0; k < RK; ++k) {
+                u32x4 x[3];
+                v_of(t, k, x);
+                if (none) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Weights<F16> w;
+                    w.set(turn[wave][4 * k + i][piece_at(lane)]);
+                    acc[i] = terms_mfma<F16>(x, w, acc[i]);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; 32 * k < a.R; ++k) {
+                u32x4 x[3];
+                v_of(t, k, x);
+                if (none) continue;
+                wave_lds_fence();
+                pieces(k, 0);
+                wave_lds_fence();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Weights<F16> w;
+                    w.set(turn[wave][i][piece_at(lane)]);
+                    acc[i] = terms_mfma<F16>(x, w, acc[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (left > 0 && 16 * t + 4 * g + j < unit.z) {
+                f32x4 o = base[j];
+                if (!none)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = fmaf(scale, acc[i][j], o[i]);
+                store4<BF16>(a.out, m[j] * a.ldo + n, o, TAIL ? left : 4);
+            }
+        if (!tall && t + 1 < nt) rows_of(t + 1);
     }
 }
 
-// parts that K is split into: about 512 workgroups, four blocks (one a wave) at least
+// Parts that K is split into: a power of two that gives up to 768 workgroups, a block a wave at
+// least.
 int64_t down_parts(int64_t E, int64_t M, int64_t K) {
-    const int64_t units = plan_layout(E, M).nunits;
-    return std::max<int64_t>(1, std::min<int64_t>(512 / units, ceil_div(K / QK, 4)));
+    const int64_t tiles = ceil_div(M, 16) + std::min(E, M);
+    int64_t S = 1;
+    while (S < MAX_PARTS && 2 * S * tiles <= 256 && 2 * S * DW <= K / QK) S *= 2;
+    return S;
 }
 
 template <bool F16, bool Q81>
 void launch_down(const LoraArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.nunits * a.S), (unsigned)ceil_div(a.R, LORA_RC));
-    if (a.R <= 16) hipLaunchKernelGGL((lora_down_kernel<1, F16, Q81>), grid, dim3(LT), 0, s, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((lora_down_kernel<2, F16, Q81>), grid, dim3(LT), 0, s, a);
-    else hipLaunchKernelGGL((lora_down_kernel<4, F16, Q81>), grid, dim3(LT), 0, s, a);
+    const dim3 grid((unsigned)a.nunits * 4 * a.S, (unsigned)ceil_div(a.R, LORA_RC));
+    if (a.R <= 16) hipLaunchKernelGGL((lora_down_kernel<1, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+    else if (a.R <= 32) hipLaunchKernelGGL((lora_down_kernel<2, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+    else hipLaunchKernelGGL((lora_down_kernel<4, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+}
+
+template <bool F16, bool BF16, bool TAIL>
+void launch_up(const LoraArgs& a, hipStream_t s) {
+    // units of more than 16 rows on average: their row tiles side by side, 64 columns a workgroup
+    const int tall = a.M > 16 * std::min(a.E, a.M);
+    const int ntiles = (int)ceil_div(a.N, tall ? 64 : UP_COLS);
+    const dim3 grid((unsigned)a.nunits * (unsigned)ntiles);
+    if (a.R <= 32) hipLaunchKernelGGL((lora_up_kernel<1, F16, BF16, TAIL>), grid, dim3(LT), 0, s, a, ntiles, tall);
+    else if (a.R <= 64) hipLaunchKernelGGL((lora_up_kernel<2, F16, BF16, TAIL>), grid, dim3(LT), 0, s, a, ntiles, tall);
+    else hipLaunchKernelGGL((lora_up_kernel<0, F16, BF16, TAIL>), grid, dim3(LT), 0, s, a, ntiles, tall);
+}
+template <bool F16, bool BF16>
+void launch_up(const LoraArgs& a, hipStream_t s) {
+    if (a.S == 1) {
+        const int ntiles = (int)ceil_div(a.N, 64);
+        const dim3 grid((unsigned)a.nunits * (unsigned)ntiles);
+        if (a.N % 4) hipLaunchKernelGGL((lora_expand_kernel<F16, BF16, true>), grid, dim3(LT), 0, s, a, ntiles);
+        else hipLaunchKernelGGL((lora_expand_kernel<F16, BF16, false>), grid, dim3(LT), 0, s, a, ntiles);
+        return;
+    }
+    if (a.N % 4) launch_up<F16, BF16, true>(a, s);
+    else launch_up<F16, BF16, false>(a, s);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R) {
-    return (size_t)round_up(down_parts(E, M, K) * M * R * 4, REGION_ALIGN);
+    const int64_t S = down_parts(E, M, K);
+    return (size_t)round_up(M * R * (S > 1 ? 4 * S : 6), REGION_ALIGN);      // f32 parts, or three bf16 planes
 }
 
-// both launches' grids stay below 2^32 threads
+// both launches' grids stay below 2^32 threads (the down kernel has nunits * 4 * S workgroups, S > 1
+// only for few units)
 bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K) {
     const int64_t units = plan_layout(E, M).nunits;
-    return units * std::max(ceil_div(N, UP_COLS), ceil_div(K, UP_COLS)) < (int64_t(1) << 32) / LT;
+    return units * std::max<int64_t>({ceil_div(N, 64), ceil_div(K, 64), 8}) < (int64_t(1) << 32) / LT;
 }
 
 hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
@@ -225,6 +325,7 @@ hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, co
                        int64_t ldb, void* out, int64_t ldo, float* v, void* ws, hipStream_t s) {
     LoraArgs a = lora_args(t, act, A, B, scale, E, R, plan, M, N, K);
     a.part = static_cast<float*>(ws);
+    a.planes = static_cast<uint16_t*>(ws);
     a.S = (int)down_parts(E, M, K);
     a.base = base;
     a.ldb = ldb;
@@ -236,15 +337,8 @@ hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, co
     else q81 ? launch_down<false, true>(a, s) : launch_down<false, false>(a, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int ntiles = (int)ceil_div(N, UP_COLS);
-    const dim3 grid((unsigned)a.nunits * (unsigned)ntiles);
-    if (f16) {
-        if (q81) hipLaunchKernelGGL((lora_up_kernel<true, false>), grid, dim3(LT), 0, s, a, ntiles);
-        else hipLaunchKernelGGL((lora_up_kernel<true, true>), grid, dim3(LT), 0, s, a, ntiles);
-    } else {
-        if (q81) hipLaunchKernelGGL((lora_up_kernel<false, false>), grid, dim3(LT), 0, s, a, ntiles);
-        else hipLaunchKernelGGL((lora_up_kernel<false, true>), grid, dim3(LT), 0, s, a, ntiles);
-    }
+    if (f16) q81 ? launch_up<true, false>(a, s) : launch_up<true, true>(a, s);
+    else q81 ? launch_up<false, false>(a, s) : launch_up<false, true>(a, s);
     return hipGetLastError();
 }
 

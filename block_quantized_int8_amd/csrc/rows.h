@@ -15,12 +15,14 @@ struct PlanLayout {
 };
 PlanLayout plan_layout(int64_t E, int64_t P);
 
-// f32 -> bf16 bits, round to nearest even, NaN kept a NaN
-__device__ inline uint16_t bf16_rne(float x) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+// f32 -> bf16 bits, round to nearest even, NaN kept a NaN (v_cvt_pk_bf16_f32)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t bf16_pair(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
+__device__ inline uint16_t bf16_rne(float x) { return (uint16_t)bf16_pair(x, x); }
 
 hipError_t launch_group_rows(const int32_t* ids, int64_t E, int64_t P, void* plan, hipStream_t s);
 hipError_t launch_moe_gather(mmq_otype o, const void* x, int64_t ldx, const void* plan, int64_t E,

@@ -182,7 +182,7 @@ template <typename T> struct Piece {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 4) r[i] = __builtin_bit_cast(uint32_t, v[i]);
-            else r[i] = (uint32_t)bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
+            else r[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
         }
     }
     __device__ T bits(int i) const {

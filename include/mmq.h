@@ -350,7 +350,7 @@ size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
  *  workspace (device) >= mmq_lora_workspace_bytes(E, M, K, R) bytes; needs no initialisation. Two
  *        calls that overlap in time must not share one.
  * R is a multiple of 8, at most 256; K a multiple of 32; 1 <= E <= 4096. The strides are in
- * elements, >= N, and need no alignment. MMQ_EINVAL also where ceil(N/256) or ceil(K/256)
+ * elements, >= N, and need no alignment. MMQ_EINVAL also where ceil(N/64) or ceil(K/64)
  * workgroups for each of the plan's units reach 2^24. */
 mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B,
                     const float* scale, int64_t E, int64_t R, const void* plan, int64_t M, int64_t N,
