@@ -3,6 +3,13 @@
 //     dx[m] = dxb[m] + A_e^T u[m]   dA_e = sum over the rows of e of u[m] x^[m]^T
 // The act buffer is read as it is: its int8 values enter the matrix core exactly and each block's
 // scale goes to u's side, so no activation is ever restored to f32 in memory.
+//
+// Two launches, each of two kinds of workgroups that need nothing of each other:
+//   1. u (16 rows, its eight waves share N) and dB_e (64 columns of N, the waves share the rows);
+//      u is left in f32 and as bf16 terms in operand order;
+//   2. dA_e (one block of K, the waves share the rows) and dx (expand_body).
+// The workgroups that sum over rows own their output tile, so nothing is added across
+// workgroups and the sums have one order.
 #include <algorithm>
 
 #include "lora.h"
@@ -23,11 +30,6 @@ template <bool BF16> struct Grad {
         }
     }
 };
-
-template <bool BF16> __device__ inline float grad_at(const void* p, int64_t at) {
-    if constexpr (BF16) return as_f((uint32_t)static_cast<const uint16_t*>(p)[at] << 16);
-    else return static_cast<const float*>(p)[at];
-}
 
 template <bool F16, bool BF16>
 __device__ inline f32x4 mfma_grad(const Weights<F16>& w, const Grad<BF16>& x, f32x4 acc) {
@@ -52,347 +54,358 @@ template <int T> __device__ inline f32x4 mfma_3(const u32x4* a, const u32x4* b, 
     return mfma_bf16(a[0], b[0], acc);
 }
 
-// Eight 16-bit values, `step` apart, as an operand's raw bits.
-__device__ inline u32x4 gather8(const uint16_t* p, int64_t step) {
-    u32x4 r;
+constexpr int GW = 8;               // waves of a workgroup of either launch
+
+// Eight bf16 values of a row, zeros from `left` on.
+__device__ inline u32x4 load8(const uint16_t* p, int left) {
+    if (left >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+    u32x4 r = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (uint32_t)p[2 * i * step] | ((uint32_t)p[(2 * i + 1) * step] << 16);
+    for (int i = 0; i < 7; ++i)
+        if (i < left) r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     return r;
 }
 
-// Partial u over the S parts of N: [s][sorted position][R].
-template <int RT, bool F16, bool BF16>
-__global__ __launch_bounds__(LT) void lora_u_kernel(LoraArgs a) {
-    __shared__ f32x4 red[4][4 * RT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, g = lane >> 4;
-    const int u = (int)blockIdx.x / a.S, s = (int)blockIdx.x % a.S;
-    const int4 unit = a.units[u];
-    if (unit.z == 0 || unit.x >= a.E) return;
-    const int r0 = (int)blockIdx.y * LORA_RC;
-    const int nt = (unit.z + 15) >> 4;
-    int64_t row[4];
+template <int RT> struct RankVec;
+template <> struct RankVec<1> { typedef float V; };
+template <> struct RankVec<2> { typedef f32x2 V; };
+template <> struct RankVec<4> { typedef f32x4 V; };
+
+// RT values of consecutive ranks of eight rows as operands (tile i: the i-th of them)
+template <int RT> __device__ inline void rank_operands(const typename RankVec<RT>::V* v, u32x4 (*t)[3]) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) row[t] = (int64_t)a.order[unit.y + min(16 * t + c, unit.z - 1)] * a.lddy;
-    f32x4 acc[4][RT];
+    for (int i = 0; i < RT; ++i) {
+        float x[8];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) acc[t][i] = 0;
-    const int NB = (a.N + 31) / 32, per = (NB + a.S - 1) / a.S;
-    const int b1 = min((s + 1) * per, NB);
-    for (int b = s * per + wave; b < b1; b += 4) {
-        const int n = 32 * b + 8 * g;
-        Weights<F16> w[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int r = min(r0 + 16 * i + c, a.R - 1);
-            const uint16_t* p = a.B + ((int64_t)unit.x * a.N) * a.R + r;
-            u32x4 raw;
-            if (n + 8 <= a.N) raw = gather8(p + (int64_t)n * a.R, a.R);
-            else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    raw[j] = (uint32_t)p[(int64_t)min(n + 2 * j, a.N - 1) * a.R] |
-                             ((uint32_t)p[(int64_t)min(n + 2 * j + 1, a.N - 1) * a.R] << 16);
-            }
-            w[i].set(raw);
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (RT == 1) x[j] = v[j];
+            else x[j] = v[j][i];
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                float x[8];
-                const f32x4 lo = n < a.N ? load4<BF16>(a.dy, row[t] + n, a.N - n) : f32x4(0);
-                const f32x4 hi = n + 4 < a.N ? load4<BF16>(a.dy, row[t] + n + 4, a.N - n - 4) : f32x4(0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] = lo[j];
-                    x[4 + j] = hi[j];
-                }
-                Grad<BF16> d;
-                d.set(x);
-#pragma unroll
-                for (int i = 0; i < RT; ++i) acc[t][i] = mfma_grad<F16, BF16>(w[i], d, acc[t][i]);
-            }
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        if (t < nt)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) red[wave][t * RT + i][lane] = acc[t][i];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < RT; ++k) {
-        const int tile = wave + 4 * k, t = tile / RT, i = tile % RT;
-        if (t >= nt) continue;
-        f32x4 d = red[0][tile][lane];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) d += red[w][tile][lane];
-        const int at = 16 * t + c, r = r0 + 16 * i + 4 * g;
-        if (at >= unit.z || r >= a.R) continue;
-        *reinterpret_cast<f32x4*>(a.part + ((int64_t)s * a.M + unit.y + at) * a.R + r) = d;
+        split3(x, t[i]);
     }
 }
 
-// u = s_e times the sum of the parts, in order; a workgroup per unit.
-__global__ __launch_bounds__(LT) void lora_u_join_kernel(LoraArgs a) {
-    const int4 unit = a.units[blockIdx.x];
-    if (unit.z == 0 || unit.x >= a.E) return;
-    const float scale = a.scale[unit.x];
-    const int64_t at = (int64_t)unit.y * a.R;
-    for (int i = 4 * threadIdx.x; i < unit.z * a.R; i += 4 * LT) {
-        f32x4 d = 0;
-        for (int s = 0; s < a.S; ++s) d += *reinterpret_cast<const f32x4*>(a.part + (int64_t)s * a.M * a.R + at + i);
-        *reinterpret_cast<f32x4*>(a.u + at + i) = d * scale;
-    }
+template <int RT> __device__ inline void store_ranks(float* p, const float* d) {
+    typename RankVec<RT>::V v;
+    if constexpr (RT == 1) v = d[0];
+    else
+#pragma unroll
+        for (int i = 0; i < RT; ++i) v[i] = d[i];
+    *reinterpret_cast<typename RankVec<RT>::V*>(p) = v;
 }
 
-// Joins the four waves' accumulators in LDS: wave w returns the tiles w, w + 4, ... .
-template <int NT> __device__ inline void join_waves(f32x4 (*red)[NT][64], f32x4* acc, int wave, int lane) {
+// Joins the waves' NT accumulators; wave w is left with the tiles w, w + GW, ... .
+template <int NT> using JoinLds = f32x4[GW / 2][NT][64];
+template <int NT> __device__ inline void join_waves(JoinLds<NT>& red, f32x4* acc, int wave, int lane) {
+    __syncthreads();                                       // the memory may have had another use
+    if (wave >= GW / 2)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) red[wave][i][lane] = acc[i];
+        for (int i = 0; i < NT; ++i) red[wave - GW / 2][i][lane] = acc[i];
+    __syncthreads();
+    if (wave < GW / 2)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) red[wave][i][lane] += acc[i];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NT / 4; ++k) {
-        f32x4 d = red[0][wave + 4 * k][lane];
+    for (int k = 0; k < (NT + GW - 1) / GW; ++k) {
+        const int i = wave + GW * k;
+        if (i >= NT) break;
+        f32x4 d = red[0][i][lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) d += red[w][wave + 4 * k][lane];
+        for (int w = 1; w < GW / 2; ++w) d += red[w][i][lane];
         acc[k] = d;
     }
 }
 
-// dB_e[n][r] over all rows of adapter e: a workgroup has 64 columns n and up to 64 ranks, its
-// waves every fourth 32 rows.
-template <int RT, bool BF16>
-__global__ __launch_bounds__(LT) void lora_dB_kernel(LoraArgs a, int ntiles) {
-    __shared__ f32x4 red[4][4 * RT][64];
+// ------------------------------------------------------------------------------ launch 1
+// u of 16 rows. Each wave turns its blocks of 32 columns in LDS of its own: dy's rows (as terms)
+// into the B operand, B_e's rows of ranks into the A operand.
+template <int RT, bool F16, bool BF16> struct ULds {
+    uint16_t dy[Grad<BF16>::T][16][40];
+    uint16_t w[Weights<F16>::T][32][16 * RT + 8];
+};
+
+template <int RT, bool F16, bool BF16>
+__device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16, BF16>* turn, JoinLds<RT>& red) {
+    constexpr int NB = 2, T = Weights<F16>::T;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int e = (int)blockIdx.x / ntiles, n0 = ((int)blockIdx.x % ntiles) * 64;
-    const int r0 = (int)blockIdx.y * LORA_RC;
+    const int sub = block / a.nunits;                      // a unit's first 16 rows come first
+    const int4 unit = a.units[block - sub * a.nunits];
+    const int rows = min(unit.z - 16 * sub, 16);
+    if (rows <= 0 || unit.x >= a.E) return;
+    const int p0 = unit.y + 16 * sub, per_row = min(a.R - r0, LORA_RC) / 8;     // pieces of a row of B_e
+
+    const int64_t row = (int64_t)a.order[p0 + min(piece_row(lane), rows - 1)] * a.lddy;
+    const uint16_t* B = a.B + (int64_t)unit.x * a.N * a.R + r0;
+    uint32_t brow[RT], bcol[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int idx = min(lane + 64 * i, 32 * per_row - 1);                   // the last piece again past them
+        brow[i] = idx / per_row;
+        bcol[i] = 8 * (idx % per_row);
+    }
+    ULds<RT, F16, BF16>& mine = turn[wave];
+    f32x4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = 0;
+    const int blocks = (a.N + 31) / 32, per = (blocks + GW - 1) / GW;
+    const int b0 = wave * per, b1 = min(b0 + per, blocks);
+#pragma unroll 1
+    for (int b = b0; b < b1; b += NB) {
+        u32x4 x[NB][BF16 ? 1 : 2], w[NB][RT];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int n = 32 * min(b + k, b1 - 1);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                w[k][i] = *reinterpret_cast<const u32x4*>(B + (int64_t)min(n + (int)brow[i], a.N - 1) * a.R + bcol[i]);
+            if constexpr (BF16) {
+                const int nn = n + 8 * piece_of(lane);
+                x[k][0] = load8(static_cast<const uint16_t*>(a.dy) + row + nn, a.N - nn);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int nn = n + 16 * h + 4 * piece_of(lane);
+                    x[k][h] = __builtin_bit_cast(u32x4, load4<false>(a.dy, row + nn, a.N - nn));
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // every load is issued before the first use
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            if (b + k >= b1) break;
+            wave_lds_fence();
+            if constexpr (BF16) {
+                *reinterpret_cast<u32x4*>(&mine.dy[0][piece_row(lane)][8 * piece_of(lane)]) = x[k][0];
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    store_terms(&mine.dy[0][piece_row(lane)][16 * h + 4 * piece_of(lane)], 16 * 40, __builtin_bit_cast(f32x4, x[k][h]));
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                Weights<F16> ww;
+                ww.set(w[k][i]);
+#pragma unroll
+                for (int j = 0; j < T; ++j) *reinterpret_cast<u32x4*>(&mine.w[j][brow[i]][bcol[i]]) = ww.t[j];
+            }
+            wave_lds_fence();
+            Grad<BF16> d;
+#pragma unroll
+            for (int j = 0; j < Grad<BF16>::T; ++j) d.t[j] = *reinterpret_cast<const u32x4*>(&mine.dy[j][c][8 * g]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                Weights<F16> ww;
+#pragma unroll
+                for (int j = 0; j < T; ++j) ww.t[j] = turned_operand(&mine.w[j][0][16 * i], 16 * RT + 8, lane);
+                acc[i] = mfma_grad<F16, BF16>(ww, d, acc[i]);
+            }
+        }
+    }
+    join_waves<RT>(red, acc, wave, lane);
+    const int r = r0 + 16 * wave + 4 * g;
+    if (wave >= RT || c >= rows || r >= a.R) return;
+    const f32x4 d = acc[0] * a.scale[unit.x];
+    *reinterpret_cast<f32x4*>(a.u + (int64_t)(p0 + c) * a.R + r) = d;
+    store_terms(plane_at(a, p0 + c, r), (int64_t)a.M * a.R, d);
+}
+
+// dB_e[n][r] over all rows of adapter e: 64 columns n and up to 64 ranks, the waves every eighth 32
+// rows. Both operands come straight from memory: a lane loads four consecutive columns (RT
+// consecutive ranks) of eight rows, which are its k.
+template <int RT, bool BF16>
+__device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles, JoinLds<4 * RT>& red) {
+    typedef typename RankVec<RT>::V V;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4;
+    const int e = block / ntiles, n0 = (block - e * ntiles) * 64, n = n0 + 4 * c;
     const int p0 = a.offs[e], p1 = a.offs[e + 1];
+    const float* vr = a.v + min(r0 + RT * c, a.R - RT);
     f32x4 acc[4 * RT];
 #pragma unroll
     for (int i = 0; i < 4 * RT; ++i) acc[i] = 0;
-    for (int p = p0 + 32 * wave; p < p1; p += 128) {
-        int64_t row[8];
-        bool live[8];
+#pragma unroll 1
+    for (int p = p0 + 32 * wave; p < p1; p += 32 * GW) {
+        int m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = a.order[min(p + 8 * g + j, p1 - 1)];
+        f32x4 x[8];
+        V v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            live[j] = p + 8 * g + j < p1;
-            row[j] = a.order[min(p + 8 * g + j, p1 - 1)];
+            x[j] = 0;
+            if (n < a.N) x[j] = load4<BF16>(a.dy, m[j] * a.lddy + n, a.N - n);
+            v[j] = *reinterpret_cast<const V*>(vr + (int64_t)m[j] * a.R);
         }
-        u32x4 v[RT][3];
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 t[RT][3];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            float x[8];
+        for (int j = 0; j < 8; ++j)
+            if (p + 8 * g + j >= p1) v[j] = V(0);          // the last row's repeats add nothing
+        rank_operands<RT>(v, t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float w = a.v[row[j] * a.R + min(r0 + 16 * i + c, a.R - 1)];
-                x[j] = live[j] ? w : 0.f;
-            }
-            split3(x, v[i]);
-        }
+        for (int k = 0; k < 4; ++k) {
+            float f[8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            float x[8];
-            const int n = min(n0 + 16 * t + c, a.N - 1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = grad_at<BF16>(a.dy, row[j] * a.lddy + n);
+            for (int j = 0; j < 8; ++j) f[j] = x[j][k];
             Grad<BF16> d;
-            d.set(x);
+            d.set(f);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) acc[t * RT + i] = mfma_3<Grad<BF16>::T>(v[i], d.t, acc[t * RT + i]);
+            for (int i = 0; i < RT; ++i) acc[k * RT + i] = mfma_3<Grad<BF16>::T>(t[i], d.t, acc[k * RT + i]);
         }
     }
+    // rows of the accumulators: ranks r0 + RT (4g + j) + i; column: n0 + 4c + k
     join_waves<4 * RT>(red, acc, wave, lane);
     const float scale = a.scale[e];
 #pragma unroll
-    for (int k = 0; k < RT; ++k) {
-        const int tile = wave + 4 * k, n = n0 + 16 * (tile / RT) + c, r = r0 + 16 * (tile % RT) + 4 * g;
-        if (n < a.N && r < a.R) *reinterpret_cast<f32x4*>(a.dB + ((int64_t)e * a.N + n) * a.R + r) = acc[k] * scale;
+    for (int q = 0; q < (4 * RT + GW - 1) / GW; ++q) {
+        const int tile = wave + GW * q, k = tile / RT, i = tile % RT;
+        if (tile >= 4 * RT || n + k >= a.N) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = r0 + RT * (4 * g + j) + i;
+            if (r < a.R) a.dB[((int64_t)e * a.N + n + k) * a.R + r] = acc[q][j] * scale;
+        }
     }
 }
 
-// dA_e[r][k] over all rows of adapter e: a workgroup has two blocks of K and up to 64 ranks.
+template <int RT, bool F16, bool BF16>
+__global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, int ntiles) {
+    __shared__ __attribute__((aligned(16))) union {
+        struct { ULds<RT, F16, BF16> turn[GW]; } u;
+        JoinLds<RT> ju;
+        JoinLds<4 * RT> jb;
+    } lds;
+    const int r0 = (int)blockIdx.y * LORA_RC, nu = 4 * a.nunits;
+    if ((int)blockIdx.x < nu) u_body<RT, F16, BF16>(a, (int)blockIdx.x, r0, lds.u.turn, lds.ju);
+    else dB_body<RT, BF16>(a, (int)blockIdx.x - nu, r0, ntiles, lds.jb);
+}
+
+// ------------------------------------------------------------------------------ launch 2
+// dA_e[r][k] over all rows of adapter e: one block of K and up to 64 ranks, the waves every eighth
+// 32 rows. A wave loads the 32 rows' 1 KB of the block (16 bytes a lane), turns them in LDS as
+// bf16, and scales u by the rows' block scales.
+struct ALds {
+    uint16_t x[32][40];
+    float xs[32];
+};
+
 template <int RT, bool Q81>
-__global__ __launch_bounds__(LT) void lora_dA_kernel(LoraArgs a, int ktiles) {
-    __shared__ f32x4 red[4][4 * RT][64];
+__device__ inline void dA_body(const LoraArgs& a, int block, int r0, ALds* turn, JoinLds<2 * RT>& red) {
+    typedef typename RankVec<RT>::V V;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int e = (int)blockIdx.x / ktiles, b0 = ((int)blockIdx.x % ktiles) * 2;
-    const int r0 = (int)blockIdx.y * LORA_RC;
+    const int e = block / a.KB, b = block - e * a.KB;
     const int p0 = a.offs[e], p1 = a.offs[e + 1];
-    f32x4 acc[4 * RT];
+    const float* ur = a.u + min(r0 + RT * c, a.R - RT);
+    ALds& mine = turn[wave];
+    f32x4 acc[2 * RT];
 #pragma unroll
-    for (int i = 0; i < 4 * RT; ++i) acc[i] = 0;
-    for (int p = p0 + 32 * wave; p < p1; p += 128) {
-        int m[8];
-        float u[RT][8];
+    for (int i = 0; i < 2 * RT; ++i) acc[i] = 0;
+#pragma unroll 1
+    for (int p = p0 + 32 * wave; p < p1; p += 32 * GW) {
+        const int row = lane & 31, m = a.order[min(p + row, p1 - 1)];
+        V u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int at = min(p + 8 * g + j, p1 - 1);
-            m[j] = a.order[at];
+        for (int j = 0; j < 8; ++j) u[j] = *reinterpret_cast<const V*>(ur + (int64_t)min(p + 8 * g + j, p1 - 1) * a.R);
+        const int64_t cell = (int64_t)(m >> 5) * a.KBp + b;
+        const u32x4 q = *reinterpret_cast<const u32x4*>(a.xq + cell * 1024 + ((lane >> 5) * 32 + (m & 31)) * 16);
+        float xs;
+        if constexpr (Q81) xs = (float)__builtin_bit_cast(_Float16, (uint16_t)a.xs2[cell * 32 + (m & 31)]);
+        else xs = a.sa[m];
+        __builtin_amdgcn_sched_barrier(0);
+        wave_lds_fence();
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const float w = a.u[(int64_t)at * a.R + min(r0 + 16 * i + c, a.R - 1)];
-                u[i][j] = p + 8 * g + j < p1 ? w : 0.f;
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<u32x4*>(&mine.x[row][16 * (lane >> 5) + 8 * h]) = int8_operand<false>(u32x2{q[2 * h], q[2 * h + 1]});
+        if (lane < 32) mine.xs[row] = p + row < p1 ? xs : 0.f;     // the last row's repeats add nothing
+        wave_lds_fence();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= mine.xs[8 * g + j];
+        u32x4 t[RT][3], x[2];
+        rank_operands<RT>(u, t);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = turned_operand(&mine.x[0][16 * h], 40, lane);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4& s = acc[h * RT + i];
+                s = mfma_bf16(t[i][2], x[h], s);
+                s = mfma_bf16(t[i][1], x[h], s);
+                s = mfma_bf16(t[i][0], x[h], s);
             }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int b = min(b0 + k, a.KB - 1);            // past K: a block's repeat, not stored
-            u32x4 x[2];
-            float xs[8];
-            u32x2 q[2];
-            q[0] = q[1] = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t cell = (int64_t)(m[j] >> 5) * a.KBp + b;
-                const uint8_t* from = reinterpret_cast<const uint8_t*>(a.xq) + cell * 1024 + (m[j] & 31) * 16 + c;
-                q[0][j / 4] |= (uint32_t)from[0] << (8 * (j & 3));
-                q[1][j / 4] |= (uint32_t)from[512] << (8 * (j & 3));
-                if constexpr (Q81) xs[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)a.xs2[cell * 32 + (m[j] & 31)]);
-                else xs[j] = a.sa[m[j]];
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) x[h] = int8_operand<false>(q[h]);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                float w[8];
-                u32x4 t[3];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = u[i][j] * xs[j];
-                split3(w, t);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f32x4& s = acc[(2 * k + h) * RT + i];
-                    s = mfma_bf16(x[h], t[2], s);
-                    s = mfma_bf16(x[h], t[1], s);
-                    s = mfma_bf16(x[h], t[0], s);
-                }
-            }
-        }
     }
-    join_waves<4 * RT>(red, acc, wave, lane);
+    // rows of the accumulators: ranks r0 + RT (4g + j) + i; column: k = 32b + 16h + c
+    join_waves<2 * RT>(red, acc, wave, lane);
+    if (wave >= 2 * RT) return;
+    const int h = wave / RT, i = wave % RT;
 #pragma unroll
-    for (int k = 0; k < RT; ++k) {
-        const int tile = wave + 4 * k, kt = tile / RT, r = r0 + 16 * (tile % RT) + c;
-        if (b0 + kt / 2 < a.KB && r < a.R)
-            *reinterpret_cast<f32x4*>(a.dA + ((int64_t)e * a.R + r) * a.K + 32 * b0 + 16 * kt + 4 * g) = acc[k];
+    for (int j = 0; j < 4; ++j) {
+        const int r = r0 + RT * (4 * g + j) + i;
+        if (r < a.R) a.dA[((int64_t)e * a.R + r) * a.K + 32 * b + 16 * h + c] = acc[0][j];
     }
 }
 
-// dx = dxb + A_e^T u over (unit, 256 columns).
-template <bool F16>
-__global__ __launch_bounds__(LT) void lora_dx_kernel(LoraArgs a, int ktiles) {
-    constexpr int LD = LORA_RC + 8;
-    __shared__ __attribute__((aligned(16))) uint16_t ut[3][GROUP_UNIT][LD];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, g = lane >> 4;
-    const int u = (int)blockIdx.x / ktiles, tile = (int)blockIdx.x % ktiles;
+template <int RT, bool F16, bool Q81>
+__global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int ktiles) {
+    __shared__ __attribute__((aligned(16))) union {
+        ALds turn[GW];
+        JoinLds<2 * RT> ja;
+        ExpandLds<true, F16, GW> x;
+    } lds;
+    const int na = a.E * a.KB;
+    if ((int)blockIdx.x < na) {
+        dA_body<RT, Q81>(a, (int)blockIdx.x, (int)blockIdx.y * LORA_RC, lds.turn, lds.ja);
+        return;
+    }
+    if (blockIdx.y) return;
+    const int block = (int)blockIdx.x - na, u = block / ktiles;
     const int4 unit = a.units[u];
     if (unit.z == 0) return;
-    const int nt = (unit.z + 15) >> 4;
-    const bool none = unit.x >= a.E;
-    const int k0 = tile * UP_COLS + wave * 64;
-    int64_t row[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) row[t] = a.order[unit.y + min(16 * t + c, unit.z - 1)];
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[t][i] = 0;
-            const int k = k0 + 16 * i + 4 * g;
-            if (a.dxb && t < nt && k < a.K) acc[t][i] = load4<false>(a.dxb, row[t] * a.lddxb + k, a.K - k);
-        }
-    if (!none)
-        for (int r0 = 0; r0 < a.R; r0 += LORA_RC) {
-            if (r0) __syncthreads();
-            for (int idx = threadIdx.x; idx < nt * 16 * (LORA_RC / 4); idx += LT) {
-                const int at = idx / (LORA_RC / 4), r = 4 * (idx % (LORA_RC / 4));
-                f32x4 d = 0;
-                if (at < unit.z && r0 + r < a.R)
-                    d = *reinterpret_cast<const f32x4*>(a.u + ((int64_t)unit.y + at) * a.R + r0 + r);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    u32x2 w;
-                    w[0] = pack_hi(d[0], d[1]);
-                    w[1] = pack_hi(d[2], d[3]);
-                    *reinterpret_cast<u32x2*>(&ut[k][at][r]) = w;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[j] -= cut(d[j]);
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int kk = 0; kk < LORA_RC; kk += 32) {
-                if (r0 + kk >= a.R) break;
-                Weights<F16> w[4];
-                const int r = r0 + kk + 8 * g;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = min(k0 + 16 * i + c, a.K - 1);
-                    u32x4 raw = 0;
-                    if (r < a.R) raw = gather8(a.A + ((int64_t)unit.x * a.R + r) * a.K + k, a.K);
-                    w[i].set(raw);
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (t < nt) {
-                        u32x4 x[3];
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) x[k] = *reinterpret_cast<const u32x4*>(&ut[k][16 * t + c][kk + 8 * g]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[t][i] = mfma_terms(w[i], x, acc[t][i]);
-                    }
-            }
-        }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        if (t >= nt || 16 * t + c >= unit.z) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = k0 + 16 * i + 4 * g;
-            if (k < a.K) store4<false>(a.dx, row[t] * a.lddx + k, acc[t][i], a.K - k);
-        }
-    }
+    expand_body<true, F16, false, false, GW>(a, a.A, a.K, a.dxb, a.lddxb, a.dx, a.lddx, unit, block - u * ktiles, lds.x);
 }
 
-int64_t u_parts(int64_t E, int64_t M, int64_t N) {
-    const int64_t units = plan_layout(E, M).nunits;
-    return std::max<int64_t>(1, std::min<int64_t>(512 / units, ceil_div(N, 128)));
-}
+constexpr int DX_COLS = 16 * GW;                           // columns of a dx workgroup
 
 template <int RT>
-void launch_sums(const LoraArgs& a, bool f16, bool q81, hipStream_t s) {
+void launch_grads(const LoraArgs& a, bool f16, bool q81, hipStream_t s) {
     const unsigned rc = (unsigned)ceil_div(a.R, LORA_RC);
-    const dim3 gu((unsigned)(a.nunits * a.S), rc);
+    const int nt = (int)ceil_div(a.N, 64), kt = (int)ceil_div(a.K, DX_COLS);
+    const dim3 g1((unsigned)(4 * a.nunits + a.E * nt), rc), g2((unsigned)(a.E * a.KB + (a.dx ? a.nunits * kt : 0)), rc);
+    const dim3 th(GW * 64);
     if (f16) {
-        if (q81) hipLaunchKernelGGL((lora_u_kernel<RT, true, false>), gu, dim3(LT), 0, s, a);
-        else hipLaunchKernelGGL((lora_u_kernel<RT, true, true>), gu, dim3(LT), 0, s, a);
+        if (q81) {
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, false>), g1, th, 0, s, a, nt);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, true>), g2, th, 0, s, a, kt);
+        } else {
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, true>), g1, th, 0, s, a, nt);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, false>), g2, th, 0, s, a, kt);
+        }
     } else {
-        if (q81) hipLaunchKernelGGL((lora_u_kernel<RT, false, false>), gu, dim3(LT), 0, s, a);
-        else hipLaunchKernelGGL((lora_u_kernel<RT, false, true>), gu, dim3(LT), 0, s, a);
-    }
-    hipLaunchKernelGGL(lora_u_join_kernel, dim3((unsigned)a.nunits), dim3(LT), 0, s, a);
-    const int nt = (int)ceil_div(a.N, 64), kt = (int)ceil_div(a.KB, 2);
-    const dim3 gb((unsigned)(a.E * nt), rc), ga((unsigned)(a.E * kt), rc);
-    if (q81) {
-        hipLaunchKernelGGL((lora_dB_kernel<RT, false>), gb, dim3(LT), 0, s, a, nt);
-        hipLaunchKernelGGL((lora_dA_kernel<RT, true>), ga, dim3(LT), 0, s, a, kt);
-    } else {
-        hipLaunchKernelGGL((lora_dB_kernel<RT, true>), gb, dim3(LT), 0, s, a, nt);
-        hipLaunchKernelGGL((lora_dA_kernel<RT, false>), ga, dim3(LT), 0, s, a, kt);
+        if (q81) {
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, false>), g1, th, 0, s, a, nt);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, true>), g2, th, 0, s, a, kt);
+        } else {
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, true>), g1, th, 0, s, a, nt);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, false>), g2, th, 0, s, a, kt);
+        }
     }
 }
 
 }  // namespace
 
-size_t lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t R) {
-    return (size_t)(round_up(u_parts(E, M, N) * M * R * 4, REGION_ALIGN) + round_up(M * R * 4, REGION_ALIGN));
+// f32 u and its three bf16 planes
+size_t lora_grad_workspace_bytes(int64_t M, int64_t R) {
+    return (size_t)(round_up(M * R * 4, REGION_ALIGN) + round_up(M * R * 6, REGION_ALIGN));
+}
+
+// both launches' grids stay below 2^32 threads
+bool lora_grad_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K) {
+    const int64_t units = plan_layout(E, M).nunits;
+    return 4 * units + E * ceil_div(N, 64) < (int64_t(1) << 32) / (GW * 64) &&
+           E * (K / QK) + units * ceil_div(K, DX_COLS) < (int64_t(1) << 32) / (GW * 64);
 }
 
 hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
@@ -409,19 +422,12 @@ hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* 
     a.lddx = lddx;
     a.dA = dA;
     a.dB = dB;
-    a.S = (int)u_parts(E, M, N);
-    a.part = static_cast<float*>(ws);
-    a.u = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round_up((int64_t)a.S * M * R * 4, REGION_ALIGN));
+    a.u = static_cast<float*>(ws);
+    a.planes = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + round_up(M * R * 4, REGION_ALIGN));
     const bool q81 = t == MMQ_ACT_Q8_1;
-    if (R <= 16) launch_sums<1>(a, f16, q81, s);
-    else if (R <= 32) launch_sums<2>(a, f16, q81, s);
-    else launch_sums<4>(a, f16, q81, s);
-    if (dx) {
-        const int kt = (int)ceil_div(K, UP_COLS);
-        const dim3 grid((unsigned)a.nunits * (unsigned)kt);
-        if (f16) hipLaunchKernelGGL(lora_dx_kernel<true>, grid, dim3(LT), 0, s, a, kt);
-        else hipLaunchKernelGGL(lora_dx_kernel<false>, grid, dim3(LT), 0, s, a, kt);
-    }
+    if (R <= 16) launch_grads<1>(a, f16, q81, s);
+    else if (R <= 32) launch_grads<2>(a, f16, q81, s);
+    else launch_grads<4>(a, f16, q81, s);
     return hipGetLastError();
 }
 
