@@ -87,7 +87,7 @@ def lib() -> ctypes.CDLL:
     L.mmq_moe_combine.restype = e
     L.mmq_moe_combine_grad.argtypes = [e, P, I, P, I, e, P, P, I, I, I, I, P, I, P, P]
     L.mmq_moe_combine_grad.restype = e
-    L.mmq_lora_workspace_bytes.argtypes = [I, I, I, I]
+    L.mmq_lora_workspace_bytes.argtypes = [I, I, I, I, I]
     L.mmq_lora_workspace_bytes.restype = S
     L.mmq_lora.argtypes = [e, P, e, P, P, P, I, I, P, I, I, I, P, I, P, I, P, P, S, P]
     L.mmq_lora.restype = e
@@ -427,8 +427,8 @@ ADTYPE = {"bf16": 0, "f16": 1}
 
 
 @functools.lru_cache(maxsize=4096)
-def lora_workspace_bytes(E: int, M: int, K: int, R: int) -> int:
-    return int(lib().mmq_lora_workspace_bytes(E, M, K, R))
+def lora_workspace_bytes(E: int, M: int, N: int, K: int, R: int) -> int:
+    return int(lib().mmq_lora_workspace_bytes(E, M, N, K, R))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -478,12 +478,15 @@ def lora(act, A, B, scale, plan, M: int, atype="q8_1", base=None, out=None, v=No
     else:
         _flat(fn, "v", v, (M, R), torch.float32)
     if workspace is None:
-        workspace = _new(lora_workspace_bytes(E, M, K, R), torch.uint8, at, stream)
+        nbytes = lora_workspace_bytes(E, M, N, K, R)
+        if nbytes:
+            workspace = _new(nbytes, torch.uint8, at, stream)
     ldo = _ld(fn, "out", out, M, N, dt)
     ldb = _ld(fn, "base", base, M, N, dt) if base is not None else 0
     _check("mmq_lora", lib().mmq_lora(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
                                       plan.data_ptr(), M, N, K, _ptr(base), ldb, out.data_ptr(), ldo, v.data_ptr(),
-                                      workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, at)))
+                                      _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                                      _raw_stream(stream, at)))
     return out, v
 
 

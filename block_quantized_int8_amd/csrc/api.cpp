@@ -268,8 +268,8 @@ bool lora_sizes_ok(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
 }
 }  // namespace
 
-size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R) {
-    return lora_sizes_ok(E, M, 1, K, R) ? lora_workspace_bytes(E, M, K, R) : 0;
+size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    return lora_sizes_ok(E, M, N, K, R) ? lora_workspace_bytes(E, M, N, K, R) : 0;
 }
 
 mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B, const float* scale,
@@ -282,7 +282,8 @@ mmq_status mmq_lora(mmq_atype a, const void* act, mmq_adtype d, const void* A, c
     if (!aligned16(act) || !aligned16(A) || !aligned16(B) || !aligned16(scale) || !aligned16(plan) ||
         (base && !aligned16(base)) || !aligned16(out) || !aligned16(v))
         return MMQ_EALIGN;
-    if (!workspace || ws_bytes < lora_workspace_bytes(E, M, K, R)) return MMQ_EWORKSPACE;
+    const size_t need = lora_workspace_bytes(E, M, N, K, R);
+    if (need && (!workspace || ws_bytes < need)) return MMQ_EWORKSPACE;
     if (!aligned16(workspace)) return MMQ_EALIGN;
     return from_hip(launch_lora(a, d == MMQ_ADAPTER_F16, act, A, B, scale, E, R, plan, M, N, K, base, ldb, out, ldo,
                                 v, workspace, as_stream(stream)));

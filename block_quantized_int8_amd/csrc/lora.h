@@ -397,7 +397,7 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
     }
 }
 
-size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
+size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R);
 bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
                        int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const void* base,

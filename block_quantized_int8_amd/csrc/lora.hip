@@ -10,6 +10,7 @@
 //   2. s_e B_e v added to the base: lora_expand_kernel where K is not split (rows enough to fill the
 //      chip), from the terms of s_e v that the first launch leaves; lora_up_kernel otherwise, which
 //      sums the S parts in order and makes the terms itself.
+// For few rows lora_small_kernel does both in one launch.
 // Loops over rows stay loops: a launch fetches its code cold, and with the four row tiles
 // unrolled (25 KB of code) the second launch took 13.8 us on 517 x 1536 instead of 5.4.
 #include <algorithm>
@@ -22,41 +23,14 @@ namespace {
 constexpr int DW = 8;               // waves of a down workgroup
 constexpr int MAX_PARTS = 8;
 
-// Operand mapping: A = the adapter's rows r (lane c: rank r0 + 16i + c of tile i), B = the
+// acc += the adapter's rows (pieces at A + aoff) times one lane's activations over the blocks
+// [b0, b1), turned in the wave's own LDS.
+// Operand mapping: A = the adapter's rows r (lane c: rank 16i + c of tile i), B = the
 // activations (lane c: row c of the 16), so a lane ends with four consecutive ranks of a row.
 // NB blocks are loaded before the first is used.
-template <int RT, bool F16, bool Q81>
-__global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
-    constexpr int NB = RT == 1 ? 4 : 2;
-    __shared__ u32x4 lds[DW][NB * RT][64];      // each wave's pieces; the waves' sums at the end
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, g = lane >> 4;
-    // a unit's first 16 rows come first in the grid (units of few rows have no others); the part
-    // turns with the unit, so that no XCD's L2 gets the same columns of every row of the adapters
-    // (those are a few of its channels only: 14 us against 6.5 for 64 rows of 32 adapters)
-    const int at = (int)blockIdx.x / a.S, s = ((int)blockIdx.x + at) % a.S;
-    const int sub = at / a.nunits;
-    const int4 unit = a.units[at - sub * a.nunits];
-    const int rows = min(unit.z - 16 * sub, 16);
-    if (rows <= 0 || unit.x >= a.E) return;
-    const int p0 = unit.y + 16 * sub, r0 = (int)blockIdx.y * LORA_RC;
-
-    const int parts = a.S * DW, per = (a.KB + parts - 1) / parts;      // blocks of a wave
-    const int b0 = (s * DW + wave) * per, b1 = min(b0 + per, a.KB);
-    // rows past the unit's last repeat it; their columns are not stored. Ranks past R likewise.
-    const int m = a.order[p0 + min(c, rows - 1)];
-    const uint16_t* A = a.A + (int64_t)unit.x * a.R * a.K;
-    uint32_t aoff[RT];                          // R * K < 2^31 values
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-        aoff[i] = (uint32_t)min(r0 + 16 * i + piece_row(lane), a.R - 1) * (uint32_t)a.K + 8u * piece_of(lane);
-    const int64_t tile = (int64_t)(m >> 5) * a.KBp;
-    const int8_t* xrow = a.xq + tile * 1024 + ((g >> 1) * 32 + (m & 31)) * 16 + (g & 1) * 8;
-    const uint16_t* srow = reinterpret_cast<const uint16_t*>(a.xs2 + tile * 32 + (m & 31));
-
-    f32x4 acc[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i] = 0;
+template <int RT, int NB, bool F16, bool Q81>
+__device__ inline void down_blocks(const uint16_t* A, const uint32_t (&aoff)[RT], const int8_t* xrow, const uint16_t* srow,
+                                   int b0, int b1, u32x4 (*lds)[64], int lane, f32x4 (&acc)[RT]) {
 #pragma unroll 1
     for (int b = b0; b < b1; b += NB) {
         u32x4 w[NB][RT];
@@ -77,7 +51,7 @@ __global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) lds[wave][k * RT + i][lane] = w[k][i];
+            for (int i = 0; i < RT; ++i) lds[k * RT + i][lane] = w[k][i];
         wave_lds_fence();
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -85,7 +59,7 @@ __global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
             const u32x4 x = int8_operand<F16>(q[k]);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-                const u32x4 ww = lds[wave][k * RT + i][piece_at(lane)];
+                const u32x4 ww = lds[k * RT + i][piece_at(lane)];
                 const f32x4 from = Q81 ? f32x4(0) : acc[i];
                 const f32x4 d = F16 ? mfma_f16(ww, x, from) : mfma_bf16(ww, x, from);
                 if constexpr (Q81) {
@@ -99,6 +73,41 @@ __global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
         }
         wave_lds_fence();
     }
+}
+
+template <int RT, bool F16, bool Q81>
+__global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
+    constexpr int NB = RT == 1 ? 4 : 2;
+    __shared__ u32x4 lds[DW][NB * RT][64];      // each wave's pieces; the waves' sums at the end
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4;
+    // a unit's first 16 rows come first in the grid (units of few rows have no others); the part
+    // turns with the unit, so that no XCD's L2 gets the same columns of every row of the adapters
+    // (those are a few of its channels only: 14 us against 6.5 for 64 rows of 32 adapters)
+    const int at = (int)blockIdx.x / a.S, s = ((int)blockIdx.x + at) % a.S;
+    const int sub = at / a.nunits;
+    const int4 unit = a.units[at - sub * a.nunits];
+    const int rows = min(unit.z - 16 * sub, 16);
+    if (rows <= 0 || unit.x >= a.E) return;
+    const int p0 = unit.y + 16 * sub, r0 = (int)blockIdx.y * 16 * RT;
+
+    const int parts = a.S * DW, per = (a.KB + parts - 1) / parts;      // blocks of a wave
+    const int b0 = (s * DW + wave) * per, b1 = min(b0 + per, a.KB);
+    // rows past the unit's last repeat it; their columns are not stored. Ranks past R likewise.
+    const int m = a.order[p0 + min(c, rows - 1)];
+    const uint16_t* A = a.A + (int64_t)unit.x * a.R * a.K;
+    uint32_t aoff[RT];                          // R * K < 2^31 values
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+        aoff[i] = (uint32_t)min(r0 + 16 * i + piece_row(lane), a.R - 1) * (uint32_t)a.K + 8u * piece_of(lane);
+    const int64_t tile = (int64_t)(m >> 5) * a.KBp;
+    const int8_t* xrow = a.xq + tile * 1024 + ((g >> 1) * 32 + (m & 31)) * 16 + (g & 1) * 8;
+    const uint16_t* srow = reinterpret_cast<const uint16_t*>(a.xs2 + tile * 32 + (m & 31));
+
+    f32x4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = 0;
+    down_blocks<RT, NB, F16, Q81>(A, aoff, xrow, srow, b0, b1, lds[wave], lane, acc);
     // the waves' sums: wave i joins and stores tile i
 #pragma unroll
     for (int i = 0; i < RT; ++i) lds[wave][i][lane] = __builtin_bit_cast(u32x4, acc[i]);
@@ -266,6 +275,130 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
     }
 }
 
+// Both steps in one launch, for few rows: a workgroup has 16 of a unit's rows and 1024 columns, makes
+// v for itself (its sixteen waves share K) and multiplies. The adapters' A is read again for each
+// 1024 columns; a second launch and the parts' way through memory are saved.
+constexpr int SW = 16;              // waves
+constexpr int SMALL_COLS = 64 * SW;
+
+template <int RT, bool F16, bool Q81, bool TAIL>
+__global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int ntiles, int subs) {
+    constexpr int NB = RT == 1 ? 4 : 2, RK = RT == 4 ? 2 : 1, LD = 32 * RK + 8;
+    static_assert(NB * RT >= 4 * RK, "the columns' pieces use the blocks' memory");
+    constexpr bool BF16 = !Q81;
+    __shared__ u32x4 lds[SW][NB * RT][64];
+    __shared__ __attribute__((aligned(16))) uint16_t vt[3][16][LD];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4;
+    const int tile = (int)blockIdx.x % ntiles, us = (int)blockIdx.x / ntiles, u = us / subs, sub = us - u * subs;
+    const int4 unit = a.units[u];
+    const bool none = unit.x >= a.E;
+    const int64_t e = none ? 0 : unit.x;
+    const int n0 = tile * SMALL_COLS + 64 * wave, n = n0 + 4 * c, left = a.N - n;
+    // sixteen rows at a time; a unit's further ones where the grid has no workgroups for them
+#pragma unroll 1
+    for (int s0 = sub; 16 * s0 < unit.z; s0 += subs) {
+        const int rows = min(unit.z - 16 * s0, 16), p0 = unit.y + 16 * s0;
+        f32x4 acc[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = 0;
+        const int m = a.order[p0 + min(c, rows - 1)];
+        if (!none) {
+            const int per = (a.KB + SW - 1) / SW, b0 = wave * per, b1 = min(b0 + per, a.KB);
+            const uint16_t* A = a.A + e * a.R * a.K;
+            uint32_t aoff[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                aoff[i] = (uint32_t)min(16 * i + piece_row(lane), a.R - 1) * (uint32_t)a.K + 8u * piece_of(lane);
+            const int64_t cell = (int64_t)(m >> 5) * a.KBp;
+            const int8_t* xrow = a.xq + cell * 1024 + ((g >> 1) * 32 + (m & 31)) * 16 + (g & 1) * 8;
+            const uint16_t* srow = reinterpret_cast<const uint16_t*>(a.xs2 + cell * 32 + (m & 31));
+            down_blocks<RT, NB, F16, Q81>(A, aoff, xrow, srow, b0, b1, lds[wave], lane, acc);
+        }
+        // the columns' pieces and the base are on their way while the waves join
+        u32x4 raw[RK][4];
+        f32x4 base[4];
+        int to[4];
+        const uint16_t* B = a.B + (e * a.N + n0) * a.R;
+        const uint32_t col = 4u * piece_row(lane), last = (uint32_t)max(a.N - 1 - n0, 0);
+#pragma unroll
+        for (int k = 0; k < RK; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = 32u * k + 8u * piece_of(lane);
+                raw[k][i] = 0;
+                if (r < (uint32_t)a.R && n0 < a.N && !none)
+                    raw[k][i] = *reinterpret_cast<const u32x4*>(B + min(col + i, last) * (uint32_t)a.R + r);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = a.order[p0 + min(4 * g + j, rows - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            base[j] = 0;
+            if (a.base && left > 0) base[j] = load4<BF16>(a.base, to[j] * a.ldb + n, TAIL ? left : 4);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) lds[wave][i][lane] = __builtin_bit_cast(u32x4, acc[i]);
+        __syncthreads();
+        if (wave < 2 * RK) {                               // wave i: ranks 16i .., zeros past R
+            f32x4 d = 0;
+            const int r = 16 * wave + 4 * g;
+            if (wave < RT && r < a.R) {
+#pragma unroll
+                for (int w = 0; w < SW; ++w) d += __builtin_bit_cast(f32x4, lds[w][wave][lane]);
+                if constexpr (!Q81) d *= a.sa[m];
+                if (tile == 0 && c < rows) *reinterpret_cast<f32x4*>(a.v + (int64_t)m * a.R + r) = d;
+            }
+            store_terms(&vt[0][c][r], 16 * LD, d);
+        }
+        __syncthreads();
+        if (n0 < a.N) {
+            const float scale = none ? 0.f : a.scale[e];
+            f32x4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = 0;
+#pragma unroll
+            for (int k = 0; k < RK; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lds[wave][4 * k + i][lane] = raw[k][i];
+            wave_lds_fence();
+            if (!none)
+#pragma unroll
+                for (int k = 0; k < RK; ++k) {
+                    u32x4 x[3];
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) x[j] = *reinterpret_cast<const u32x4*>(&vt[j][c][32 * k + 8 * g]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        Weights<F16> w;
+                        w.set(lds[wave][4 * k + i][piece_at(lane)]);
+                        o[i] = terms_mfma<F16>(x, w, o[i]);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (left > 0 && 4 * g + j < rows) {
+                    f32x4 d = base[j];
+                    if (!none)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = fmaf(scale, o[i][j], d[i]);
+                    store4<BF16>(a.out, to[j] * a.ldo + n, d, TAIL ? left : 4);
+                }
+        }
+        __syncthreads();
+    }
+}
+
+// One launch while the adapters' A, read again for each 1024 columns of each 16 rows, come to 32 MB at
+// most: it saves the host 4 us a call. Measured: one row 4096 x 4096, rank 16: 7.1 us against 4.2 +
+// 4.9 in two launches; 517 rows of 6 adapters 1536 x 4096, rank 24 (15 MB): 10.4 against 4.8 + 5.4;
+// 64 rows of 32 adapters 14336 x 4096, rank 32 (132 MB): 34 against 6.0 + 11.7.
+bool small_call(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    const int64_t tiles = ceil_div(M, 16) + std::min(E, M);
+    return R <= 64 && K * R <= (int64_t(1) << 18) && tiles * ceil_div(N, SMALL_COLS) * K * R <= (int64_t(1) << 24);
+}
+
 // Parts that K is split into: a power of two that gives up to 768 workgroups, a block a wave at
 // least.
 int64_t down_parts(int64_t E, int64_t M, int64_t K) {
@@ -277,10 +410,25 @@ int64_t down_parts(int64_t E, int64_t M, int64_t K) {
 
 template <bool F16, bool Q81>
 void launch_down(const LoraArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.nunits * 4 * a.S, (unsigned)ceil_div(a.R, LORA_RC));
-    if (a.R <= 16) hipLaunchKernelGGL((lora_down_kernel<1, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((lora_down_kernel<2, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+    const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
+    const dim3 grid((unsigned)a.nunits * 4 * a.S, (unsigned)ceil_div(a.R, 16 * rt));
+    if (rt == 1) hipLaunchKernelGGL((lora_down_kernel<1, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+    else if (rt == 2) hipLaunchKernelGGL((lora_down_kernel<2, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
     else hipLaunchKernelGGL((lora_down_kernel<4, F16, Q81>), grid, dim3(DW * 64), 0, s, a);
+}
+
+template <bool F16, bool Q81, bool TAIL>
+void launch_small(const LoraArgs& a, hipStream_t s) {
+    const int ntiles = (int)ceil_div(a.N, SMALL_COLS), subs = a.M > 16 ? 4 : 1;
+    const dim3 grid((unsigned)(a.nunits * subs * ntiles)), th(SW * 64);
+    if (a.R <= 16) hipLaunchKernelGGL((lora_small_kernel<1, F16, Q81, TAIL>), grid, th, 0, s, a, ntiles, subs);
+    else if (a.R <= 32) hipLaunchKernelGGL((lora_small_kernel<2, F16, Q81, TAIL>), grid, th, 0, s, a, ntiles, subs);
+    else hipLaunchKernelGGL((lora_small_kernel<4, F16, Q81, TAIL>), grid, th, 0, s, a, ntiles, subs);
+}
+template <bool F16, bool Q81>
+void launch_small(const LoraArgs& a, hipStream_t s) {
+    if (a.N % 4) launch_small<F16, Q81, true>(a, s);
+    else launch_small<F16, Q81, false>(a, s);
 }
 
 template <bool F16, bool BF16, bool TAIL>
@@ -308,7 +456,8 @@ void launch_up(const LoraArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R) {
+size_t lora_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
+    if (small_call(E, M, N, K, R)) return 0;
     const int64_t S = down_parts(E, M, K);
     return (size_t)round_up(M * R * (S > 1 ? 4 * S : 6), REGION_ALIGN);      // f32 parts, or three bf16 planes
 }
@@ -333,6 +482,11 @@ hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, co
     a.ldo = ldo;
     a.v = v;
     const bool q81 = t == MMQ_ACT_Q8_1;
+    if (small_call(E, M, N, K, R)) {
+        if (f16) q81 ? launch_small<true, true>(a, s) : launch_small<true, false>(a, s);
+        else q81 ? launch_small<false, true>(a, s) : launch_small<false, false>(a, s);
+        return hipGetLastError();
+    }
     if (f16) q81 ? launch_down<true, true>(a, s) : launch_down<true, false>(a, s);
     else q81 ? launch_down<false, true>(a, s) : launch_down<false, false>(a, s);
     hipError_t e = hipGetLastError();

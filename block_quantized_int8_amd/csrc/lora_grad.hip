@@ -364,7 +364,9 @@ __global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int kti
     const int block = (int)blockIdx.x - na, u = block / ktiles;
     const int4 unit = a.units[u];
     if (unit.z == 0) return;
-    expand_body<true, F16, false, false, GW>(a, a.A, a.K, a.dxb, a.lddxb, a.dx, a.lddx, unit, block - u * ktiles, lds.x);
+    // the columns turn with the unit, so that an XCD's L2 sees all of its channels
+    expand_body<true, F16, false, false, GW>(a, a.A, a.K, a.dxb, a.lddxb, a.dx, a.lddx, unit,
+                                             (block - u * ktiles + u) % ktiles, lds.x);
 }
 
 constexpr int DX_COLS = 16 * GW;                           // columns of a dx workgroup

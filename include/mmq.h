@@ -331,9 +331,9 @@ mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const
  * --------------------------------------------------------------------------------------- */
 typedef enum { MMQ_ADAPTER_BF16 = 0, MMQ_ADAPTER_F16 = 1 } mmq_adtype;
 
-/* Workspace bytes of mmq_lora for E adapters of rank R and M rows; 0 if the arguments are invalid
- * (see mmq_lora). (host) */
-size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
+/* Workspace bytes of mmq_lora for E adapters of rank R and M rows; 0 if the call needs none (few
+ * rows), or if the arguments are invalid (see mmq_lora). (host) */
+size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R);
 
 /* The forward call.
  *  act   (device) of M rows and K columns, as mmq_quantize_act(a, ...) writes it
@@ -347,8 +347,8 @@ size_t mmq_lora_workspace_bytes(int64_t E, int64_t M, int64_t K, int64_t R);
  *        writes for these activations (base has the same type). Columns past N are left
  *        untouched.
  *  v     (device) f32 [M][R], written whole: the backward call needs it
- *  workspace (device) >= mmq_lora_workspace_bytes(E, M, K, R) bytes; needs no initialisation. Two
- *        calls that overlap in time must not share one.
+ *  workspace (device) >= mmq_lora_workspace_bytes(E, M, N, K, R) bytes (NULL if that is 0); needs
+ *        no initialisation. Two calls that overlap in time must not share one.
  * R is a multiple of 8, at most 256; K a multiple of 32; 1 <= E <= 4096. The strides are in
  * elements, >= N, and need no alignment. MMQ_EINVAL also where ceil(N/64) or ceil(K/64)
  * workgroups for each of the plan's units reach 2^24. */

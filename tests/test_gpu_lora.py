@@ -239,8 +239,10 @@ def test_binding_refusals(env):
         mmq.lora(act, A, B, scale, plan, M, base=torch.zeros((M, N), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError, match="out"):
         mmq.lora(act, A, B, scale, plan, M, out=torch.zeros((M, N + 1), device="cuda"))
+    assert mmq.lora_workspace_bytes(E, M, N, K, R) == 0            # few rows: no workspace
+    A2, B2, _ = (t.cuda() for t in adapters(torch, "bf16", E, 72, K, N, 1))
     with pytest.raises(mmq.MMQError) as err:
-        mmq.lora(act, A, B, scale, plan, M, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+        mmq.lora(act, A2, B2, scale, plan, M, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert err.value.code == mmq.MMQ_EWORKSPACE
     with pytest.raises(mmq.MMQError) as err:                       # a rank that is no multiple of 8
         mmq.lora(act, A[:, :7].contiguous(), B[:, :, :7].contiguous(), scale, plan, M)

@@ -24,16 +24,16 @@ SIZES_REFUSED = [dict(E=0), dict(E=4097), dict(M=0), dict(M=(1 << 24) + 1), dict
 
 @pytest.mark.parametrize("bad", SIZES_REFUSED)
 def test_workspace_sizes_refused(mmq, bad):
-    k = dict(E=4, M=100, K=512, R=16)
-    assert mmq.lora_workspace_bytes(**k) >= 100 * 16 * 4
+    k = dict(E=4, M=4000, N=4096, K=4096, R=64)
+    assert mmq.lora_workspace_bytes(**k) >= 4000 * 64 * 4
     k.update(bad)
     assert mmq.lora_workspace_bytes(**k) == 0
 
 
-def _lora(mmq, a=0, act=GOOD, d=0, A=GOOD, B=GOOD, scale=GOOD, E=4, R=16, plan=GOOD, M=100, N=64, K=512, base=GOOD,
-          ldb=64, out=GOOD, ldo=64, v=GOOD, ws=GOOD, nbytes=None):
+def _lora(mmq, a=0, act=GOOD, d=0, A=GOOD, B=GOOD, scale=GOOD, E=4, R=64, plan=GOOD, M=4000, N=4096, K=4096, base=GOOD,
+          ldb=4096, out=GOOD, ldo=4096, v=GOOD, ws=GOOD, nbytes=None):
     if nbytes is None:
-        nbytes = mmq.lora_workspace_bytes(E, M, K, R) - 1         # one short: nothing is ever enqueued
+        nbytes = mmq.lora_workspace_bytes(E, M, N, K, R) - 1      # one short: nothing is ever enqueued
     return mmq.lib().mmq_lora(a, act, d, A, B, scale, E, R, plan, M, N, K, base, ldb, out, ldo, v, ws, max(nbytes, 0), None)
 
 
@@ -45,11 +45,11 @@ def test_lora_refusals(mmq):
         assert _lora(mmq, **{p: None}) == mmq.MMQ_EINVAL, p
         assert _lora(mmq, **{p: BAD}) == mmq.MMQ_EALIGN, p
     assert _lora(mmq, base=BAD) == mmq.MMQ_EALIGN
-    for bad in SIZES_REFUSED + [dict(a=2), dict(a=-1), dict(d=2), dict(N=0), dict(N=65), dict(ldb=63), dict(ldo=63),
-                                dict(ldb=65), dict(N=1 << 24, M=1 << 24, ldb=1 << 24, ldo=1 << 24)]:
+    for bad in SIZES_REFUSED + [dict(a=2), dict(a=-1), dict(d=2), dict(N=0), dict(N=4097), dict(ldb=4095),
+                                dict(ldo=4095), dict(ldb=4097), dict(N=1 << 24, M=1 << 24, ldb=1 << 24, ldo=1 << 24)]:
         assert _lora(mmq, **bad) == mmq.MMQ_EINVAL, bad
     # a base of another stride is fine unless it is the output itself; no base needs no stride
-    assert _lora(mmq, base=ctypes.c_void_p(0x20000), ldb=65) == mmq.MMQ_EWORKSPACE
+    assert _lora(mmq, base=ctypes.c_void_p(0x20000), ldb=4097) == mmq.MMQ_EWORKSPACE
     assert _lora(mmq, base=None, ldb=0) == mmq.MMQ_EWORKSPACE
 
 
