@@ -152,30 +152,44 @@ template <bool F16> __device__ inline u32x4 int8_operand(u32x2 q) {
     return r;
 }
 
-// Four values of a row of the output's type from column n on, as f32 (columns past N read 0).
-template <bool BF16> __device__ inline f32x4 load4(const void* p, int64_t at, int left) {
-    f32x4 r = 0;
-    if constexpr (BF16) {
-        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-        if (left >= 4) {
-            const u32x2 w = *reinterpret_cast<const u32x2_any*>(q);
+// Four values of an f32 or bf16 row, as they lie in memory: a load that is turned into f32 at once
+// has to be waited for at once.
+template <bool BF16> struct Quad { typedef f32x4 Raw; };
+template <> struct Quad<true> { typedef u32x2 Raw; };
+template <bool BF16> __device__ inline typename Quad<BF16>::Raw load_quad(const void* p, int64_t at) {
+    if constexpr (BF16) return *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(p) + at);
+    else return *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + at);
+}
+// At a row's end a quad is loaded from the last place that is whole, n - off, and what lies before n
+// is dropped once it is used (zeros come in behind it): no lane takes a branch of its own, in which
+// it would wait for its load. Rows of less than four values are loaded value by value.
+struct QuadEnd {
+    int at, off;
+    __device__ QuadEnd(int n, int N) : at(N < 4 ? n : min(n, N - 4)), off(n - at) {}
+};
+template <bool BF16> __device__ inline typename Quad<BF16>::Raw load_quad_end(const void* p, int64_t row, QuadEnd q, int N) {
+    if (N >= 4) return load_quad<BF16>(p, row + q.at);
+    typename Quad<BF16>::Raw r = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = as_f(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) r[j] = as_f((uint32_t)q[j] << 16);
+    for (int j = 0; j < 3; ++j)
+        if (q.at + j < N) {
+            if constexpr (BF16) r[j / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[row + q.at + j] << (16 * (j & 1));
+            else r[j] = static_cast<const float*>(p)[row + q.at + j];
         }
-    } else {
-        const float* q = static_cast<const float*>(p) + at;
-        if (left >= 4) r = *reinterpret_cast<const f32x4_any*>(q);
-        else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < left) r[j] = q[j];
-        }
-    }
     return r;
+}
+__device__ inline u32x2 drop_quad(u32x2 r, int off) {
+    const uint64_t v = off < 4 ? __builtin_bit_cast(uint64_t, r) >> (16 * off) : 0;
+    return __builtin_bit_cast(u32x2, v);
+}
+__device__ inline f32x4 drop_quad(f32x4 r, int off) {
+    if (off & 1) r = f32x4{r[1], r[2], r[3], 0.f};
+    if (off & 2) r = f32x4{r[2], r[3], 0.f, 0.f};
+    return off < 4 ? r : f32x4(0);
+}
+__device__ inline f32x4 quad_f32(f32x4 r) { return r; }
+__device__ inline f32x4 quad_f32(u32x2 r) {
+    return f32x4{as_f(r[0] << 16), as_f(r[0] & 0xFFFF0000u), as_f(r[1] << 16), as_f(r[1] & 0xFFFF0000u)};
 }
 
 template <bool BF16> __device__ inline void store4(void* p, int64_t at, f32x4 v, int left) {
@@ -305,7 +319,7 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = 0;
-    f32x4 base[4];
+    typename Quad<BF16>::Raw base[4];
 #pragma unroll 1
     for (int r0 = 0; r0 < a.R; r0 += LORA_RC) {
         const int rc = min(a.R - r0, LORA_RC);
@@ -347,7 +361,8 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
                     for (int i = 0; i < 4; ++i)
                         if (n0 + 16 * i < C) base[j][i] = p[16 * i];
                 } else {
-                    if (n < C) base[j] = load4<BF16>(base_, m[j] * ldb + n, TAIL ? C - n : 4);
+                    if constexpr (TAIL) base[j] = load_quad_end<BF16>(base_, m[j] * ldb, QuadEnd(n, C), C);
+                    else if (n < C) base[j] = load_quad<BF16>(base_, m[j] * ldb + n);
                 }
             }
         } else {
@@ -389,7 +404,7 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
             for (int i = 0; i < 4; ++i)
                 if (n0 + 16 * i < C) p[16 * i] = base[j][i] + acc[i][j];
         } else if (n < C) {
-            f32x4 o = base[j];
+            f32x4 o = quad_f32(TAIL ? drop_quad(base[j], QuadEnd(n, C).off) : base[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] += acc[i][j];
             store4<BF16>(out, m[j] * ldo + n, o, TAIL ? C - n : 4);

@@ -224,11 +224,15 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
     const float scale = none ? 0.f : a.scale[unit.x];
 #pragma unroll 1
     for (int t = t0; t < nt; t += tall ? 4 : 1) {
-        f32x4 base[4], acc[4];
+        typename Quad<BF16>::Raw base[4];
+        f32x4 acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            acc[j] = base[j] = 0;
-            if (a.base && left > 0) base[j] = load4<BF16>(a.base, m[j] * a.ldb + n, TAIL ? left : 4);
+            acc[j] = 0;
+            base[j] = 0;
+            if (!a.base) continue;
+            if constexpr (TAIL) base[j] = load_quad_end<BF16>(a.base, m[j] * a.ldb, QuadEnd(n, a.N), a.N);
+            else if (left > 0) base[j] = load_quad<BF16>(a.base, m[j] * a.ldb + n);
         }
         __builtin_amdgcn_sched_barrier(0);
         wave_lds_fence();
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (left > 0 && 16 * t + 4 * g + j < unit.z) {
-                f32x4 o = base[j];
+                f32x4 o = quad_f32(TAIL ? drop_quad(base[j], QuadEnd(n, a.N).off) : base[j]);
                 if (!none)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = fmaf(scale, acc[i][j], o[i]);
@@ -317,7 +321,7 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
         }
         // the columns' pieces and the base are on their way while the waves join
         u32x4 raw[RK][4];
-        f32x4 base[4];
+        typename Quad<BF16>::Raw base[4];
         int to[4];
         const uint16_t* B = a.B + (e * a.N + n0) * a.R;
         const uint32_t col = 4u * piece_row(lane), last = (uint32_t)max(a.N - 1 - n0, 0);
@@ -335,7 +339,9 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             base[j] = 0;
-            if (a.base && left > 0) base[j] = load4<BF16>(a.base, to[j] * a.ldb + n, TAIL ? left : 4);
+            if (!a.base) continue;
+            if constexpr (TAIL) base[j] = load_quad_end<BF16>(a.base, to[j] * a.ldb, QuadEnd(n, a.N), a.N);
+            else if (left > 0) base[j] = load_quad<BF16>(a.base, to[j] * a.ldb + n);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -379,7 +385,7 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (left > 0 && 4 * g + j < rows) {
-                    f32x4 d = base[j];
+                    f32x4 d = quad_f32(TAIL ? drop_quad(base[j], QuadEnd(n, a.N).off) : base[j]);
                     if (!none)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) d[i] = fmaf(scale, o[i][j], d[i]);

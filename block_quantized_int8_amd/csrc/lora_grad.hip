@@ -56,16 +56,6 @@ template <int T> __device__ inline f32x4 mfma_3(const u32x4* a, const u32x4* b, 
 
 constexpr int GW = 8;               // waves of a workgroup of either launch
 
-// Eight bf16 values of a row, zeros from `left` on.
-__device__ inline u32x4 load8(const uint16_t* p, int left) {
-    if (left >= 8) return *reinterpret_cast<const u32x4_any*>(p);
-    u32x4 r = 0;
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < left) r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    return r;
-}
-
 template <int RT> struct RankVec;
 template <> struct RankVec<1> { typedef float V; };
 template <> struct RankVec<2> { typedef f32x2 V; };
@@ -160,14 +150,27 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
 #pragma unroll
             for (int i = 0; i < RT; ++i)
                 w[k][i] = *reinterpret_cast<const u32x4*>(B + (int64_t)min(n + (int)brow[i], a.N - 1) * a.R + bcol[i]);
-            if constexpr (BF16) {
-                const int nn = n + 8 * piece_of(lane);
-                x[k][0] = load8(static_cast<const uint16_t*>(a.dy) + row + nn, a.N - nn);
+            // (bf16: values 8p .. 8p+7 of piece p; f32: 4p .. and 16 + 4p ..)
+            if (n + 32 <= a.N) {
+                if constexpr (BF16) {
+                    x[k][0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(a.dy) + row + n + 8 * piece_of(lane));
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        x[k][h] = __builtin_bit_cast(u32x4, load_quad<false>(a.dy, row + n + 16 * h + 4 * piece_of(lane)));
+                }
             } else {
+                typename Quad<BF16>::Raw q[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int nn = n + 16 * h + 4 * piece_of(lane);
-                    x[k][h] = __builtin_bit_cast(u32x4, load4<false>(a.dy, row + nn, a.N - nn));
+                    const QuadEnd at(n + (BF16 ? 8 * piece_of(lane) + 4 * h : 16 * h + 4 * piece_of(lane)), a.N);
+                    q[h] = drop_quad(load_quad_end<BF16>(a.dy, row, at, a.N), at.off);
+                }
+                if constexpr (BF16) {
+                    x[k][0] = u32x4{q[0][0], q[0][1], q[1][0], q[1][1]};
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) x[k][h] = __builtin_bit_cast(u32x4, q[h]);
                 }
             }
         }
@@ -230,15 +233,21 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
         int m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) m[j] = a.order[min(p + 8 * g + j, p1 - 1)];
-        f32x4 x[8];
+        typename Quad<BF16>::Raw x[8];
         V v[8];
+        if (n0 + 64 <= a.N) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = 0;
-            if (n < a.N) x[j] = load4<BF16>(a.dy, m[j] * a.lddy + n, a.N - n);
-            v[j] = *reinterpret_cast<const V*>(vr + (int64_t)m[j] * a.R);
+            for (int j = 0; j < 8; ++j) x[j] = load_quad<BF16>(a.dy, m[j] * a.lddy + n);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = load_quad_end<BF16>(a.dy, m[j] * a.lddy, QuadEnd(n, a.N), a.N);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const V*>(vr + (int64_t)m[j] * a.R);
         __builtin_amdgcn_sched_barrier(0);
+        if (n0 + 64 > a.N)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = drop_quad(x[j], QuadEnd(n, a.N).off);
         u32x4 t[RT][3];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -248,7 +257,7 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
         for (int k = 0; k < 4; ++k) {
             float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = x[j][k];
+            for (int j = 0; j < 8; ++j) f[j] = quad_f32(x[j])[k];
             Grad<BF16> d;
             d.set(f);
 #pragma unroll
