@@ -296,7 +296,7 @@ bool lora_grad_sizes_ok(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
 }  // namespace
 
 size_t mmq_lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K, int64_t R) {
-    return lora_grad_sizes_ok(E, M, N, K, R) ? lora_grad_workspace_bytes(M, R) : 0;
+    return lora_grad_sizes_ok(E, M, N, K, R) ? lora_grad_workspace_bytes(E, M, N, R) : 0;
 }
 
 mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B, const float* scale,
@@ -312,7 +312,7 @@ mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void*
         !aligned16(dy) || (dx_base && !aligned16(dx_base)) || (dx && !aligned16(dx)) || !aligned16(dA) ||
         !aligned16(dB))
         return MMQ_EALIGN;
-    if (!workspace || ws_bytes < lora_grad_workspace_bytes(M, R)) return MMQ_EWORKSPACE;
+    if (!workspace || ws_bytes < lora_grad_workspace_bytes(E, M, N, R)) return MMQ_EWORKSPACE;
     if (!aligned16(workspace)) return MMQ_EALIGN;
     return from_hip(launch_lora_grad(a, d == MMQ_ADAPTER_F16, act, A, B, scale, E, R, plan, M, N, K, v, dy, lddy,
                                      dx_base, ldxb, dx, lddx, dA, dB, workspace, as_stream(stream)));

@@ -417,7 +417,7 @@ bool lora_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
                        int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const void* base,
                        int64_t ldb, void* out, int64_t ldo, float* v, void* ws, hipStream_t s);
-size_t lora_grad_workspace_bytes(int64_t M, int64_t R);
+size_t lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t R);
 bool lora_grad_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,
                             int64_t E, int64_t R, const void* plan, int64_t M, int64_t N, int64_t K, const float* v,

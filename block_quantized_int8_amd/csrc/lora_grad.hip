@@ -75,15 +75,6 @@ template <int RT> __device__ inline void rank_operands(const typename RankVec<RT
     }
 }
 
-template <int RT> __device__ inline void store_ranks(float* p, const float* d) {
-    typename RankVec<RT>::V v;
-    if constexpr (RT == 1) v = d[0];
-    else
-#pragma unroll
-        for (int i = 0; i < RT; ++i) v[i] = d[i];
-    *reinterpret_cast<typename RankVec<RT>::V*>(p) = v;
-}
-
 // Joins the waves' NT accumulators; wave w is left with the tiles w, w + GW, ... .
 template <int NT> using JoinLds = f32x4[GW / 2][NT][64];
 template <int NT> __device__ inline void join_waves(JoinLds<NT>& red, f32x4* acc, int wave, int lane) {
@@ -108,7 +99,15 @@ template <int NT> __device__ inline void join_waves(JoinLds<NT>& red, f32x4* acc
 }
 
 // ------------------------------------------------------------------------------ launch 1
-// u of 16 rows. Each wave turns its blocks of 32 columns in LDS of its own: dy's rows (as terms)
+constexpr int MAX_U_PARTS = 8;
+
+// four ranks of a row's u, in f32 and as terms
+__device__ inline void keep_u(const LoraArgs& a, int pos, int r, f32x4 d) {
+    *reinterpret_cast<f32x4*>(a.u + (int64_t)pos * a.R + r) = d;
+    store_terms(plane_at(a, pos, r), (int64_t)a.M * a.R, d);
+}
+
+// u of 16 rows, over one of S parts of N. Each wave turns its blocks of 32 columns in LDS of its own: dy's rows (as terms)
 // into the B operand, B_e's rows of ranks into the A operand.
 template <int RT, bool F16, bool BF16> struct ULds {
     uint16_t dy[Grad<BF16>::T][16][40];
@@ -120,8 +119,8 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
     constexpr int NB = 2, T = Weights<F16>::T;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int sub = block / a.nunits;                      // a unit's first 16 rows come first
-    const int4 unit = a.units[block - sub * a.nunits];
+    const int at = block / a.S, s = block - at * a.S, sub = at / a.nunits;     // a unit's first 16 rows come first
+    const int4 unit = a.units[at - sub * a.nunits];
     const int rows = min(unit.z - 16 * sub, 16);
     if (rows <= 0 || unit.x >= a.E) return;
     const int p0 = unit.y + 16 * sub, per_row = min(a.R - r0, LORA_RC) / 8;     // pieces of a row of B_e
@@ -139,8 +138,8 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
     f32x4 acc[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[i] = 0;
-    const int blocks = (a.N + 31) / 32, per = (blocks + GW - 1) / GW;
-    const int b0 = wave * per, b1 = min(b0 + per, blocks);
+    const int blocks = (a.N + 31) / 32, per = (blocks + GW * a.S - 1) / (GW * a.S);
+    const int b0 = (s * GW + wave) * per, b1 = min(b0 + per, blocks);
 #pragma unroll 1
     for (int b = b0; b < b1; b += NB) {
         u32x4 x[NB][BF16 ? 1 : 2], w[NB][RT];
@@ -209,27 +208,46 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
     join_waves<RT>(red, acc, wave, lane);
     const int r = r0 + 16 * wave + 4 * g;
     if (wave >= RT || c >= rows || r >= a.R) return;
-    const f32x4 d = acc[0] * a.scale[unit.x];
-    *reinterpret_cast<f32x4*>(a.u + (int64_t)(p0 + c) * a.R + r) = d;
-    store_terms(plane_at(a, p0 + c, r), (int64_t)a.M * a.R, d);
+    if (a.S > 1) *reinterpret_cast<f32x4*>(a.part + ((int64_t)s * a.M + p0 + c) * a.R + r) = acc[0];
+    else keep_u(a, p0 + c, r, acc[0] * a.scale[unit.x]);
+}
+
+// u from its parts, in order: a workgroup per unit.
+__global__ __launch_bounds__(LT) void lora_join_kernel(LoraArgs a) {
+    const int4 unit = a.units[blockIdx.x];
+    if (unit.z == 0 || unit.x >= a.E) return;
+    const float scale = a.scale[unit.x];
+    for (int i = 4 * threadIdx.x; i < unit.z * a.R; i += 4 * LT) {
+        const float* p = a.part + (int64_t)unit.y * a.R + i;
+        f32x4 v[MAX_U_PARTS], d = 0;
+#pragma unroll
+        for (int s = 0; s < MAX_U_PARTS; ++s)
+            if (s < a.S) v[s] = *reinterpret_cast<const f32x4*>(p + (int64_t)s * a.M * a.R);
+#pragma unroll
+        for (int s = 0; s < MAX_U_PARTS; ++s)
+            if (s < a.S) d += v[s];
+        keep_u(a, unit.y + i / a.R, i % a.R, d * scale);
+    }
 }
 
 // dB_e[n][r] over all rows of adapter e: 64 columns n and up to 64 ranks, the waves every eighth 32
-// rows. Both operands come straight from memory: a lane loads four consecutive columns (RT
+// rows; `alone` (adapters of few rows): 64 columns and all rows a wave, nothing to join. Both operands come straight from memory: a lane loads four consecutive columns (RT
 // consecutive ranks) of eight rows, which are its k.
 template <int RT, bool BF16>
-__device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles, JoinLds<4 * RT>& red) {
+__device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles, bool alone, JoinLds<4 * RT>& red) {
     typedef typename RankVec<RT>::V V;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int e = block / ntiles, n0 = (block - e * ntiles) * 64, n = n0 + 4 * c;
-    const int p0 = a.offs[e], p1 = a.offs[e + 1];
+    const int e = block / ntiles, tile0 = block - e * ntiles;
+    const int n0 = 64 * (alone ? GW * tile0 + wave : tile0), n = n0 + 4 * c;
+    const int p0 = a.offs[e], p1 = a.offs[e + 1], step = alone ? 32 : 32 * GW;
+    if (alone && n0 >= a.N) return;
     const float* vr = a.v + min(r0 + RT * c, a.R - RT);
     f32x4 acc[4 * RT];
 #pragma unroll
     for (int i = 0; i < 4 * RT; ++i) acc[i] = 0;
 #pragma unroll 1
-    for (int p = p0 + 32 * wave; p < p1; p += 32 * GW) {
+    for (int p = p0 + (alone ? 0 : 32 * wave); p < p1; p += step) {
         int m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) m[j] = a.order[min(p + 8 * g + j, p1 - 1)];
@@ -265,8 +283,23 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
         }
     }
     // rows of the accumulators: ranks r0 + RT (4g + j) + i; column: n0 + 4c + k
-    join_waves<4 * RT>(red, acc, wave, lane);
     const float scale = a.scale[e];
+    if (alone) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = r0 + RT * (4 * g + j);
+                V d;
+                if constexpr (RT == 1) d = acc[k][j] * scale;
+                else
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) d[i] = acc[k * RT + i][j] * scale;
+                if (n + k < a.N && r < a.R) *reinterpret_cast<V*>(a.dB + ((int64_t)e * a.N + n + k) * a.R + r) = d;
+            }
+        return;
+    }
+    join_waves<4 * RT>(red, acc, wave, lane);
 #pragma unroll
     for (int q = 0; q < (4 * RT + GW - 1) / GW; ++q) {
         const int tile = wave + GW * q, k = tile / RT, i = tile % RT;
@@ -280,20 +313,20 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
 }
 
 template <int RT, bool F16, bool BF16>
-__global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, int ntiles) {
+__global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, int ntiles, int alone) {
     __shared__ __attribute__((aligned(16))) union {
         struct { ULds<RT, F16, BF16> turn[GW]; } u;
         JoinLds<RT> ju;
         JoinLds<4 * RT> jb;
     } lds;
-    const int r0 = (int)blockIdx.y * LORA_RC, nu = 4 * a.nunits;
+    const int r0 = (int)blockIdx.y * LORA_RC, nu = 4 * a.nunits * a.S;
     if ((int)blockIdx.x < nu) u_body<RT, F16, BF16>(a, (int)blockIdx.x, r0, lds.u.turn, lds.ju);
-    else dB_body<RT, BF16>(a, (int)blockIdx.x - nu, r0, ntiles, lds.jb);
+    else dB_body<RT, BF16>(a, (int)blockIdx.x - nu, r0, ntiles, alone != 0, lds.jb);
 }
 
 // ------------------------------------------------------------------------------ launch 2
 // dA_e[r][k] over all rows of adapter e: one block of K and up to 64 ranks, the waves every eighth
-// 32 rows. A wave loads the 32 rows' 1 KB of the block (16 bytes a lane), turns them in LDS as
+// 32 rows; `alone`: one block and all rows a wave. A wave loads the 32 rows' 1 KB of the block (16 bytes a lane), turns them in LDS as
 // bf16, and scales u by the rows' block scales.
 struct ALds {
     uint16_t x[32][40];
@@ -301,19 +334,21 @@ struct ALds {
 };
 
 template <int RT, bool Q81>
-__device__ inline void dA_body(const LoraArgs& a, int block, int r0, ALds* turn, JoinLds<2 * RT>& red) {
+__device__ inline void dA_body(const LoraArgs& a, int block, int r0, int kblocks, bool alone, ALds* turn,
+                               JoinLds<2 * RT>& red) {
     typedef typename RankVec<RT>::V V;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int e = block / a.KB, b = block - e * a.KB;
-    const int p0 = a.offs[e], p1 = a.offs[e + 1];
+    const int e = block / kblocks, b = alone ? GW * (block - e * kblocks) + wave : block - e * kblocks;
+    const int p0 = a.offs[e], p1 = a.offs[e + 1], step = alone ? 32 : 32 * GW;
+    if (alone && b >= a.KB) return;
     const float* ur = a.u + min(r0 + RT * c, a.R - RT);
     ALds& mine = turn[wave];
     f32x4 acc[2 * RT];
 #pragma unroll
     for (int i = 0; i < 2 * RT; ++i) acc[i] = 0;
 #pragma unroll 1
-    for (int p = p0 + 32 * wave; p < p1; p += 32 * GW) {
+    for (int p = p0 + (alone ? 0 : 32 * wave); p < p1; p += step) {
         const int row = lane & 31, m = a.order[min(p + row, p1 - 1)];
         V u[8];
 #pragma unroll
@@ -347,26 +382,39 @@ __device__ inline void dA_body(const LoraArgs& a, int block, int r0, ALds* turn,
             }
     }
     // rows of the accumulators: ranks r0 + RT (4g + j) + i; column: k = 32b + 16h + c
+    float* to = a.dA + (int64_t)e * a.R * a.K + 32 * b + c;
+    if (alone) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = r0 + RT * (4 * g + j) + i;
+                if (r >= a.R) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) to[(int64_t)r * a.K + 16 * h] = acc[h * RT + i][j];
+            }
+        return;
+    }
     join_waves<2 * RT>(red, acc, wave, lane);
     if (wave >= 2 * RT) return;
     const int h = wave / RT, i = wave % RT;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int r = r0 + RT * (4 * g + j) + i;
-        if (r < a.R) a.dA[((int64_t)e * a.R + r) * a.K + 32 * b + 16 * h + c] = acc[0][j];
+        if (r < a.R) to[(int64_t)r * a.K + 16 * h] = acc[0][j];
     }
 }
 
 template <int RT, bool F16, bool Q81>
-__global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int ktiles) {
+__global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int ktiles, int kblocks, int alone) {
     __shared__ __attribute__((aligned(16))) union {
         ALds turn[GW];
         JoinLds<2 * RT> ja;
         ExpandLds<true, F16, GW> x;
     } lds;
-    const int na = a.E * a.KB;
+    const int na = a.E * kblocks;
     if ((int)blockIdx.x < na) {
-        dA_body<RT, Q81>(a, (int)blockIdx.x, (int)blockIdx.y * LORA_RC, lds.turn, lds.ja);
+        dA_body<RT, Q81>(a, (int)blockIdx.x, (int)blockIdx.y * LORA_RC, kblocks, alone != 0, lds.turn, lds.ja);
         return;
     }
     if (blockIdx.y) return;
@@ -383,39 +431,61 @@ constexpr int DX_COLS = 16 * GW;                           // columns of a dx wo
 template <int RT>
 void launch_grads(const LoraArgs& a, bool f16, bool q81, hipStream_t s) {
     const unsigned rc = (unsigned)ceil_div(a.R, LORA_RC);
-    const int nt = (int)ceil_div(a.N, 64), kt = (int)ceil_div(a.K, DX_COLS);
-    const dim3 g1((unsigned)(4 * a.nunits + a.E * nt), rc), g2((unsigned)(a.E * a.KB + (a.dx ? a.nunits * kt : 0)), rc);
+    // adapters of up to 64 rows on average: a wave of dB and dA takes all of them (41 rows of 4
+    // adapters, N = 10342, rank 64: the first launch 27.4 us with shared rows, 11.8 alone)
+    const int alone = a.M <= 64 * std::min(a.E, a.M), per = alone ? GW : 1;
+    const int nt = (int)ceil_div(a.N, 64 * per), kt = (int)ceil_div(a.K, DX_COLS), kb = (int)ceil_div(a.KB, per);
+    const dim3 g1((unsigned)(4 * a.nunits * a.S + a.E * nt), rc), g2((unsigned)(a.E * kb + (a.dx ? a.nunits * kt : 0)), rc);
     const dim3 th(GW * 64);
+    const auto join = [&] {
+        if (a.S > 1) hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)a.nunits), dim3(LT), 0, s, a);
+    };
     if (f16) {
         if (q81) {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, false>), g1, th, 0, s, a, nt);
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, true>), g2, th, 0, s, a, kt);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, false>), g1, th, 0, s, a, nt, alone);
+            join();
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, true>), g2, th, 0, s, a, kt, kb, alone);
         } else {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, true>), g1, th, 0, s, a, nt);
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, false>), g2, th, 0, s, a, kt);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, true>), g1, th, 0, s, a, nt, alone);
+            join();
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, false>), g2, th, 0, s, a, kt, kb, alone);
         }
     } else {
         if (q81) {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, false>), g1, th, 0, s, a, nt);
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, true>), g2, th, 0, s, a, kt);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, false>), g1, th, 0, s, a, nt, alone);
+            join();
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, true>), g2, th, 0, s, a, kt, kb, alone);
         } else {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, true>), g1, th, 0, s, a, nt);
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, false>), g2, th, 0, s, a, kt);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, true>), g1, th, 0, s, a, nt, alone);
+            join();
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, false>), g2, th, 0, s, a, kt, kb, alone);
         }
     }
 }
 
-}  // namespace
-
-// f32 u and its three bf16 planes
-size_t lora_grad_workspace_bytes(int64_t M, int64_t R) {
-    return (size_t)(round_up(M * R * 4, REGION_ALIGN) + round_up(M * R * 6, REGION_ALIGN));
+// Parts of N for u: one while a wave has twelve steps of two blocks at most (N <= 6144); else as many
+// as give it four, within 512 workgroups. Their sum is a launch of its own, 3 us of the host and 4
+// of the card (64 rows of 32 adapters, N = 4096, rank 16: 17.1 us in one part, 13.8 + 4.2 in two;
+// 37 rows of one adapter, N = 5221, rank 64: 20.4 us a call in one, 23.3 in two).
+int64_t u_parts(int64_t E, int64_t M, int64_t N) {
+    const int64_t blocks = ceil_div(N, 32), tiles = ceil_div(M, 16) + std::min(E, M);
+    if (blocks <= 24 * GW) return 1;
+    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, ceil_div(blocks, 8 * GW), MAX_U_PARTS}));
 }
 
-// both launches' grids stay below 2^32 threads
+}  // namespace
+
+// f32 u, its three bf16 planes, and its parts
+size_t lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t R) {
+    const int64_t S = u_parts(E, M, N);
+    return (size_t)(round_up(M * R * 4, REGION_ALIGN) + round_up(M * R * 6, REGION_ALIGN) +
+                    (S > 1 ? round_up(S * M * R * 4, REGION_ALIGN) : 0));
+}
+
+// both launches' grids stay below 2^32 threads (u's parts are split for few units only)
 bool lora_grad_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K) {
     const int64_t units = plan_layout(E, M).nunits;
-    return 4 * units + E * ceil_div(N, 64) < (int64_t(1) << 32) / (GW * 64) &&
+    return 4 * units * u_parts(E, M, N) + E * ceil_div(N, 64) < (int64_t(1) << 32) / (GW * 64) &&
            E * (K / QK) + units * ceil_div(K, DX_COLS) < (int64_t(1) << 32) / (GW * 64);
 }
 
@@ -435,6 +505,8 @@ hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* 
     a.dB = dB;
     a.u = static_cast<float*>(ws);
     a.planes = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + round_up(M * R * 4, REGION_ALIGN));
+    a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.planes) + round_up(M * R * 6, REGION_ALIGN));
+    a.S = (int)u_parts(E, M, N);
     const bool q81 = t == MMQ_ACT_Q8_1;
     if (R <= 16) launch_grads<1>(a, f16, q81, s);
     else if (R <= 32) launch_grads<2>(a, f16, q81, s);

@@ -49,7 +49,8 @@ CASES = [
     ("i8_token", "bf16", 130, 70, 544, 128, 3, "runs"), ("q8_1", "bf16", 200, 301, 512, 256, 2, "runs"),
     ("q8_1", "f16", 333, 99, 800, 8, 70, "mixed"), ("i8_token", "f16", 301, 777, 96, 16, 1, "one"),
     ("q8_1", "bf16", 40, 50, 64, 16, 3, "none"), ("q8_1", "bf16", 1000, 260, 128, 48, 4, "runs"),
-    ("i8_token", "bf16", 100, 33, 4128, 8, 2, "runs"), ("q8_1", "bf16", 90, 65, 64, 8, 4096, "mixed"),
+    ("i8_token", "bf16", 100, 33, 4128, 8, 2, "runs"), ("q8_1", "bf16", 41, 10342, 96, 64, 4, "mixed"),
+    ("i8_token", "f16", 20, 4129, 64, 24, 2, "mixed"), ("q8_1", "f16", 70, 8193, 32, 136, 1, "one"), ("q8_1", "bf16", 90, 65, 64, 8, 4096, "mixed"),
 ]
 
 
