@@ -285,13 +285,13 @@ def _plan_of(fn: str, plan, E: int, T: int, top_k: int):
 
 
 def _new(shape, dtype, at: int, stream):
-    """A tensor for a call's result. One made for a call on another stream than the current one
-    must outlive the call's kernels there."""
+    """A tensor for a call's result or workspace, from the memory of the call's own stream: what the
+    current stream's earlier work still uses is not handed to another stream's call."""
     import torch
-    t = torch.empty(shape, dtype=dtype, device=at)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=at)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=at)
 
 
 @functools.lru_cache(maxsize=4096)

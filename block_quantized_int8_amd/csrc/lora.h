@@ -246,6 +246,21 @@ struct LoraArgs {
     float *dA, *dB, *u;         // u: [M][R] by sorted position
 };
 
+// The plan's entries, held inside the buffers: a plan that was made for another batch gives
+// meaningless results, but no access outside them and no endless loop.
+__device__ inline int4 unit_at(const LoraArgs& a, int u) {
+    int4 v = a.units[u];
+    v.x = v.x < 0 ? a.E : v.x;
+    v.y = min(max(v.y, 0), a.M);
+    v.z = min(max(v.z, 0), min(GROUP_UNIT, a.M - v.y));
+    return v;
+}
+__device__ inline int row_at(const LoraArgs& a, int pos) { return (int)min((uint32_t)a.order[pos], (uint32_t)a.M - 1u); }
+__device__ inline int2 rows_of_group(const LoraArgs& a, int e) {
+    const int p0 = min(max(a.offs[e], 0), a.M);
+    return make_int2(p0, min(max(a.offs[e + 1], p0), a.M));
+}
+
 // The planes' values of ranks r .. of a position: eight ranks of consecutive positions lie side by
 // side, so that a matrix-core operand of 16 positions is loaded in whole cache lines.
 __device__ inline uint16_t* plane_at(const LoraArgs& a, int pos, int r) {
@@ -315,7 +330,7 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
 
     int m[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = a.order[unit.y + min(16 * t + 4 * g + j, unit.z - 1)];
+    for (int j = 0; j < 4; ++j) m[j] = row_at(a, unit.y + min(16 * t + 4 * g + j, unit.z - 1));
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = 0;

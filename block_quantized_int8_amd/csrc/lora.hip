@@ -86,7 +86,7 @@ __global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
     // (those are a few of its channels only: 14 us against 6.5 for 64 rows of 32 adapters)
     const int at = (int)blockIdx.x / a.S, s = ((int)blockIdx.x + at) % a.S;
     const int sub = at / a.nunits;
-    const int4 unit = a.units[at - sub * a.nunits];
+    const int4 unit = unit_at(a, at - sub * a.nunits);
     const int rows = min(unit.z - 16 * sub, 16);
     if (rows <= 0 || unit.x >= a.E) return;
     const int p0 = unit.y + 16 * sub, r0 = (int)blockIdx.y * 16 * RT;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(DW * 64) void lora_down_kernel(LoraArgs a) {
     const int parts = a.S * DW, per = (a.KB + parts - 1) / parts;      // blocks of a wave
     const int b0 = (s * DW + wave) * per, b1 = min(b0 + per, a.KB);
     // rows past the unit's last repeat it; their columns are not stored. Ranks past R likewise.
-    const int m = a.order[p0 + min(c, rows - 1)];
+    const int m = row_at(a, p0 + min(c, rows - 1));
     const uint16_t* A = a.A + (int64_t)unit.x * a.R * a.K;
     uint32_t aoff[RT];                          // R * K < 2^31 values
 #pragma unroll
@@ -132,11 +132,11 @@ template <bool F16, bool BF16, bool TAIL>
 __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs a, int ntiles) {
     __shared__ __attribute__((aligned(16))) ExpandLds<false, F16, 4> lds;
     const int u = (int)blockIdx.x / ntiles, tile = (int)blockIdx.x % ntiles;
-    const int4 unit = a.units[u];
+    const int4 unit = unit_at(a, u);
     if (unit.z == 0) return;
     if (unit.x >= a.E && tile == 0)                         // rows without an adapter: v = 0
         for (int i = 8 * threadIdx.x; i < unit.z * a.R; i += 8 * LT) {
-            float* to = a.v + (int64_t)a.order[unit.y + i / a.R] * a.R + i % a.R;
+            float* to = a.v + (int64_t)row_at(a, unit.y + i / a.R) * a.R + i % a.R;
             *reinterpret_cast<f32x4*>(to) = *reinterpret_cast<f32x4*>(to + 4) = 0;
         }
     expand_body<false, F16, BF16, TAIL, 4>(a, a.B, a.N, a.base, a.ldb, a.out, a.ldo, unit, tile, lds);
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int u = (int)blockIdx.x / ntiles, tile = (int)blockIdx.x % ntiles;
-    const int4 unit = a.units[u];
+    const int4 unit = unit_at(a, u);
     const int nt = (unit.z + 15) >> 4;
     const int t0 = tall ? wave : 0, group = tall ? tile : 4 * tile + wave;
     const int n0 = 64 * group, n = n0 + 4 * c, left = a.N - n;
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
                 }
             }
             if (group == 0) {
-                float* to = a.v + (int64_t)a.order[unit.y + at] * a.R + r;
+                float* to = a.v + (int64_t)row_at(a, unit.y + at) * a.R + r;
                 *reinterpret_cast<f32x4*>(to) = d[0];
                 *reinterpret_cast<f32x4*>(to + 4) = d[1];
             }
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int
     int m[4];
     auto rows_of = [&](int t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = a.order[unit.y + min(16 * t + 4 * g + j, unit.z - 1)];
+        for (int j = 0; j < 4; ++j) m[j] = row_at(a, unit.y + min(16 * t + 4 * g + j, unit.z - 1));
     };
 
     rows_of(t0);
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int tile = (int)blockIdx.x % ntiles, us = (int)blockIdx.x / ntiles, u = us / subs, sub = us - u * subs;
-    const int4 unit = a.units[u];
+    const int4 unit = unit_at(a, u);
     const bool none = unit.x >= a.E;
     const int64_t e = none ? 0 : unit.x;
     const int n0 = tile * SMALL_COLS + 64 * wave, n = n0 + 4 * c, left = a.N - n;
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
         f32x4 acc[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[i] = 0;
-        const int m = a.order[p0 + min(c, rows - 1)];
+        const int m = row_at(a, p0 + min(c, rows - 1));
         if (!none) {
             const int per = (a.KB + SW - 1) / SW, b0 = wave * per, b1 = min(b0 + per, a.KB);
             const uint16_t* A = a.A + e * a.R * a.K;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
                     raw[k][i] = *reinterpret_cast<const u32x4*>(B + min(col + i, last) * (uint32_t)a.R + r);
             }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = a.order[p0 + min(4 * g + j, rows - 1)];
+        for (int j = 0; j < 4; ++j) to[j] = row_at(a, p0 + min(4 * g + j, rows - 1));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             base[j] = 0;

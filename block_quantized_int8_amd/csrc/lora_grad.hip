@@ -120,12 +120,12 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int at = block / a.S, s = block - at * a.S, sub = at / a.nunits;     // a unit's first 16 rows come first
-    const int4 unit = a.units[at - sub * a.nunits];
+    const int4 unit = unit_at(a, at - sub * a.nunits);
     const int rows = min(unit.z - 16 * sub, 16);
     if (rows <= 0 || unit.x >= a.E) return;
     const int p0 = unit.y + 16 * sub, per_row = min(a.R - r0, LORA_RC) / 8;     // pieces of a row of B_e
 
-    const int64_t row = (int64_t)a.order[p0 + min(piece_row(lane), rows - 1)] * a.lddy;
+    const int64_t row = (int64_t)row_at(a, p0 + min(piece_row(lane), rows - 1)) * a.lddy;
     const uint16_t* B = a.B + (int64_t)unit.x * a.N * a.R + r0;
     uint32_t brow[RT], bcol[RT];
 #pragma unroll
@@ -214,7 +214,7 @@ __device__ inline void u_body(const LoraArgs& a, int block, int r0, ULds<RT, F16
 
 // u from its parts, in order: a workgroup per unit.
 __global__ __launch_bounds__(LT) void lora_join_kernel(LoraArgs a) {
-    const int4 unit = a.units[blockIdx.x];
+    const int4 unit = unit_at(a, blockIdx.x);
     if (unit.z == 0 || unit.x >= a.E) return;
     const float scale = a.scale[unit.x];
     for (int i = 4 * threadIdx.x; i < unit.z * a.R; i += 4 * LT) {
@@ -240,7 +240,8 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
     const int c = lane & 15, g = lane >> 4;
     const int e = block / ntiles, tile0 = block - e * ntiles;
     const int n0 = 64 * (alone ? GW * tile0 + wave : tile0), n = n0 + 4 * c;
-    const int p0 = a.offs[e], p1 = a.offs[e + 1], step = alone ? 32 : 32 * GW;
+    const int2 range = rows_of_group(a, e);
+    const int p0 = range.x, p1 = range.y, step = alone ? 32 : 32 * GW;
     if (alone && n0 >= a.N) return;
     const float* vr = a.v + min(r0 + RT * c, a.R - RT);
     f32x4 acc[4 * RT];
@@ -250,7 +251,7 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
     for (int p = p0 + (alone ? 0 : 32 * wave); p < p1; p += step) {
         int m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = a.order[min(p + 8 * g + j, p1 - 1)];
+        for (int j = 0; j < 8; ++j) m[j] = row_at(a, min(p + 8 * g + j, p1 - 1));
         typename Quad<BF16>::Raw x[8];
         V v[8];
         if (n0 + 64 <= a.N) {
@@ -340,7 +341,8 @@ __device__ inline void dA_body(const LoraArgs& a, int block, int r0, int kblocks
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int e = block / kblocks, b = alone ? GW * (block - e * kblocks) + wave : block - e * kblocks;
-    const int p0 = a.offs[e], p1 = a.offs[e + 1], step = alone ? 32 : 32 * GW;
+    const int2 range = rows_of_group(a, e);
+    const int p0 = range.x, p1 = range.y, step = alone ? 32 : 32 * GW;
     if (alone && b >= a.KB) return;
     const float* ur = a.u + min(r0 + RT * c, a.R - RT);
     ALds& mine = turn[wave];
@@ -349,7 +351,7 @@ __device__ inline void dA_body(const LoraArgs& a, int block, int r0, int kblocks
     for (int i = 0; i < 2 * RT; ++i) acc[i] = 0;
 #pragma unroll 1
     for (int p = p0 + (alone ? 0 : 32 * wave); p < p1; p += step) {
-        const int row = lane & 31, m = a.order[min(p + row, p1 - 1)];
+        const int row = lane & 31, m = row_at(a, min(p + row, p1 - 1));
         V u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = *reinterpret_cast<const V*>(ur + (int64_t)min(p + 8 * g + j, p1 - 1) * a.R);
@@ -419,7 +421,7 @@ __global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int kti
     }
     if (blockIdx.y) return;
     const int block = (int)blockIdx.x - na, u = block / ktiles;
-    const int4 unit = a.units[u];
+    const int4 unit = unit_at(a, u);
     if (unit.z == 0) return;
     // the columns turn with the unit, so that an XCD's L2 sees all of its channels
     expand_body<true, F16, false, false, GW>(a, a.A, a.K, a.dxb, a.lddxb, a.dx, a.lddx, unit,

@@ -281,9 +281,14 @@ struct RowArgs {
 
 constexpr int ROW_THREADS = 256;
 
+// the pair's sorted position, -1 if it has none (or one outside the rows: a plan of another batch)
+__device__ inline int pos_of(const RowArgs& a, int p) {
+    const int r = a.pos[p];
+    return (uint32_t)r < (uint32_t)(a.T * a.top_k) ? r : -1;
+}
 // the row of z that holds pair p, -1 if it has none
 __device__ inline int pair_row(const RowArgs& a, int p) {
-    const int r = a.pos[p];
+    const int r = pos_of(a, p);
     return r < 0 ? -1 : a.sorted ? r : p;
 }
 
@@ -295,7 +300,7 @@ __global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowArgs a) {
     for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
         const Piece<T> v = load_piece<T>(a.x, (int64_t)t * a.ldx + n, a.N - n);
         for (int j = 0; j < a.top_k; ++j) {
-            const int r = a.pos[t * a.top_k + j];
+            const int r = pos_of(a, t * a.top_k + j);
             if (r >= 0) store_piece<T>(a.y, (int64_t)r * a.ldy + n, v, a.N - n);
         }
     }

@@ -267,6 +267,8 @@ size_t mmq_gemm_id_noalloc_max_workspace_bytes(void);
  *             group each, as (group, first position, positions, 0), in sorted order; the pairs
  *             without a group are group E; unused entries hold zeros
  *   region 4  the sort's scratch (its contents mean nothing afterwards)
+ * A call given a plan of another batch (other ids, or other sizes whose plan is no larger) gives
+ * meaningless results, but reads and writes nothing outside its buffers.
  * --------------------------------------------------------------------------------------- */
 
 /* Total bytes of a plan; 0 if the arguments are invalid: 1 <= E <= 4096, 1 <= top_k <= E,

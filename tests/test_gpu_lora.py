@@ -247,3 +247,18 @@ def test_binding_refusals(env):
     with pytest.raises(mmq.MMQError) as err:                       # a rank that is no multiple of 8
         mmq.lora(act, A[:, :7].contiguous(), B[:, :, :7].contiguous(), scale, plan, M)
     assert err.value.code == mmq.MMQ_EINVAL
+
+
+def test_a_plan_of_another_batch_stays_inside_the_buffers(env):
+    """The entries of a plan made for more rows point past this batch's: the calls hold them inside."""
+    torch, mmq = env
+    big, N, K, R, E = 3000, 64, 64, 8, 2
+    A, B, scale = (t.cuda() for t in adapters(torch, "bf16", E, R, K, N, 1))
+    plan = mmq.group_rows(torch.from_numpy(row_ids(big, E, "runs", 1)).cuda(), E)
+    for M in (5, 40, 600):
+        act = torch.zeros(mmq.act_bytes("q8_1", M, K), dtype=torch.uint8, device="cuda")
+        frame = torch.full((M + 64, N), 3.0, device="cuda")
+        out, v = mmq.lora(act, A, B, scale, plan, M, base=frame[:M], out=frame[:M])
+        dx, dA, dB = mmq.lora_grad(act, A, B, scale, plan, v, out, want_dx=True)
+        torch.cuda.synchronize()
+        assert bool((frame[M:] == 3.0).all()) and dx.shape == (M, K)

@@ -240,3 +240,36 @@ def test_plan_must_fit(env):
         mmq.moe_combine(torch.zeros((16, 8), device="cuda"), plan, 4, 8, 2, weights=torch.zeros((16, 1), device="cuda"))
     with pytest.raises(mmq.MMQError):
         mmq.group_rows(ids, 1)                     # top_k > E
+
+
+def test_results_come_from_the_calls_own_stream(env):
+    """A call on another stream gets no memory that work of the current stream may still be using."""
+    torch, mmq = env
+    other = torch.cuda.Stream()
+    x = torch.zeros((64, 1000), device="cuda")
+    ids = torch.zeros((64, 2), dtype=torch.int32, device="cuda")
+    plan = mmq.group_rows(ids, 4)
+    torch.cuda.synchronize()
+    used = torch.empty((128, 1000), device="cuda")
+    at = used.data_ptr()
+    del used                                           # free for the current stream's next call alone
+    rows = mmq.moe_gather(x, plan, 4, 2, stream=other)
+    assert rows.data_ptr() != at
+    other.synchronize()
+    assert not bool(rows[:64].any())
+
+
+def test_a_plan_of_another_batch_stays_inside_the_buffers(env):
+    """The entries of a plan made for more tokens point past this batch's rows: the calls drop them."""
+    torch, mmq = env
+    T, big, top_k, E, N = 8, 1000, 2, 4, 64
+    ids = torch.from_numpy(_ids(big, top_k, E, 0.0, 1)).cuda()
+    plan = mmq.group_rows(ids, E)
+    x, z = torch.ones((T, N), device="cuda"), torch.ones((T * top_k, N), device="cuda")
+    frame = torch.full((T * top_k + 64, N), -7.0, device="cuda")
+    mmq.moe_gather(x, plan, E, top_k, out=frame[:T * top_k])
+    y = torch.full((T + 64, N), -7.0, device="cuda")
+    mmq.moe_combine(z, plan, E, T, top_k, order="sorted", out=y[:T])
+    torch.cuda.synchronize()
+    assert bool((frame[T * top_k:] == -7.0).all()) and bool((y[T:] == -7.0).all())
+    assert bool(((frame == 1.0) | (frame == -7.0)).all()) and bool(torch.isfinite(y).all())
