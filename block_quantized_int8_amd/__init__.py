@@ -248,7 +248,18 @@ def _gpu(fn: str, *tensors) -> int:
 
 def _raw_stream(stream, at: int) -> int:
     import torch
-    return torch._C._cuda_getCurrentRawStream(at) if stream is None else int(stream.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(at)
+    if stream.device_index != at:
+        raise ValueError(f"the stream must be one of the current GPU ({at}), got one of GPU {stream.device_index}")
+    return int(stream.cuda_stream)
+
+
+def _scratch(fn: str, workspace) -> int:
+    """The bytes of a caller's workspace."""
+    if not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous, got strides {workspace.stride()}")
+    return workspace.nbytes
 
 
 def _ld(fn: str, name: str, t, rows: int, cols: int, dtype) -> int:
@@ -485,7 +496,7 @@ def lora(act, A, B, scale, plan, M: int, atype="q8_1", base=None, out=None, v=No
     ldb = _ld(fn, "base", base, M, N, dt) if base is not None else 0
     _check("mmq_lora", lib().mmq_lora(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
                                       plan.data_ptr(), M, N, K, _ptr(base), ldb, out.data_ptr(), ldo, v.data_ptr(),
-                                      _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                                      _ptr(workspace), 0 if workspace is None else _scratch(fn, workspace),
                                       _raw_stream(stream, at)))
     return out, v
 
@@ -529,7 +540,7 @@ def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None
     _check("mmq_lora_grad",
            lib().mmq_lora_grad(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
                                plan.data_ptr(), M, N, K, v.data_ptr(), dy.data_ptr(), lddy, _ptr(dx_base), ldxb,
-                               _ptr(dx), lddx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                               _ptr(dx), lddx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), _scratch(fn, workspace),
                                _raw_stream(stream, at)))
     return dx, dA, dB
 

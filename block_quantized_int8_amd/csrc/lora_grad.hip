@@ -8,6 +8,8 @@
 //   1. u (16 rows, its eight waves share N) and dB_e (64 columns of N, the waves share the rows);
 //      u is left in f32 and as bf16 terms in operand order;
 //   2. dA_e (one block of K, the waves share the rows) and dx (expand_body).
+// 2048 rows of 4 adapters 4096 x 4096, rank 16: 17.7 + 18.9 us. The first launch reads dy twice (71 MB
+// of L2 misses, 4.0 TB/s); the second moves 84 MB (4.4 TB/s), most of it dx's base and dx.
 // The workgroups that sum over rows own their output tile, so nothing is added across
 // workgroups and the sums have one order.
 #include <algorithm>

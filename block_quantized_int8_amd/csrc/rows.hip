@@ -88,7 +88,8 @@ __device__ inline int2 block_scan(int2 v, int2* wtot) {
 // The stable sort. Every workgroup knows all counts (its own, or the count kernel's where that ran:
 // `counted`); wave w of a workgroup places segment w in pair order: 64 pairs
 // at a time find the lanes of their own key by one ballot per key bit, so a pair's position is
-// the wave's running start of its key plus the lanes before it.
+// the wave's running start of its key plus the lanes before it. Bound by latency: 80 pairs 4.7 us,
+// 16384 pairs of 64 groups 9.3 us in 16 workgroups (17.6 us in one).
 template <int GW, int KEYS>
 __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, int counted) {
     __shared__ int cur[GW][KEYS];
@@ -292,7 +293,9 @@ __device__ inline int pair_row(const RowArgs& a, int p) {
     return r < 0 ? -1 : a.sorted ? r : p;
 }
 
-// A token's row is read once and written to each of its pairs' places.
+// A token's row is read once and written to each of its pairs' places. Bound by memory: 2048 tokens x 8
+// of 4096 bf16 values, a quarter of the pairs without an expert, 118 MB in 23.1 us (5.1 TB/s; a
+// large copy reaches 5.2).
 template <typename T>
 __global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowArgs a) {
     const int n = ((int)blockIdx.x * ROW_THREADS + (int)threadIdx.x) * Piece<T>::V;
@@ -306,7 +309,9 @@ __global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowArgs a) {
     }
 }
 
-// y[t] = sum over j of w[t][j] z[row(t, j)]: f32 sums in rising j, one rounding at the end.
+// y[t] = sum over j of w[t][j] z[row(t, j)]: f32 sums in rising j, one rounding at the end. Eight rows'
+// loads are in flight before the first is used. 512 tokens x 8 of 2048 f32 values: 38 MB in 8.3 us
+// (4.6 TB/s).
 template <typename T>
 __global__ __launch_bounds__(ROW_THREADS) void combine_kernel(RowArgs a) {
     constexpr int V = Piece<T>::V, J = 8;      // J rows in flight
@@ -344,7 +349,9 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_kernel(RowArgs a) {
 }
 
 // dz[row] = w dy[t] and dw = <dy[t], z[row]> of one pair: W waves each (the dot is summed per
-// lane, then over lanes and waves in a fixed order).
+// lane, then over lanes and waves in a fixed order). The four pairs of a workgroup are neighbours, so
+// a token's dy comes from L2 for all but the first. 512 tokens x 8 of 2048 f32 values: 71 MB in
+// 13.2 us (5.4 TB/s).
 template <typename T, int W>
 __global__ __launch_bounds__(ROW_THREADS) void combine_grad_kernel(RowArgs a) {
     constexpr int V = Piece<T>::V, PW = ROW_THREADS / 64 / W;   // pairs per workgroup
@@ -499,8 +506,10 @@ hipError_t launch_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, co
     a.top_k = (int)top_k;
     a.N = (int)N;
     constexpr int W = ROW_THREADS / 64;
-    // a wave per pair, or all four of a workgroup while that leaves the chip's waves idle
-    const bool wide = P < 4096;
+    // A wave per pair, or all four of a workgroup for up to 1024 pairs. Measured, four waves against
+    // one, f32: 512 pairs x 2048 4.3 against 5.8 us, 1024 x 2048 6.4 against 6.9, 1024 x 8192 17.6
+    // against 29.1, 1536 x 2048 8.3 against 7.5, 4096 x 2048 17.8 against 13.2.
+    const bool wide = P <= 1024;
     const dim3 grid((unsigned)std::min<int64_t>(wide ? P : ceil_div(P, W), GRID_MAX));
     if (o == MMQ_OUT_F32) {
         if (wide) hipLaunchKernelGGL((combine_grad_kernel<uint32_t, W>), grid, dim3(ROW_THREADS), 0, s, a);

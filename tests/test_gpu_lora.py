@@ -239,6 +239,8 @@ def test_binding_refusals(env):
         mmq.lora(act, A, B, scale, plan, M, base=torch.zeros((M, N), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError, match="out"):
         mmq.lora(act, A, B, scale, plan, M, out=torch.zeros((M, N + 1), device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):             # one byte, repeated
+        mmq.lora(act, A, B, scale, plan, M, workspace=torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20))
     assert mmq.lora_workspace_bytes(E, M, N, K, R) == 0            # few rows: no workspace
     A2, B2, _ = (t.cuda() for t in adapters(torch, "bf16", E, 72, K, N, 1))
     with pytest.raises(mmq.MMQError) as err:
@@ -262,3 +264,75 @@ def test_a_plan_of_another_batch_stays_inside_the_buffers(env):
         dx, dA, dB = mmq.lora_grad(act, A, B, scale, plan, v, out, want_dx=True)
         torch.cuda.synchronize()
         assert bool((frame[M:] == 3.0).all()) and dx.shape == (M, K)
+
+
+SMALL_SCALED = [(1, 70, 64, 8, 1), (33, 100, 256, 16, 3), (150, 300, 512, 64, 2), (70, 65, 96, 136, 2)]
+
+
+@pytest.mark.parametrize("act", ["q8_1", "i8_token"])
+@pytest.mark.parametrize("kind,ea,eb", [("f16", -24, -24), ("bf16", -60, -50), ("bf16", 40, 50)])
+@pytest.mark.parametrize("M,N,K,R,E", SMALL_SCALED)
+def test_forward_exact_far_from_one(env, act, kind, ea, eb, M, N, K, R, E):
+    """The integers times powers of two: f16 adapters below the smallest normal value (2^-14), bf16
+    adapters whose products come near the ends of f32. Nothing rounds but a bf16 output."""
+    torch, mmq = env
+    print(f"[case] lora scaled {act} {kind} 2^{ea} 2^{eb} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    buf, x, A, B = integer_case(mmq, act, kind, M, N, K, R, E, [M, N, K])
+    if kind == "f16":
+        assert np.abs(A).max() < 2 ** 11 and np.abs(B).max() < 2 ** 10
+        A = np.where(np.abs(A) < 1024, A, np.sign(A) * 1023)            # subnormal: below 2^10 units of 2^-24
+    A, B = A * np.float32(2.0 ** ea), B * np.float32(2.0 ** eb)
+    ids = row_ids(M, E, "mixed", 5)
+    scale = 2.0 ** (np.arange(E) % 2) / 2
+    want, wv, mag, mag_v = rowmodel.lora(x, A, B, scale, ids, np.zeros((M, N)))
+    assert mag_v.max() < 2.0 ** (24 + ea) and (2 * mag).max() < 2.0 ** (25 + ea + eb)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float16
+    dA, dB = torch.from_numpy(A).to(dt), torch.from_numpy(B).to(dt)
+    assert np.array_equal(host(dA), A) and np.array_equal(host(dB), B)
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    out, v = mmq.lora(torch.from_numpy(buf).cuda(), dA.cuda(), dB.cuda(),
+                      torch.from_numpy(scale.astype(np.float32)).cuda(), plan, M, atype=act)
+    assert np.array_equal(host(v), wv)
+    want = want if act == "q8_1" else rowmodel.bf16(want).astype(np.float64)
+    assert np.array_equal(host(out), want)
+
+
+CONTAINED = [("q8_1", "f16", 5, 70, 64, 16, 2), ("q8_1", "bf16", 130, 1100, 128, 72, 3), ("i8_token", "bf16", 150, 301, 512, 64, 2),
+             ("i8_token", "f16", 700, 260, 4096, 64, 4), ("q8_1", "bf16", 2300, 130, 64, 72, 3)]
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E", CONTAINED)
+def test_what_is_not_finite_stays_in_its_row(env, act, kind, M, N, K, R, E):
+    """A row whose activations' scale or base is not finite changes no other row, nor does what the
+    workspace held before."""
+    torch, mmq = env
+    print(f"[case] lora not finite {act} {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    ids = row_ids(M, E, "runs", 3)
+    ids[M // 2] = E - 1
+    r = np.random.default_rng([M, N])
+    q = r.integers(-127, 128, (M, K)).astype(np.int8)
+    q[q == 0] = 1                                                # so that the row's every product is NaN
+    s = r.random((M, K // 32) if act == "q8_1" else M).astype(np.float32)
+    A, B, scale = (t.cuda() for t in adapters(torch, kind, E, R, K, N, 8))
+    io = torch.float32 if act == "q8_1" else torch.bfloat16
+    base = torch.randn((M, N), generator=torch.Generator().manual_seed(4)).to(io).cuda()
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    need = mmq.lora_workspace_bytes(E, M, N, K, R)
+
+    def run(scales, b, fill):
+        buf = mmq.act_q8_1_pack_host(q, scales) if act == "q8_1" else mmq.act_i8_pack_host(q, scales)
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda") if need else None
+        return mmq.lora(torch.from_numpy(buf).cuda(), A, B, scale, plan, M, atype=act, base=b, workspace=ws)
+    out, v = run(s, base, 0)
+    assert bool(out.isfinite().all()) and bool(v.isfinite().all())
+    bad = s.copy()
+    bad[M // 2] = np.nan
+    badb = base.clone()
+    badb[0, N - 1] = float("inf")
+    out2, v2 = run(bad, badb, 255)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[M // 2] = False
+    assert torch.equal(v2[keep], v[keep]) and bool(v2[M // 2].isnan().all())
+    assert bool(out2[M // 2].isnan().all())
+    out[0, N - 1] = float("inf")                                 # a value added to the base alone
+    assert torch.equal(out2[keep], out[keep])

@@ -235,3 +235,64 @@ def test_graph_and_streams(env):
         for res in every:
             for a, b in zip(res, got["out"]):
                 assert torch.equal(a, b), rep
+
+
+@pytest.mark.parametrize("act", ["q8_1", "i8_token"])
+@pytest.mark.parametrize("M,N,K,R,E", [(1, 70, 64, 8, 1), (70, 100, 96, 16, 3), (150, 130, 64, 40, 2), (300, 6500, 64, 72, 2)])
+def test_gradients_exact_far_from_one(env, act, M, N, K, R, E):
+    """Integers times powers of two: f16 adapters below the smallest normal value, gradients near
+    2^-60 (what a loss's mean leaves); nothing rounds, so the gradients have to be equal."""
+    torch, mmq = env
+    print(f"[case] lora_grad scaled {act} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    r = np.random.default_rng([M, N, K, R])
+    ids = row_ids(M, E, "mixed", 5)
+    q = (r.integers(-2, 3, (M, K)) * (r.random((M, K)) < 0.2)).astype(np.int8)
+    s = np.ones((M, K // 32) if act == "q8_1" else M, np.float32)
+    buf = mmq.act_q8_1_pack_host(q, s) if act == "q8_1" else mmq.act_i8_pack_host(q, s)
+    A = (r.integers(-2, 3, (E, R, K)) * (r.random((E, R, K)) < 0.2) * 2.0 ** -24).astype(np.float32)
+    B = (r.integers(-1023, 1024, (E, N, R)) * (r.random((E, N, R)) < 2 / N) * 2.0 ** -24).astype(np.float32)
+    dy = (r.integers(-127, 128, (M, N)) * (r.random((M, N)) < 0.1) * 2.0 ** -60).astype(np.float32)
+    v = (r.integers(-3, 4, (M, R)) * 2.0 ** -30).astype(np.float32)
+    scale = np.ones(E, np.float32)
+    want, mag = rowmodel.lora_grad(q.astype(np.float64), A, B, scale, ids, v, dy, np.zeros((M, K)))
+    for m, unit in zip(mag, (-108, -84, -90)):                   # dx, dA, dB in units of their products
+        assert m.max() < 2.0 ** (24 + unit)
+    io = torch.float32 if act == "q8_1" else torch.bfloat16
+    got = mmq.lora_grad(torch.from_numpy(buf).cuda(), torch.from_numpy(A).half().cuda(), torch.from_numpy(B).half().cuda(),
+                        torch.from_numpy(scale).cuda(), mmq.group_rows(torch.from_numpy(ids).cuda(), E),
+                        torch.from_numpy(v).cuda(), torch.from_numpy(dy).to(io).cuda(), atype=act)
+    for name, g, w in zip(("dx", "dA", "dB"), got, want):
+        assert np.array_equal(host(g), w), name
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E", [
+    ("q8_1", "f16", 5, 70, 64, 16, 3), ("q8_1", "bf16", 400, 300, 128, 72, 3), ("i8_token", "bf16", 150, 131, 96, 64, 2),
+    ("i8_token", "f16", 90, 6500, 64, 32, 4)])
+def test_what_is_not_finite_stays_with_its_adapter(env, act, kind, M, N, K, R, E):
+    """A row whose dy is not finite in one column, of an adapter: other rows' dx, other adapters' dA
+    and dB and the adapter's dB of other columns stay bit for bit, whatever the workspace held."""
+    torch, mmq = env
+    print(f"[case] lora_grad not finite {act} {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    ids, buf, x, A, B, scale, dy, v, dxb = problem(torch, mmq, act, kind, M, N, K, R, E, "runs", seed=5)
+    at, e, n = M // 2, E - 1, N - 2
+    ids[at] = e
+    v[at] = 1.0
+    dev = [t.cuda() for t in (torch.from_numpy(buf), A, B, scale)]
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    need = mmq.lora_grad_workspace_bytes(E, M, N, K, R)
+
+    def run(g, fill):
+        return mmq.lora_grad(*dev, plan, v.cuda(), g.cuda(), atype=act, dx_base=dxb.cuda(),
+                             workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+    clean = run(dy, 0)
+    assert all(bool(t.isfinite().all()) for t in clean)
+    others = [i for i in range(M) if i != at]
+    for value in (float("nan"), float("inf"), float("-inf")):
+        bad = dy.clone()
+        bad[at, n] = value
+        dx, dA, dB = run(bad, 255)
+        assert torch.equal(dx[others], clean[0][others]) and not bool(dx[at].isfinite().any())
+        assert torch.equal(dA[:e], clean[1][:e]) and torch.equal(dB[:e], clean[2][:e])
+        assert not bool(dA[e].isfinite().any()) and not bool(dB[e, n].isfinite().any())
+        cols = [i for i in range(N) if i != n]
+        assert torch.equal(dB[e, cols], clean[2][e, cols])

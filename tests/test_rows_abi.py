@@ -97,3 +97,12 @@ def test_binding_refuses_host_tensors(mmq):
         mmq.moe_combine(torch.zeros(8, 64), plan, 8, 4, 2)
     with pytest.raises(ValueError, match="GPU"):
         mmq.moe_combine_grad(torch.zeros(4, 64), torch.zeros(8, 64), plan, 8, 2, torch.zeros(4, 2))
+
+
+def test_binding_refuses_another_gpus_stream(mmq):
+    class Stream:
+        cuda_stream = 0
+        device_index = 1
+    with pytest.raises(ValueError, match="stream"):
+        mmq._raw_stream(Stream, 0)
+    assert mmq._raw_stream(Stream, 1) == 0
