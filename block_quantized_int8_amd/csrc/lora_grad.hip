@@ -102,6 +102,12 @@ template <int NT> __device__ inline void join_waves(JoinLds<NT>& red, f32x4* acc
 
 // ------------------------------------------------------------------------------ launch 1
 constexpr int MAX_U_PARTS = 8;
+// Rows of an adapter that one wave sums alone (each_sum): 64, or 256 where the adapters in use have
+// blocks enough for the chip. Measured, all alone against all shared (us a call): 41 rows of 4
+// adapters, N = 10342, rank 64: first launch 11.8, 27.4; 800 rows of 8, 4096 x 4096, rank 64: 31.4,
+// 42.8; 200 rows of 2: 26.8, 23.8; 1200 rows of 8: 42.2, 52.0; 4096 rows of 8, rank 16: 94.6, 69.4.
+constexpr int FEW = 64, FEW_FULL = 256;
+constexpr int MANY_MAX = 512;       // workgroups that share rows, where the plan has such adapters
 
 // four ranks of a row's u, in f32 and as terms
 __device__ inline void keep_u(const LoraArgs& a, int pos, int r, f32x4 d) {
@@ -232,15 +238,69 @@ __global__ __launch_bounds__(LT) void lora_join_kernel(LoraArgs a) {
     }
 }
 
-// dB_e[n][r] over all rows of adapter e: 64 columns n and up to 64 ranks, the waves every eighth 32
-// rows; `alone` (adapters of few rows): 64 columns and all rows a wave, nothing to join. Both operands come straight from memory: a lane loads four consecutive columns (RT
-// consecutive ranks) of eight rows, which are its k.
+// The sums over an adapter's rows (dB, dA) are dealt out by the rows that it has, which only the
+// device knows. An adapter's output is cut into `blocks`. With few rows a wave takes one of them and
+// all rows, eight blocks a workgroup, nothing to join (`alone`); else the eight waves share the rows
+// of a block. The first `many` workgroups deal out the blocks of the adapters of many rows, the rest
+// are one for each eight blocks of every adapter and end at once where it has many. (By the rows
+// an adapter has on average, 2048 rows that all went to one of 32 adapters took 293 us, now 67;
+// spread evenly 76 and 78.)
+struct SumGrid {
+    int blocks, one, many, full;                           // one: workgroups of an adapter of few rows
+};
+
+template <typename Body> __device__ inline void each_sum(const LoraArgs& a, const SumGrid& s, int w, Body body) {
+    auto rows_of = [&](int e) {
+        if (e >= a.E) return 0;
+        const int2 r = rows_of_group(a, e);
+        return r.y - r.x;
+    };
+    int e0 = 0, few;
+    uint64_t big;                                          // which of 64 adapters from e0 on have many rows
+    {
+        const int rows = rows_of(threadIdx.x & 63);
+        few = __popcll(__ballot(rows > 0)) * s.blocks >= s.full ? FEW_FULL : FEW;
+        big = __ballot(rows > few);
+    }
+    const bool alone = w >= s.many;
+    int i = alone ? w - s.many : w;
+#pragma unroll 1
+    for (;;) {
+        int e, block;
+        if (alone) {
+            e = i / s.one;
+            block = i - e * s.one;
+            if (rows_of(e) > few) return;
+        } else {
+            while (i >= __popcll(big) * s.blocks) {
+                i -= __popcll(big) * s.blocks;
+                e0 += 64;
+                if (e0 >= a.E) return;
+                big = __ballot(rows_of(e0 + (int)(threadIdx.x & 63)) > few);
+            }
+            const int q = i / s.blocks;
+            uint64_t left = big;
+            for (int k = 0; k < q; ++k) left &= left - 1;
+            e = e0 + __builtin_ctzll(left);
+            block = i - q * s.blocks;
+        }
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));                      // nothing of the body is held across the loop
+        body(e, block, alone, tid);
+        if (alone) return;
+        __syncthreads();                                   // the join's memory is free again
+        i += s.many;
+    }
+}
+
+// dB_e[n][r] over all rows of adapter e: 64 columns n (eight times that if alone) and up to 64 ranks.
+// Both operands come straight from memory: a lane loads four consecutive columns (RT consecutive
+// ranks) of eight rows, which are its k.
 template <int RT, bool BF16>
-__device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles, bool alone, JoinLds<4 * RT>& red) {
+__device__ inline void dB_body(const LoraArgs& a, int e, int tile0, int r0, bool alone, int tid, JoinLds<4 * RT>& red) {
     typedef typename RankVec<RT>::V V;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int e = block / ntiles, tile0 = block - e * ntiles;
     const int n0 = 64 * (alone ? GW * tile0 + wave : tile0), n = n0 + 4 * c;
     const int2 range = rows_of_group(a, e);
     const int p0 = range.x, p1 = range.y, step = alone ? 32 : 32 * GW;
@@ -316,7 +376,7 @@ __device__ inline void dB_body(const LoraArgs& a, int block, int r0, int ntiles,
 }
 
 template <int RT, bool F16, bool BF16>
-__global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, int ntiles, int alone) {
+__global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, SumGrid sums) {
     __shared__ __attribute__((aligned(16))) union {
         struct { ULds<RT, F16, BF16> turn[GW]; } u;
         JoinLds<RT> ju;
@@ -324,25 +384,27 @@ __global__ __launch_bounds__(GW * 64) void lora_grad1_kernel(LoraArgs a, int nti
     } lds;
     const int r0 = (int)blockIdx.y * LORA_RC, nu = 4 * a.nunits * a.S;
     if ((int)blockIdx.x < nu) u_body<RT, F16, BF16>(a, (int)blockIdx.x, r0, lds.u.turn, lds.ju);
-    else dB_body<RT, BF16>(a, (int)blockIdx.x - nu, r0, ntiles, alone != 0, lds.jb);
+    else
+        each_sum(a, sums, (int)blockIdx.x - nu,
+                 [&](int e, int block, bool alone, int tid) { dB_body<RT, BF16>(a, e, block, r0, alone, tid, lds.jb); });
 }
 
 // ------------------------------------------------------------------------------ launch 2
-// dA_e[r][k] over all rows of adapter e: one block of K and up to 64 ranks, the waves every eighth
-// 32 rows; `alone`: one block and all rows a wave. A wave loads the 32 rows' 1 KB of the block (16 bytes a lane), turns them in LDS as
-// bf16, and scales u by the rows' block scales.
+// dA_e[r][k] over all rows of adapter e: one block of K (eight if alone) and up to 64 ranks. A wave
+// loads the 32 rows' 1 KB of the block (16 bytes a lane), turns them in LDS as bf16, and scales u by
+// the rows' block scales.
 struct ALds {
     uint16_t x[32][40];
     float xs[32];
 };
 
 template <int RT, bool Q81>
-__device__ inline void dA_body(const LoraArgs& a, int block, int r0, int kblocks, bool alone, ALds* turn,
+__device__ inline void dA_body(const LoraArgs& a, int e, int block, int r0, bool alone, int tid, ALds* turn,
                                JoinLds<2 * RT>& red) {
     typedef typename RankVec<RT>::V V;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int e = block / kblocks, b = alone ? GW * (block - e * kblocks) + wave : block - e * kblocks;
+    const int b = alone ? GW * block + wave : block;
     const int2 range = rows_of_group(a, e);
     const int p0 = range.x, p1 = range.y, step = alone ? 32 : 32 * GW;
     if (alone && b >= a.KB) return;
@@ -410,15 +472,17 @@ __device__ inline void dA_body(const LoraArgs& a, int block, int r0, int kblocks
 }
 
 template <int RT, bool F16, bool Q81>
-__global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int ktiles, int kblocks, int alone) {
+__global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int ktiles, SumGrid sums) {
     __shared__ __attribute__((aligned(16))) union {
         ALds turn[GW];
         JoinLds<2 * RT> ja;
         ExpandLds<true, F16, GW> x;
     } lds;
-    const int na = a.E * kblocks;
+    const int na = sums.many + a.E * sums.one;
     if ((int)blockIdx.x < na) {
-        dA_body<RT, Q81>(a, (int)blockIdx.x, (int)blockIdx.y * LORA_RC, kblocks, alone != 0, lds.turn, lds.ja);
+        each_sum(a, sums, (int)blockIdx.x, [&](int e, int block, bool alone, int tid) {
+            dA_body<RT, Q81>(a, e, block, (int)blockIdx.y * LORA_RC, alone, tid, lds.turn, lds.ja);
+        });
         return;
     }
     if (blockIdx.y) return;
@@ -432,37 +496,42 @@ __global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int kti
 
 constexpr int DX_COLS = 16 * GW;                           // columns of a dx workgroup
 
+// `blocks` of an adapter's output, and where they count as enough to fill the chip with a wave each
+SumGrid sum_grid(const LoraArgs& a, int64_t blocks, int full) {
+    const int64_t big = std::min<int64_t>(a.E, a.M / (FEW + 1));       // adapters of many rows at most
+    return SumGrid{(int)blocks, (int)ceil_div(blocks, GW), (int)std::min<int64_t>(MANY_MAX, big * blocks), full};
+}
+
 template <int RT>
 void launch_grads(const LoraArgs& a, bool f16, bool q81, hipStream_t s) {
     const unsigned rc = (unsigned)ceil_div(a.R, LORA_RC);
-    // adapters of up to 64 rows on average: a wave of dB and dA takes all of them (41 rows of 4
-    // adapters, N = 10342, rank 64: the first launch 27.4 us with shared rows, 11.8 alone)
-    const int alone = a.M <= 64 * std::min(a.E, a.M), per = alone ? GW : 1;
-    const int nt = (int)ceil_div(a.N, 64 * per), kt = (int)ceil_div(a.K, DX_COLS), kb = (int)ceil_div(a.KB, per);
-    const dim3 g1((unsigned)(4 * a.nunits * a.S + a.E * nt), rc), g2((unsigned)(a.E * kb + (a.dx ? a.nunits * kt : 0)), rc);
+    const SumGrid sb = sum_grid(a, ceil_div(a.N, 64), 512), sa = sum_grid(a, a.KB, 1024);
+    const int kt = (int)ceil_div(a.K, DX_COLS);
+    const dim3 g1((unsigned)(4 * a.nunits * a.S + sb.many + a.E * sb.one), rc);
+    const dim3 g2((unsigned)(sa.many + a.E * sa.one + (a.dx ? a.nunits * kt : 0)), rc);
     const dim3 th(GW * 64);
     const auto join = [&] {
         if (a.S > 1) hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)a.nunits), dim3(LT), 0, s, a);
     };
     if (f16) {
         if (q81) {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, false>), g1, th, 0, s, a, nt, alone);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, false>), g1, th, 0, s, a, sb);
             join();
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, true>), g2, th, 0, s, a, kt, kb, alone);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, true>), g2, th, 0, s, a, kt, sa);
         } else {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, true>), g1, th, 0, s, a, nt, alone);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, true, true>), g1, th, 0, s, a, sb);
             join();
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, false>), g2, th, 0, s, a, kt, kb, alone);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, true, false>), g2, th, 0, s, a, kt, sa);
         }
     } else {
         if (q81) {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, false>), g1, th, 0, s, a, nt, alone);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, false>), g1, th, 0, s, a, sb);
             join();
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, true>), g2, th, 0, s, a, kt, kb, alone);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, true>), g2, th, 0, s, a, kt, sa);
         } else {
-            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, true>), g1, th, 0, s, a, nt, alone);
+            hipLaunchKernelGGL((lora_grad1_kernel<RT, false, true>), g1, th, 0, s, a, sb);
             join();
-            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, false>), g2, th, 0, s, a, kt, kb, alone);
+            hipLaunchKernelGGL((lora_grad2_kernel<RT, false, false>), g2, th, 0, s, a, kt, sa);
         }
     }
 }
@@ -489,8 +558,8 @@ size_t lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t R) {
 // both launches' grids stay below 2^32 threads (u's parts are split for few units only)
 bool lora_grad_grid_ok(int64_t E, int64_t M, int64_t N, int64_t K) {
     const int64_t units = plan_layout(E, M).nunits;
-    return 4 * units * u_parts(E, M, N) + E * ceil_div(N, 64) < (int64_t(1) << 32) / (GW * 64) &&
-           E * (K / QK) + units * ceil_div(K, DX_COLS) < (int64_t(1) << 32) / (GW * 64);
+    return 4 * units * u_parts(E, M, N) + E * ceil_div(N, 64) < (int64_t(1) << 32) / (GW * 64) - MANY_MAX &&
+           E * (K / QK) + units * ceil_div(K, DX_COLS) < (int64_t(1) << 32) / (GW * 64) - MANY_MAX;
 }
 
 hipError_t launch_lora_grad(mmq_atype t, bool f16, const void* act, const void* A, const void* B, const float* scale,

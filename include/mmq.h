@@ -383,8 +383,8 @@ size_t mmq_lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K,
  *  dA, dB  (device) f32 [E][R][K] and [E][N][R], written whole (zeros for an adapter without rows)
  *  workspace (device) >= mmq_lora_grad_workspace_bytes(E, M, N, K, R) bytes, as for mmq_lora
  * Sizes, strides and errors as for mmq_lora; MMQ_EINVAL also where E * ceil(N/64) plus four for
- * each of the plan's units, or E * K/32 plus ceil(K/128) for each of them, reaches 2^23. f32 sums
- * of exact products in a fixed order, as in mmq_lora. */
+ * each of the plan's units, or E * K/32 plus ceil(K/128) for each of them, reaches 2^23 - 512. f32
+ * sums of exact products in an order fixed by the sizes and the plan. */
 mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B,
                          const float* scale, int64_t E, int64_t R, const void* plan, int64_t M, int64_t N,
                          int64_t K, const float* v, const void* dy, int64_t lddy, const float* dx_base,

@@ -296,3 +296,27 @@ def test_what_is_not_finite_stays_with_its_adapter(env, act, kind, M, N, K, R, E
         assert not bool(dA[e].isfinite().any()) and not bool(dB[e, n].isfinite().any())
         cols = [i for i in range(N) if i != n]
         assert torch.equal(dB[e, cols], clean[2][e, cols])
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E,big", [
+    ("q8_1", "bf16", 900, 70, 96, 16, 200, (150,)), ("i8_token", "f16", 700, 300, 64, 40, 129, (0, 63, 64, 128)),
+    ("q8_1", "f16", 400, 65, 64, 8, 2, (1,)), ("q8_1", "bf16", 1100, 33, 11008, 8, 4, (0, 1, 2, 3)),
+    ("i8_token", "bf16", 1100, 16500, 32, 8, 4, (0, 1, 2, 3)), ("q8_1", "bf16", 640, 500, 160, 72, 6, (2, 5))])
+def test_adapters_of_many_and_of_few_rows(env, act, kind, M, N, K, R, E, big):
+    """Nearly all rows with a few adapters (some of them past the 64th), the rest with a few rows or
+    none; more blocks of output than workgroups that share them."""
+    torch, mmq = env
+    print(f"[case] lora_grad many {act} {kind} M={M} N={N} K={K} R={R} E={E} {big}", flush=True)
+    _, buf, x, A, B, scale, dy, v, dxb = problem(torch, mmq, act, kind, M, N, K, R, E, "none", seed=6)
+    r = np.random.default_rng([M, E])
+    ids = np.asarray(big, np.int32)[np.arange(M) % len(big)]
+    few = r.random(M) < 0.03
+    ids[few] = r.integers(-1, E, int(few.sum()))
+    v = torch.randn((M, R), generator=torch.Generator().manual_seed(2))
+    got = mmq.lora_grad(*(t.cuda() for t in (torch.from_numpy(buf), A, B, scale)),
+                        mmq.group_rows(torch.from_numpy(ids).cuda(), E), v.cuda(), dy.cuda(), atype=act, dx_base=dxb.cuda())
+    want, mag = rowmodel.lora_grad(x, host(A), host(B), host(scale), ids, host(v), host(dy), host(dxb))
+    rows, nu = int(np.bincount(ids[ids >= 0]).max()), 5 * N + 8
+    for name, g, w, m, n in zip(("dx", "dA", "dB"), got, want, mag, (nu + 5 * R + 8, nu + 3 * rows + 10, 6 * rows + 8)):
+        assert np.all(np.abs(host(g) - w) <= n * U23 * m * 1.01), name
+        assert np.linalg.norm(host(g) - w) <= 1e-6 * np.linalg.norm(w), name
