@@ -16,17 +16,21 @@ namespace {
 
 // Sizes of the sort. Up to GROUP_ONE pairs one launch sorts: up to GROUP_WGS workgroups, each of
 // which counts all pairs (64 KB of ids at most, from L2) and places a segment. Past that a launch of
-// up to GROUP_MAX workgroups counts their segments first. KEYS bounds the groups (E + 1, the last
-// being "no group") of an instance, whose LDS holds a counter for each wave and key.
+// up to GROUP_MAX workgroups counts their segments first. There are two instances: 16 waves for up to
+// SMALL_KEYS groups (E + 1, the last being "no group"), whose LDS has room for a counter for each wave
+// and key, else 4 waves. Segments of a counted sort, measured with 2048, 4096, 8192 and 16384 pairs
+// (us): 32768 pairs of 64 groups 8.4, 9.7, 12.7, 20.0; 800000 of 64 17.5, 16.7, 17.3, 23.3; 240000
+// of 4096 428, 232, 145, 124 (each workgroup reads all segments' counts of all keys).
 constexpr int64_t GROUP_ONE = 16384;
 constexpr int64_t GROUP_WGS = 16;
 constexpr int64_t GROUP_MAX = 256;
+constexpr int SMALL_KEYS = 1024, MAX_KEYS = 4097;
 
 bool group_counts_first(int64_t P) { return P > GROUP_ONE; }
-// workgroups of an instance with `threads` threads
-int64_t group_blocks(int64_t P, int64_t threads) {
-    return group_counts_first(P) ? std::min<int64_t>(GROUP_MAX, ceil_div(P, GROUP_ONE))
-                                 : std::min<int64_t>(GROUP_WGS, ceil_div(P, threads));
+int64_t group_blocks(int64_t E, int64_t P) {
+    const bool small = E + 1 <= SMALL_KEYS;
+    return group_counts_first(P) ? std::min<int64_t>(GROUP_MAX, ceil_div(P, small ? 2048 : 16384))
+                                 : std::min<int64_t>(GROUP_WGS, ceil_div(P, small ? 1024 : 256));
 }
 
 struct GroupArgs {
@@ -50,18 +54,29 @@ __device__ inline void load_ids(const GroupArgs& a, int64_t p, int64_t end, int*
     }
 }
 
+// Lanes that add to one LDS address wait for each other, so a key has several counters. (16384 pairs
+// of 64 groups, a quarter of them without one: 9.1 us with one counter, 7.9 with two, 7.2 with
+// four or eight; all of one group: 18.6, 12.0, 9.0, 7.4.)
+template <int KEYS> constexpr int COPIES = KEYS <= SMALL_KEYS ? 8 : 1;
+
 // counts of each workgroup's segment: scratch[block][E + 1]
 template <int GW, int KEYS>
 __global__ __launch_bounds__(GW * 64) void group_count_kernel(GroupArgs a) {
-    __shared__ int cnt[KEYS];
+    constexpr int C = COPIES<KEYS>;
+    __shared__ int cnt[KEYS][C];
     const int keys = a.E + 1;
-    for (int e = threadIdx.x; e < keys; e += GW * 64) cnt[e] = 0;
+    for (int i = threadIdx.x; i < C * keys; i += GW * 64) cnt[0][i] = 0;
     __syncthreads();
     const int64_t p0 = (int64_t)blockIdx.x * a.seg;
     const int p1 = (int)min(p0 + a.seg, (int64_t)a.P);
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += GW * 64) atomicAdd(&cnt[key_of(a, a.ids[p])], 1);
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += GW * 64) atomicAdd(&cnt[key_of(a, a.ids[p])][threadIdx.x % C], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e < keys; e += GW * 64) a.scratch[(int64_t)blockIdx.x * keys + e] = cnt[e];
+    for (int e = threadIdx.x; e < keys; e += GW * 64) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) n += cnt[e][i];
+        a.scratch[(int64_t)blockIdx.x * keys + e] = n;
+    }
 }
 
 // Inclusive scan of (x, y) over the workgroup's threads.
@@ -89,17 +104,18 @@ __device__ inline int2 block_scan(int2 v, int2* wtot) {
 // `counted`); wave w of a workgroup places segment w in pair order: 64 pairs
 // at a time find the lanes of their own key by one ballot per key bit, so a pair's position is
 // the wave's running start of its key plus the lanes before it. Bound by latency: 80 pairs 4.7 us,
-// 16384 pairs of 64 groups 9.3 us in 16 workgroups (17.6 us in one).
+// 16384 pairs of 64 groups 7.2 us.
 template <int GW, int KEYS>
 __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, int counted) {
     __shared__ int cur[GW][KEYS];
-    __shared__ int before[KEYS], after[KEYS];              // the earlier and later workgroups' pairs
+    constexpr int C = COPIES<KEYS>;
+    __shared__ int before[KEYS][C], after[KEYS][C];        // the earlier and later workgroups' pairs
     __shared__ int offs[KEYS + 1], uoff[KEYS + 1];
     __shared__ int2 wtot[GW];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int keys = a.E + 1, nblk = (int)gridDim.x, blk = (int)blockIdx.x;
     for (int i = lane; i < keys; i += 64) cur[wave][i] = 0;
-    for (int i = tid; i < keys; i += GW * 64) before[i] = after[i] = 0;
+    for (int i = tid; i < C * keys; i += GW * 64) before[0][i] = after[0][i] = 0;
     const int64_t b0 = min((int64_t)blk * a.seg, (int64_t)a.P);
     const int64_t b1 = min(b0 + a.seg, (int64_t)a.P);
     const int wseg = (int)(((b1 - b0 + GW - 1) / GW + 63) & ~(int64_t)63);   // pairs per wave
@@ -112,8 +128,8 @@ __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, i
 #pragma unroll
             for (int i = 0; i < KEYS_AT_ONCE; ++i) {
                 const int64_t at = p + 64 * i;
-                if (at < b0) atomicAdd(&before[key_of(a, id[i])], 1);
-                else if (at >= b1 && at < a.P) atomicAdd(&after[key_of(a, id[i])], 1);
+                if (at < b0) atomicAdd(&before[key_of(a, id[i])][lane % C], 1);
+                else if (at >= b1 && at < a.P) atomicAdd(&after[key_of(a, id[i])][lane % C], 1);
             }
         }
     for (int64_t p = s0 + lane; p - lane < s1; p += 64 * KEYS_AT_ONCE) {
@@ -123,14 +139,22 @@ __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, i
         for (int i = 0; i < KEYS_AT_ONCE; ++i)
             if (p + 64 * i < s1) atomicAdd(&cur[wave][key_of(a, id[i])], 1);
     }
-    if (counted)
+    if (counted && KEYS <= SMALL_KEYS) {                     // few keys: a count a thread
+        const uint32_t n = (uint32_t)nblk * keys;
+#pragma unroll 8
+        for (uint32_t x = tid; x < n; x += GW * 64) {
+            const int b = (int)(x / (uint32_t)keys), e = (int)x - b * keys, c = a.scratch[x];
+            if (b != blk) atomicAdd(b < blk ? &before[e][lane % C] : &after[e][lane % C], c);
+        }
+    } else if (counted) {                                  // a key a thread
         for (int e = tid; e < keys; e += GW * 64) {
             int x = 0, y = 0;
             for (int b = 0; b < blk; ++b) x += a.scratch[(int64_t)b * keys + e];
             for (int b = blk + 1; b < nblk; ++b) y += a.scratch[(int64_t)b * keys + e];
-            before[e] = x;
-            after[e] = y;
+            before[e][0] = x;
+            after[e][0] = y;
         }
+    }
     __syncthreads();
 
     // thread t owns keys [t*KPT, t*KPT + KPT): all pairs of a key, then the waves' starts
@@ -138,7 +162,9 @@ __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, i
     const int e0 = min(tid * KPT, keys), e1 = min(e0 + KPT, keys);
     int2 sum = make_int2(0, 0);
     for (int e = e0; e < e1; ++e) {
-        int all = before[e] + after[e];
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) all += before[e][i] + after[e][i];
 #pragma unroll
         for (int w = 0; w < GW; ++w) all += cur[w][e];
         offs[e] = all;
@@ -149,7 +175,9 @@ __global__ __launch_bounds__(GW * 64) void group_kernel(GroupArgs a, int bits, i
     int px = inc.x - sum.x, py = inc.y - sum.y;
     for (int e = e0; e < e1; ++e) {
         const int all = offs[e];
-        int c[GW], run = px + before[e];
+        int c[GW], run = px;
+#pragma unroll
+        for (int i = 0; i < C; ++i) run += before[e][i];
 #pragma unroll
         for (int w = 0; w < GW; ++w) c[w] = cur[w][e];
 #pragma unroll
@@ -404,13 +432,13 @@ PlanLayout plan_layout(int64_t E, int64_t P) {
     L.pos_off = L.order_off + round_up(P * 4, REGION_ALIGN);
     L.units_off = L.pos_off + round_up(P * 4, REGION_ALIGN);
     L.scratch_off = L.units_off + round_up(L.nunits * 16, REGION_ALIGN);
-    L.bytes = L.scratch_off + (group_counts_first(P) ? round_up(group_blocks(P, 0) * (E + 1) * 4, REGION_ALIGN) : 0);
+    L.bytes = L.scratch_off + (group_counts_first(P) ? round_up(group_blocks(E, P) * (E + 1) * 4, REGION_ALIGN) : 0);
     return L;
 }
 
 template <int GW, int KEYS>
 static void launch_group(GroupArgs a, int bits, hipStream_t s) {
-    const int64_t blocks = group_blocks(a.P, GW * 64);
+    const int64_t blocks = group_blocks(a.E, a.P);
     const bool counted = group_counts_first(a.P);
     a.seg = (int)ceil_div(a.P, blocks);
     if (counted) hipLaunchKernelGGL((group_count_kernel<GW, KEYS>), dim3(blocks), dim3(GW * 64), 0, s, a);
@@ -432,9 +460,8 @@ hipError_t launch_group_rows(const int32_t* ids, int64_t E, int64_t P, void* pla
     a.nunits = (int)L.nunits;
     int bits = 1;
     while ((int64_t(1) << bits) < E + 1) ++bits;
-    // 16 waves while their counters fit in LDS (1024 keys: 64 KB), else 4 (4097 keys: 64 KB)
-    if (E + 1 <= 1024) launch_group<16, 1024>(a, bits, s);
-    else launch_group<4, 4097>(a, bits, s);
+    if (E + 1 <= SMALL_KEYS) launch_group<16, SMALL_KEYS>(a, bits, s);
+    else launch_group<4, MAX_KEYS>(a, bits, s);
     return hipGetLastError();
 }
 

@@ -273,3 +273,23 @@ def test_a_plan_of_another_batch_stays_inside_the_buffers(env):
     torch.cuda.synchronize()
     assert bool((frame[T * top_k:] == -7.0).all()) and bool((y[T:] == -7.0).all())
     assert bool(((frame == 1.0) | (frame == -7.0)).all()) and bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("T,top_k,E,away", [
+    (16384, 1, 64, 0.1), (16385, 1, 64, 0.1), (4096, 8, 64, 0.25), (9000, 2, 1023, 0.1),
+    (9000, 2, 1024, 0.1), (262144, 3, 7, 0.0), (40000, 1, 4096, 0.5)])
+def test_plans_of_one_and_of_two_launches(env, T, top_k, E, away):
+    """Around the number of pairs, and of groups, where the sort changes its form."""
+    test_plan_is_the_stable_sort(env, T, top_k, E, away)
+
+
+@pytest.mark.parametrize("P", [1000, 16384, 50000])
+def test_plan_of_runs(env, P):
+    """Sorted ids: whole waves of one group, and everything in one."""
+    torch, mmq = env
+    print(f"[case] plan of runs P={P}", flush=True)
+    for ids in (np.arange(P) * 5 // P, np.zeros(P), np.full(P, -1), np.arange(P) * 600 // P):
+        ids = ids.astype(np.int32)
+        plan = mmq.group_rows(torch.from_numpy(ids).cuda(), 600)
+        for name, g, w in zip(("offs", "order", "pos", "units"), mmq.group_views(plan, 600, P), rowmodel.plan(ids, 600)):
+            assert np.array_equal(g.cpu().numpy(), w), name
