@@ -237,11 +237,13 @@ def gemm_id_noalloc(wtype, packed, E: int, act, ids, T: int, top_k: int, N: int,
 # build their messages only when they fail.
 
 def _gpu(fn: str, *tensors) -> int:
-    """The current GPU's index, on which every tensor (None skipped) has to be."""
+    """The current GPU's index, on which every tensor (None skipped, not the first) has to be."""
     import torch
-    at = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    at = tensors[0].get_device()
+    if at >= 0 and at != torch._C._cuda_getDevice():
+        at = -1
     for t in tensors:
-        if t is not None and t.get_device() != at:
+        if t is not None and (at < 0 or t.get_device() != at):
             raise ValueError(f"{fn}: every tensor must be on the current GPU, got one on {t.device}")
     return at
 
@@ -264,7 +266,7 @@ def _scratch(fn: str, workspace) -> int:
 
 def _ld(fn: str, name: str, t, rows: int, cols: int, dtype) -> int:
     """The row stride of a [rows, cols] tensor of `dtype` whose columns are contiguous."""
-    if t.dtype is not dtype or t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.dtype is not dtype or t.shape != (rows, cols):
         raise ValueError(f"{fn}: {name} must be {dtype} {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
     ld, step = t.stride()
     if step != 1 and cols != 1:
@@ -273,7 +275,7 @@ def _ld(fn: str, name: str, t, rows: int, cols: int, dtype) -> int:
 
 
 def _flat(fn: str, name: str, t, shape, dtype):
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -295,14 +297,15 @@ def _plan_of(fn: str, plan, E: int, T: int, top_k: int):
         raise ValueError(f"{fn}: plan must be the {nbytes} bytes that group_rows returns for E={E}, T={T}, top_k={top_k}")
 
 
-def _new(shape, dtype, at: int, stream):
-    """A tensor for a call's result or workspace, from the memory of the call's own stream: what the
-    current stream's earlier work still uses is not handed to another stream's call."""
+def _new(like, shape, dtype, stream):
+    """A tensor on `like`'s GPU for a call's result or workspace, from the memory of the call's own
+    stream: what the current stream's earlier work still uses is not handed to another stream's
+    call. shape None: of `like`'s shape."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=at)
+        return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=at)
+        return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -331,7 +334,7 @@ def group_rows(ids, E: int, out=None, stream=None):
         nbytes = group_bytes(E, T, top_k)
         if nbytes == 0:
             raise MMQError("mmq_group_bytes", MMQ_EINVAL)
-        out = _new(nbytes, torch.uint8, at, stream)
+        out = _new(ids, nbytes, torch.uint8, stream)
     else:
         _plan_of(fn, out, E, T, top_k)
     _check("mmq_group_rows", lib().mmq_group_rows(ids.data_ptr(), E, T, top_k, out.data_ptr(), _raw_stream(stream, at)))
@@ -362,7 +365,7 @@ def moe_gather(x, plan, E: int, top_k: int, out=None, stream=None):
     T, N = x.shape
     _plan_of(fn, plan, E, T, top_k)
     if out is None:
-        out = _new((T * top_k, N), x.dtype, at, stream)
+        out = _new(x, (T * top_k, N), x.dtype, stream)
     ldx = _ld(fn, "x", x, T, N, x.dtype)
     ldr = _ld(fn, "out", out, T * top_k, N, x.dtype)
     _check("mmq_moe_gather", lib().mmq_moe_gather(o, x.data_ptr(), ldx, plan.data_ptr(), E, T, top_k, N,
@@ -396,7 +399,7 @@ def moe_combine(z, plan, E: int, T: int, top_k: int, weights=None, order="pair",
     if weights is not None:
         _flat(fn, "weights", weights, (T, top_k), torch.float32)
     if out is None:
-        out = _new((T, N), z.dtype, at, stream)
+        out = _new(z, (T, N), z.dtype, stream)
     ldy = _ld(fn, "out", out, T, N, z.dtype)
     _check("mmq_moe_combine", lib().mmq_moe_combine(o, z.data_ptr(), ldz, ROWORDER[order], _ptr(weights),
                                                     plan.data_ptr(), E, T, top_k, N, out.data_ptr(), ldy,
@@ -417,9 +420,9 @@ def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=
     _plan_of(fn, plan, E, T, top_k)
     lddy = _ld(fn, "dy", dy, T, N, z.dtype)
     if dz is None:
-        dz = _new(z.shape, z.dtype, at, stream)
+        dz = _new(z, None, None, stream)
     if dw is None:
-        dw = _new((T, top_k), torch.float32, at, stream)
+        dw = _new(weights, None, None, stream)
     z, rows = _pair_rows(fn, z, P), _pair_rows(fn, dz, P)
     ldz = _ld(fn, "z", z, P, N, z.dtype)
     lddz = _ld(fn, "dz", rows, P, N, z.dtype)
@@ -483,17 +486,17 @@ def lora(act, A, B, scale, plan, M: int, atype="q8_1", base=None, out=None, v=No
     d, E, R, K, N = _adapters(fn, act, A, B, scale, plan, M, at_)
     dt = torch.float32 if at_ == 0 else torch.bfloat16
     if out is None:
-        out = _new((M, N), dt, at, stream)
+        out = _new(act, (M, N), dt, stream) if base is None else _new(base, None, None, stream)
     if v is None:
-        v = _new((M, R), torch.float32, at, stream)
+        v = _new(scale, (M, R), torch.float32, stream)
     else:
         _flat(fn, "v", v, (M, R), torch.float32)
     if workspace is None:
         nbytes = lora_workspace_bytes(E, M, N, K, R)
         if nbytes:
-            workspace = _new(nbytes, torch.uint8, at, stream)
-    ldo = _ld(fn, "out", out, M, N, dt)
+            workspace = _new(act, nbytes, torch.uint8, stream)
     ldb = _ld(fn, "base", base, M, N, dt) if base is not None else 0
+    ldo = _ld(fn, "out", out, M, N, dt)
     _check("mmq_lora", lib().mmq_lora(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
                                       plan.data_ptr(), M, N, K, _ptr(base), ldb, out.data_ptr(), ldo, v.data_ptr(),
                                       _ptr(workspace), 0 if workspace is None else _scratch(fn, workspace),
@@ -524,19 +527,19 @@ def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None
     lddy = _ld(fn, "dy", dy, M, N, f32 if at_ == 0 else torch.bfloat16)
     _flat(fn, "v", v, (M, R), f32)
     if want_dx and dx is None:
-        dx = _new((M, K), f32, at, stream)
+        dx = _new(scale, (M, K), f32, stream)
     if dA is None:
-        dA = _new((E, R, K), f32, at, stream)
+        dA = _new(scale, (E, R, K), f32, stream)
     else:
         _flat(fn, "dA", dA, (E, R, K), f32)
     if dB is None:
-        dB = _new((E, N, R), f32, at, stream)
+        dB = _new(scale, (E, N, R), f32, stream)
     else:
         _flat(fn, "dB", dB, (E, N, R), f32)
     lddx = _ld(fn, "dx", dx, M, K, f32) if dx is not None else 0
     ldxb = _ld(fn, "dx_base", dx_base, M, K, f32) if dx_base is not None else 0
     if workspace is None:
-        workspace = _new(lora_grad_workspace_bytes(E, M, N, K, R), torch.uint8, at, stream)
+        workspace = _new(act, lora_grad_workspace_bytes(E, M, N, K, R), torch.uint8, stream)
     _check("mmq_lora_grad",
            lib().mmq_lora_grad(at_, act.data_ptr(), d, A.data_ptr(), B.data_ptr(), scale.data_ptr(), E, R,
                                plan.data_ptr(), M, N, K, v.data_ptr(), dy.data_ptr(), lddy, _ptr(dx_base), ldxb,
