@@ -155,7 +155,7 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs a, int ntiles)
 // workgroup's four waves the unit's rows; else 256 columns, rows past 16 in a loop) and works
 // alone: its loads depend on the unit, and the base on its rows, and on nothing else. RK: steps of
 // 32 ranks, their operands held; 0 for any number, loaded step by step. TAIL: N % 4 != 0.
-// 64 rows of 32 adapters, N = 14336, rank 32, f16: 11.9 us for 36 MB (3.0 TB/s): the vector unit
+// 64 rows of 32 adapters, N = 14336, rank 32, f16: 11.4 us for 36 MB (3.2 TB/s): the vector unit
 // (an f16 weight is split into two bf16 terms by every wave) and the launch's latencies.
 template <int RK, bool F16, bool BF16, bool TAIL>
 __global__ __launch_bounds__(LT) void lora_up_kernel(LoraArgs a, int ntiles, int tall) {

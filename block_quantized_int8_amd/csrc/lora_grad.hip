@@ -5,10 +5,10 @@
 // scale goes to u's side, so no activation is ever restored to f32 in memory.
 //
 // Two launches, each of two kinds of workgroups that need nothing of each other:
-//   1. u (16 rows, its eight waves share N) and dB_e (64 columns of N, the waves share the rows);
+//   1. u (16 rows, its eight waves share N) and dB_e (64 columns of N a workgroup or a wave);
 //      u is left in f32 and as bf16 terms in operand order;
-//   2. dA_e (one block of K, the waves share the rows) and dx (expand_body).
-// 2048 rows of 4 adapters 4096 x 4096, rank 16: 17.7 + 18.9 us. The first launch reads dy twice (71 MB
+//   2. dA_e (one block of K a workgroup or a wave) and dx (expand_body).
+// 2048 rows of 4 adapters 4096 x 4096, rank 16: 17.8 + 19.1 us. The first launch reads dy twice (71 MB
 // of L2 misses, 4.0 TB/s); the second moves 84 MB (4.4 TB/s), most of it dx's base and dx.
 // The workgroups that sum over rows own their output tile, so nothing is added across
 // workgroups and the sums have one order.
