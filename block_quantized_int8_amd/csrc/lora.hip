@@ -362,7 +362,8 @@ __global__ __launch_bounds__(SW * 64) void lora_small_kernel(LoraArgs a, int nti
             if (wave < RT && r < a.R) {
 #pragma unroll
                 for (int w = 0; w < SW; ++w) d += __builtin_bit_cast(f32x4, lds[w][wave][lane]);
-                if constexpr (!Q81) d *= a.sa[m];
+                if constexpr (!Q81)
+                    if (!none) d *= a.sa[m];           // 0 without an adapter, whatever the row's scale is
                 if (tile == 0 && c < rows) *reinterpret_cast<f32x4*>(a.v + (int64_t)m * a.R + r) = d;
             }
             store_terms(&vt[0][c][r], 16 * LD, d);

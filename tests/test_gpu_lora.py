@@ -336,3 +336,34 @@ def test_what_is_not_finite_stays_in_its_row(env, act, kind, M, N, K, R, E):
     assert bool(out2[M // 2].isnan().all())
     out[0, N - 1] = float("inf")                                 # a value added to the base alone
     assert torch.equal(out2[keep], out[keep])
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E", [
+    ("i8_token", "f16", 5, 70, 64, 16, 2), ("q8_1", "bf16", 40, 70, 64, 16, 2), ("i8_token", "bf16", 40, 1030, 96, 64, 3),
+    ("i8_token", "bf16", 150, 301, 512, 72, 3), ("q8_1", "f16", 150, 300, 512, 72, 3),
+    ("i8_token", "f16", 1100, 130, 64, 72, 3), ("q8_1", "bf16", 1100, 132, 64, 72, 3)])
+def test_rows_without_an_adapter_do_not_see_their_activations(env, act, kind, M, N, K, R, E):
+    """v = 0 and out = base, whatever such a row's activations hold, in one launch and in two."""
+    torch, mmq = env
+    print(f"[case] lora away {act} {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    ids = row_ids(M, E, "runs", 3)
+    away = [0, M // 2, M - 1]
+    ids[away] = [-1, E, -1]
+    r = np.random.default_rng([M, N])
+    q = r.integers(-127, 128, (M, K)).astype(np.int8)
+    s = r.random((M, K // 32) if act == "q8_1" else M).astype(np.float32)
+    A, B, scale = (t.cuda() for t in adapters(torch, kind, E, R, K, N, 8))
+    io = torch.float32 if act == "q8_1" else torch.bfloat16
+    base = torch.randn((M, N), generator=torch.Generator().manual_seed(4)).to(io).cuda()
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+
+    def run(scales):
+        buf = mmq.act_q8_1_pack_host(q, scales) if act == "q8_1" else mmq.act_i8_pack_host(q, scales)
+        return mmq.lora(torch.from_numpy(buf).cuda(), A, B, scale, plan, M, atype=act, base=base)
+    out, v = run(s)
+    for value in (np.nan, np.inf):
+        bad = s.copy()
+        bad[away] = value
+        out2, v2 = run(bad)
+        assert not bool(v2[away].any()) and torch.equal(out2[away], base[away]), value
+        assert torch.equal(out2, out) and torch.equal(v2, v), value
