@@ -7,8 +7,10 @@
 //
 // Products keep f32: an f32 value is exactly the sum of three bf16 terms of 8 significand bits
 // each (an f16 value of two), so a product of terms is exact in f32 and only the accumulation
-// rounds. Terms are cut off, not rounded, so that the rest is exact and of the same sign. Pairs
-// of terms below 2^-23 of the product are left out.
+// rounds. Terms are cut off, not rounded, so that the rest is exact and of the same sign: the second
+// is below 2^-7 of the value, the third below 2^-15. Only the pair of two third terms, below
+// 2^-30 of the product, is left out; without the pairs of a second and a third too, a product
+// would be up to 2^-21 of itself too small.
 #pragma once
 
 #include "mmq_internal.h"
@@ -115,6 +117,7 @@ template <bool F16> struct Weights {
 template <bool F16>
 __device__ inline f32x4 mfma_terms(const Weights<F16>& w, const u32x4* x, f32x4 acc) {
     if constexpr (F16) {
+        acc = mfma_bf16(w.t[1], x[2], acc);
         acc = mfma_bf16(w.t[1], x[1], acc);
         acc = mfma_bf16(w.t[0], x[2], acc);
         acc = mfma_bf16(w.t[1], x[0], acc);
@@ -129,6 +132,7 @@ __device__ inline f32x4 mfma_terms(const Weights<F16>& w, const u32x4* x, f32x4 
 template <bool F16>
 __device__ inline f32x4 terms_mfma(const u32x4* x, const Weights<F16>& w, f32x4 acc) {
     if constexpr (F16) {
+        acc = mfma_bf16(x[2], w.t[1], acc);
         acc = mfma_bf16(x[1], w.t[1], acc);
         acc = mfma_bf16(x[2], w.t[0], acc);
         acc = mfma_bf16(x[0], w.t[1], acc);

@@ -45,6 +45,8 @@ __device__ inline f32x4 mfma_grad(const Weights<F16>& w, const Grad<BF16>& x, f3
 // acc += a (three terms) times b, small products first
 template <int T> __device__ inline f32x4 mfma_3(const u32x4* a, const u32x4* b, f32x4 acc) {
     if constexpr (T == 3) {
+        acc = mfma_bf16(a[1], b[2], acc);
+        acc = mfma_bf16(a[2], b[1], acc);
         acc = mfma_bf16(a[0], b[2], acc);
         acc = mfma_bf16(a[1], b[1], acc);
         acc = mfma_bf16(a[2], b[0], acc);

@@ -327,9 +327,10 @@ mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const
  *
  * x^ are the values that the act buffer stands for: xs * xq (MMQ_ACT_Q8_1) or sa * a
  * (MMQ_ACT_I8_TOKEN), so the adapters see the same quantised activations as the projection.
- * A row without an adapter gets v = 0 and out = base. Products and sums are f32-exact products
- * with f32 sums (no operand is rounded); `out` is rounded once to its type. Results repeat bit
- * for bit. Adapters and scales must be finite. Where a row's other inputs are not, or a sum
+ * A row without an adapter gets v = 0 and out = base. No operand is rounded to fewer bits: a
+ * product is the sum of exact products of its factors' terms, all of them but what is below 2^-30
+ * of it. Sums are f32; v, and scale[e] * v where that is taken before the second product, are f32
+ * values; `out` is rounded once to its type. Results repeat bit for bit. Adapters and scales must be finite. Where a row's other inputs are not, or a sum
  * overflows, what depends on it by these formulas is not finite either (an infinity may come out
  * as NaN), and nothing else changes.
  * --------------------------------------------------------------------------------------- */
@@ -383,8 +384,9 @@ size_t mmq_lora_grad_workspace_bytes(int64_t E, int64_t M, int64_t N, int64_t K,
  *  dA, dB  (device) f32 [E][R][K] and [E][N][R], written whole (zeros for an adapter without rows)
  *  workspace (device) >= mmq_lora_grad_workspace_bytes(E, M, N, K, R) bytes, as for mmq_lora
  * Sizes, strides and errors as for mmq_lora; MMQ_EINVAL also where E * ceil(N/64) plus four for
- * each of the plan's units, or E * K/32 plus ceil(K/128) for each of them, reaches 2^23 - 512. f32
- * sums of exact products in an order fixed by the sizes and the plan. */
+ * each of the plan's units, or E * K/32 plus ceil(K/128) for each of them, reaches 2^23 - 512.
+ * Products and sums as for mmq_lora, in an order fixed by the sizes and the plan; u is an f32
+ * value, and so is u times a row's activation scale, which dA's products take. */
 mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void* A, const void* B,
                          const float* scale, int64_t E, int64_t R, const void* plan, int64_t M, int64_t N,
                          int64_t K, const float* v, const void* dy, int64_t lddy, const float* dx_base,

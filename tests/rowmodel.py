@@ -72,3 +72,11 @@ def lora_grad(x, A, B, scale, ids, v, dy, dx_base):
             to[1][e] = u.T @ f(x[at])
             to[2][e] = f(scale[e]) * (f(dy[at]).T @ f(v[at]))
     return res, mag
+
+
+def full_significands(r, n, bits):
+    """n values in [1, 2) of `bits` significand bits: random ones, and ones whose upper parts end in
+    ones, 1 + 2^-7 - 2^(1 - bits)."""
+    v = r.integers(1 << (bits - 1), 1 << bits, n)
+    v[::3] = (1 << (bits - 1)) + (1 << (bits - 8)) - 1
+    return v

@@ -367,3 +367,47 @@ def test_rows_without_an_adapter_do_not_see_their_activations(env, act, kind, M,
         out2, v2 = run(bad)
         assert not bool(v2[away].any()) and torch.equal(out2[away], base[away]), value
         assert torch.equal(out2, out) and torch.equal(v2, v), value
+
+
+def summands(total):
+    """(q, a): int8 and f16 values with sum q a = total (below 2^24)."""
+    q, a = [], []
+    while total >= 127:
+        h = np.float16(min(total // 127, 65504))
+        if int(h) > total // 127:
+            h = np.nextafter(h, np.float16(0))
+        q.append(127)
+        a.append(h)
+        total -= 127 * int(h)
+    return q + [1], a + [np.float16(total)]
+
+
+@pytest.mark.parametrize("M,N,K,R,launches", [(6, 70, 64, 8, 1), (6, 70, 512, 72, 2), (6, 68, 64, 72, 2)])
+def test_a_single_product_keeps_f32(env, M, N, K, R, launches):
+    """One f16 weight times one v of 24 bits a column, the scale a power of two. Both are exactly the
+    sums of their terms and all products of terms are added, the small ones first: only additions
+    round. The last is off by at most 2^-23 of the result, those before it by 2^-23 of partial sums
+    that are below 2^-6, 2^-7 and far less of it; together below (1 + 2^-4) 2^-23."""
+    torch, mmq = env
+    print(f"[case] lora one product M={M} N={N} K={K} R={R}", flush=True)
+    E, r = M, np.random.default_rng([M, N, K, R])
+    assert (mmq.lora_workspace_bytes(E, M, N, K, R) == 0) == (launches == 1)
+    V = rowmodel.full_significands(r, M, 24)                       # an adapter a row, of one rank that is not 0
+    q, A, at = np.zeros((M, K), np.int8), np.zeros((E, R, K), np.float16), r.integers(0, R, M)
+    for m in range(M):
+        qm, am = summands(int(V[m]))
+        where = r.permutation(K)[:len(qm)]
+        q[m, where], A[m, at[m], where] = qm, am
+    buf = mmq.act_q8_1_pack_host(q, np.full((M, K // 32), 2.0 ** -23, np.float32))
+    B = np.zeros((E, N, R), np.float16)
+    b = rowmodel.full_significands(r, (E, N), 11) * 2.0 ** -10
+    for m in range(M):
+        B[m, :, at[m]] = b[m]
+    scale = (2.0 ** (np.arange(E) % 3 - 1)).astype(np.float32)
+    plan = mmq.group_rows(torch.arange(M, dtype=torch.int32, device="cuda"), E)
+    out, v = mmq.lora(torch.from_numpy(buf).cuda(), torch.from_numpy(A).cuda(), torch.from_numpy(B).cuda(),
+                      torch.from_numpy(scale).cuda(), plan, M)
+    v64 = V * 2.0 ** -23
+    assert np.array_equal(host(v)[np.arange(M), at], v64)
+    want = scale[:, None].astype(np.float64) * v64[:, None] * b
+    assert np.all(np.abs(host(out) - want) <= (1 + 2.0 ** -4) * U23 * want)

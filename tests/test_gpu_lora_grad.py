@@ -320,3 +320,43 @@ def test_adapters_of_many_and_of_few_rows(env, act, kind, M, N, K, R, E, big):
     for name, g, w, m, n in zip(("dx", "dA", "dB"), got, want, mag, (nu + 5 * R + 8, nu + 3 * rows + 10, 6 * rows + 8)):
         assert np.all(np.abs(host(g) - w) <= n * U23 * m * 1.01), name
         assert np.linalg.norm(host(g) - w) <= 1e-6 * np.linalg.norm(w), name
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,R,E", [(5, 70, 64, 8, 5), (300, 131, 96, 40, 2), (20, 6500, 64, 72, 2)])
+def test_a_single_product_keeps_f32(env, kind, M, N, K, R, E):
+    """One row of each adapter has a gradient; its dy and v have 24 bits, a rank one weight, the
+    scale is a power of two. dB is one product of f32 values and u one of an f32 value with a weight:
+    all pairs of terms are added but one below 2^-30 of the product, the small ones first, so
+    that only additions round. The last is off by at most 2^-23 of the result, those before it by
+    2^-23 of partial sums that are below 2^-6, 2^-7 and far less of it; together with the pair
+    below (1 + 2^-4) 2^-23. dA is u itself (x^ = 1), dx one product of u."""
+    torch, mmq = env
+    print(f"[case] lora_grad one product {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    r = np.random.default_rng([M, N, K, R])
+    wbits = 11 if kind == "f16" else 8
+    ids = (np.arange(M) % E).astype(np.int32)
+    hot = np.arange(M - E, M)                             # the last rows: one of each adapter
+    e_of = ids[hot]
+    dy, v = np.zeros((M, N), np.float32), np.zeros((M, R), np.float32)
+    dy[hot] = rowmodel.full_significands(r, (E, N), 24) * 2.0 ** -23
+    v[hot] = rowmodel.full_significands(r, (E, R), 24) * 2.0 ** -23
+    A, B = np.zeros((E, R, K), np.float32), np.zeros((E, N, R), np.float32)
+    n_of, r_of = r.integers(0, N, R), r.integers(0, R, K)
+    B[:, n_of, np.arange(R)] = rowmodel.full_significands(r, (E, R), wbits) * 2.0 ** (1 - wbits)
+    A[:, r_of, np.arange(K)] = rowmodel.full_significands(r, (E, K), wbits) * 2.0 ** (1 - wbits)
+    scale = (2.0 ** (np.arange(E) % 3 - 1)).astype(np.float32)
+    buf = mmq.act_q8_1_pack_host(np.ones((M, K), np.int8), np.ones((M, K // 32), np.float32))
+    dt = torch.float16 if kind == "f16" else torch.bfloat16
+    dx, dA, dB = mmq.lora_grad(torch.from_numpy(buf).cuda(), torch.from_numpy(A).to(dt).cuda(),
+                               torch.from_numpy(B).to(dt).cuda(), torch.from_numpy(scale).cuda(),
+                               mmq.group_rows(torch.from_numpy(ids).cuda(), E), torch.from_numpy(v).cuda(),
+                               torch.from_numpy(dy).cuda())
+    s, one = scale[e_of].astype(np.float64), (1 + 2.0 ** -4) * U23
+    want = s[:, None, None] * dy[hot].astype(np.float64)[:, :, None] * v[hot][:, None, :]
+    assert np.all(np.abs(host(dB)[e_of] - want) <= one * want)
+    u = s[:, None] * dy[hot].astype(np.float64)[:, n_of] * B[e_of][:, n_of, np.arange(R)]
+    got = host(dA)[e_of]
+    assert np.all(np.abs(got - u[:, :, None]) <= one * u[:, :, None])
+    want = u[:, r_of] * A[e_of][:, r_of, np.arange(K)]
+    assert np.all(np.abs(host(dx)[hot] - want) <= one * (2 + one) * want)
