@@ -308,6 +308,15 @@ def _new(like, shape, dtype, stream):
         return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
 
 
+def _zeros(like, stream):
+    """As _new, of `like`'s shape and filled with zeros on the call's stream."""
+    import torch
+    if stream is None:
+        return torch.zeros_like(like)
+    with torch.cuda.stream(stream):
+        return torch.zeros_like(like)
+
+
 @functools.lru_cache(maxsize=4096)
 def group_bytes(E: int, T: int, top_k: int) -> int:
     return int(lib().mmq_group_bytes(E, T, top_k))
@@ -356,7 +365,9 @@ def group_views(plan, E: int, T: int, top_k: int = 1):
 
 
 def moe_gather(x, plan, E: int, top_k: int, out=None, stream=None):
-    """Token rows x (CUDA float32 or bfloat16 [T, N]) in expert order: [T * top_k, N]."""
+    """Token rows x (CUDA float32 or bfloat16 [T, N]) in expert order: [T * top_k, N]. The rows past
+    the last pair with an expert (from the plan's offs[E] on) are not written: in a tensor made here
+    they hold whatever its memory held."""
     fn = "moe_gather"
     at = _gpu(fn, x, plan, out)
     o = _row_otype(fn, x)
@@ -408,7 +419,9 @@ def moe_combine(z, plan, E: int, T: int, top_k: int, weights=None, order="pair",
 
 
 def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=None, dw=None, stream=None):
-    """Gradients of moe_combine for the rows and the weights: dz like z, dw float32 [T, top_k]."""
+    """Gradients of moe_combine for the rows and the weights: dz like z, dw float32 [T, top_k]. Rows of
+    dz that no pair has (moe_combine does not read them) are zeros where dz is made here, and left as
+    they are in a dz that is given, which saves the fill."""
     import torch
     fn = "moe_combine_grad"
     at = _gpu(fn, dy, z, plan, weights, dz, dw)
@@ -420,7 +433,7 @@ def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=
     _plan_of(fn, plan, E, T, top_k)
     lddy = _ld(fn, "dy", dy, T, N, z.dtype)
     if dz is None:
-        dz = _new(z, None, None, stream)
+        dz = _zeros(z, stream)
     if dw is None:
         dw = _new(weights, None, None, stream)
     z, rows = _pair_rows(fn, z, P), _pair_rows(fn, dz, P)

@@ -293,3 +293,29 @@ def test_plan_of_runs(env, P):
         plan = mmq.group_rows(torch.from_numpy(ids).cuda(), 600)
         for name, g, w in zip(("offs", "order", "pos", "units"), mmq.group_views(plan, 600, P), rowmodel.plan(ids, 600)):
             assert np.array_equal(g.cpu().numpy(), w), name
+
+
+@pytest.mark.parametrize("order", ["pair", "sorted"])
+@pytest.mark.parametrize("dims", [2, 3])
+def test_gradient_rows_of_pairs_without_an_expert_are_zeros(env, order, dims):
+    """Where the binding makes dz itself, it holds no earlier tensor's values: a row that the
+    forward call does not read has a gradient of zeros."""
+    torch, mmq = env
+    T, top_k, E, N = 40, 3, 5, 70
+    ids = _ids(T, top_k, E, 0.3, 12)
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    g = torch.Generator().manual_seed(1)
+    z, dy = torch.randn((T * top_k, N), generator=g).cuda(), torch.randn((T, N), generator=g).cuda()
+    w = torch.randn((T, top_k), generator=g).cuda()
+    want, dw = mmq.moe_combine_grad(dy, z, plan, E, top_k, w, order=order, dz=torch.zeros_like(z))
+    if dims == 3:
+        z = z.view(T, top_k, N)
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            used = [torch.full_like(z, float("nan")) for _ in range(4)]
+        torch.cuda.synchronize()
+        del used                                          # the next tensors of that size get this memory
+        dz, dw2 = mmq.moe_combine_grad(dy, z, plan, E, top_k, w, order=order, stream=stream)
+        torch.cuda.synchronize()
+        assert dz.shape == z.shape and torch.equal(dz.view(-1, N), want) and torch.equal(dw2, dw)
