@@ -526,8 +526,8 @@ def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None
               want_dx: bool = True, workspace=None, stream=None):
     """Gradients of lora from its 8-bit activations: dy [M, N] float32 (q8_1) or bfloat16
     (i8_token), v as lora returned it, the other inputs as given to it. Returns (dx, dA, dB) in
-    float32: dx [M, K] = dx_base + the adapters' part (dx=dx_base adds in place; None with
-    want_dx=False), dA and dB like A and B."""
+    float32: dx [M, K] = dx_base + the adapters' part (dx=dx_base adds in place; with want_dx=False
+    None, and a dx that is given is left as it is), dA and dB like A and B."""
     import torch
     fn = "lora_grad"
     at = _gpu(fn, act, A, B, scale, plan, v, dy, dx_base, dx, dA, dB, workspace)
@@ -539,7 +539,9 @@ def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None
     f32 = torch.float32
     lddy = _ld(fn, "dy", dy, M, N, f32 if at_ == 0 else torch.bfloat16)
     _flat(fn, "v", v, (M, R), f32)
-    if want_dx and dx is None:
+    if not want_dx:
+        dx = None
+    elif dx is None:
         dx = _new(scale, (M, K), f32, stream)
     if dA is None:
         dA = _new(scale, (E, R, K), f32, stream)

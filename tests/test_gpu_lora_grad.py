@@ -360,3 +360,16 @@ def test_a_single_product_keeps_f32(env, kind, M, N, K, R, E):
     assert np.all(np.abs(got - u[:, :, None]) <= one * u[:, :, None])
     want = u[:, r_of] * A[e_of][:, r_of, np.arange(K)]
     assert np.all(np.abs(host(dx)[hot] - want) <= one * (2 + one) * want)
+
+
+def test_no_dx_where_none_is_wanted(env):
+    """want_dx=False returns None and writes no dx, given or not."""
+    torch, mmq = env
+    ids, buf, _, A, B, scale, dy, v, dxb = problem(torch, mmq, "q8_1", "bf16", 40, 70, 64, 16, 3, "runs")
+    args = [t.cuda() for t in (torch.from_numpy(buf), A, B, scale)] + [mmq.group_rows(torch.from_numpy(ids).cuda(), 3)]
+    args += [v.cuda(), dy.cuda()]
+    _, dA, dB = mmq.lora_grad(*args)
+    dx = torch.full((40, 64), -7.0, device="cuda")
+    got = mmq.lora_grad(*args, dx=dx, dx_base=dxb.cuda(), want_dx=False)
+    assert got[0] is None and torch.equal(got[1], dA) and torch.equal(got[2], dB)
+    assert bool((dx == -7.0).all())
