@@ -387,12 +387,21 @@ def moe_gather(x, plan, E: int, top_k: int, out=None, stream=None):
 ROWORDER = {"pair": 0, "sorted": 1}
 
 
+def _row_order(fn: str, order) -> int:
+    r = ROWORDER.get(order)
+    if r is None:
+        raise ValueError(f"{fn}: order must be one of {list(ROWORDER)}, got {order!r}")
+    return r
+
+
 def _pair_rows(fn: str, z, P: int):
     """z [P, N], or [T, top_k, N] as gemm_id returns it, as [P, N]."""
-    if z.dim() == 3:
-        z = z.view(-1, z.shape[2])
+    shape = z.shape
+    if len(shape) == 3 and (shape[0] == 1 or shape[1] == 1 or z.stride(0) == shape[1] * z.stride(1)):
+        z = z.view(shape[0] * shape[1], shape[2])
     if z.dim() != 2 or z.shape[0] != P:
-        raise ValueError(f"{fn}: the pairs' rows must be [T * top_k, N] or [T, top_k, N] with {P} pairs, got {tuple(z.shape)}")
+        raise ValueError(f"{fn}: the pairs' rows must be [T * top_k, N], or [T, top_k, N] with one stride, and "
+                         f"{P} pairs, got {tuple(shape)} with strides {z.stride()}")
     return z
 
 
@@ -403,6 +412,7 @@ def moe_combine(z, plan, E: int, T: int, top_k: int, weights=None, order="pair",
     fn = "moe_combine"
     at = _gpu(fn, z, plan, weights, out)
     o = _row_otype(fn, z)
+    r = _row_order(fn, order)
     _plan_of(fn, plan, E, T, top_k)
     z = _pair_rows(fn, z, T * top_k)
     N = z.shape[1]
@@ -412,7 +422,7 @@ def moe_combine(z, plan, E: int, T: int, top_k: int, weights=None, order="pair",
     if out is None:
         out = _new(z, (T, N), z.dtype, stream)
     ldy = _ld(fn, "out", out, T, N, z.dtype)
-    _check("mmq_moe_combine", lib().mmq_moe_combine(o, z.data_ptr(), ldz, ROWORDER[order], _ptr(weights),
+    _check("mmq_moe_combine", lib().mmq_moe_combine(o, z.data_ptr(), ldz, r, _ptr(weights),
                                                     plan.data_ptr(), E, T, top_k, N, out.data_ptr(), ldy,
                                                     _raw_stream(stream, at)))
     return out
@@ -426,6 +436,7 @@ def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=
     fn = "moe_combine_grad"
     at = _gpu(fn, dy, z, plan, weights, dz, dw)
     o = _row_otype(fn, z)
+    r = _row_order(fn, order)
     if dy.dim() != 2:
         raise ValueError(f"{fn}: dy must be [T, N], got {tuple(dy.shape)}")
     T, N = dy.shape
@@ -442,7 +453,7 @@ def moe_combine_grad(dy, z, plan, E: int, top_k: int, weights, order="pair", dz=
     _flat(fn, "weights", weights, (T, top_k), torch.float32)
     _flat(fn, "dw", dw, (T, top_k), torch.float32)
     _check("mmq_moe_combine_grad",
-           lib().mmq_moe_combine_grad(o, dy.data_ptr(), lddy, z.data_ptr(), ldz, ROWORDER[order], weights.data_ptr(),
+           lib().mmq_moe_combine_grad(o, dy.data_ptr(), lddy, z.data_ptr(), ldz, r, weights.data_ptr(),
                                       plan.data_ptr(), E, T, top_k, N, rows.data_ptr(), lddz, dw.data_ptr(),
                                       _raw_stream(stream, at)))
     return dz, dw

@@ -106,3 +106,16 @@ def test_binding_refuses_another_gpus_stream(mmq):
     with pytest.raises(ValueError, match="stream"):
         mmq._raw_stream(Stream, 0)
     assert mmq._raw_stream(Stream, 1) == 0
+
+
+def test_binding_refuses_rows_and_orders_it_does_not_know(mmq):
+    import torch
+    assert mmq._pair_rows("f", torch.zeros(4, 2, 64), 8).shape == (8, 64)
+    assert mmq._pair_rows("f", torch.zeros(4, 2, 70)[:, :, :64], 8).stride() == (70, 1)
+    for z in (torch.zeros(2, 4, 64).transpose(0, 1), torch.zeros(4, 3, 64)[:, :2], torch.zeros(64), torch.zeros(9, 64)):
+        with pytest.raises(ValueError, match="pairs' rows"):
+            mmq._pair_rows("f", z, 8)
+    assert [mmq._row_order("f", r) for r in ("pair", "sorted")] == [0, 1]
+    for r in ("expert", "", None, 2):
+        with pytest.raises(ValueError, match="order"):
+            mmq._row_order("f", r)
