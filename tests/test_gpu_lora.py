@@ -411,3 +411,83 @@ def test_a_single_product_keeps_f32(env, M, N, K, R, launches):
     assert np.array_equal(host(v)[np.arange(M), at], v64)
     want = scale[:, None].astype(np.float64) * v64[:, None] * b
     assert np.all(np.abs(host(out) - want) <= (1 + 2.0 ** -4) * U23 * want)
+
+
+# sizes past the one-launch form, with the parts of K that the first of two launches has
+TWO = [
+    ("q8_1", "bf16", 10, 128, 16416, 16, 8, "mixed", 8),       # few rows an adapter
+    ("i8_token", "f16", 100, 130, 16416, 16, 8, "one", 8),     # all rows with one of several adapters
+    ("q8_1", "f16", 100, 260, 8224, 32, 2, "runs", 8), ("i8_token", "bf16", 37, 301, 8224, 40, 3, "mixed", 8),
+    ("q8_1", "bf16", 90, 303, 11040, 24, 2, "mixed", 8), ("q8_1", "bf16", 150, 516, 4128, 64, 9, "mixed", 4),
+    ("i8_token", "f16", 33, 132, 4128, 64, 3, "one", 8),
+    ("q8_1", "f16", 64, 6148, 4096, 32, 32, "mixed", 2), ("i8_token", "bf16", 40, 6150, 4096, 24, 30, "mixed", 2),
+    ("q8_1", "bf16", 1100, 4100, 2048, 32, 3, "runs", 1), ("i8_token", "f16", 1030, 4099, 2048, 32, 2, "runs", 1),
+    ("q8_1", "f16", 1100, 132, 8224, 64, 3, "mixed", 1), ("i8_token", "bf16", 1040, 260, 16416, 16, 2, "runs", 1)]
+
+
+def parts_workspace(M, R, S):
+    return -(-M * R * (4 * S if S > 1 else 6) // 256) * 256
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E,how,S", TWO)
+def test_forward_in_two_launches(env, act, kind, M, N, K, R, E, how, S):
+    assert env[1].lora_workspace_bytes(E, M, N, K, R) == parts_workspace(M, R, S)
+    test_forward(env, act, kind, M, N, K, R, E, how)
+
+
+@pytest.mark.parametrize("case", [TWO[1], TWO[3], TWO[7], TWO[10]])
+def test_two_launches_do_not_read_what_the_workspace_held(env, case):
+    torch, mmq = env
+    act, kind, M, N, K, R, E, how, S = case
+    print(f"[case] lora workspace {case}", flush=True)
+    ids = row_ids(M, E, how, 1)
+    dev = [t.cuda() for t in (torch.from_numpy(activations(mmq, act, M, K, 2)[0]), *adapters(torch, kind, E, R, K, N, 3))]
+    plan = mmq.group_rows(torch.from_numpy(ids).cuda(), E)
+    need = mmq.lora_workspace_bytes(E, M, N, K, R)
+    assert need == parts_workspace(M, R, S)
+    want = None
+    for fill in (0, 255):                                  # bytes of 255: NaN in f32 and in bf16
+        ws = torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda")
+        out, v = mmq.lora(*dev, plan, M, atype=act, workspace=ws[:need])
+        assert bool((ws[need:] == fill).all())
+        if want is not None:
+            assert torch.equal(out, want[0]) and torch.equal(v, want[1])
+        want = out, v
+    assert bool(out.isfinite().all())
+
+
+def test_two_launches_in_a_graph_and_on_streams(env):
+    """As test_graph_and_streams, at sizes that need a workspace: each call's is its own."""
+    torch, mmq = env
+    M, N, K, R, E = 77, 300, 8224, 32, 6
+    assert mmq.lora_workspace_bytes(E, M, N, K, R) == parts_workspace(M, R, 8)
+    A, B, scale = (t.cuda() for t in adapters(torch, "f16", E, R, K, N, 8))
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    base = torch.zeros((M, N), device="cuda")
+    acts = [torch.zeros(mmq.act_bytes("q8_1", M, K), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    got = {}
+
+    def path(act, stream=None):
+        return mmq.lora(act, A, B, scale, mmq.group_rows(ids, E, stream=stream), M, base=base, stream=stream)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        path(acts[0])
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got["out"] = [path(a) for a in acts]
+    for rep in range(4):
+        for i, a in enumerate(acts):
+            a.copy_(torch.from_numpy(activations(mmq, "q8_1", M, K, 30 + 2 * rep + i)[0]))
+        ids.copy_(torch.from_numpy(row_ids(M, E, ["mixed", "runs", "one", "none"][rep], rep)))
+        base.normal_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        every = [(i, path(acts[i], s)) for i, s in ((0, s1), (1, s2), (1, s1), (0, s2))]
+        torch.cuda.synchronize()
+        for i, (out, v) in every:
+            assert torch.equal(out, got["out"][i][0]) and torch.equal(v, got["out"][i][1]), rep

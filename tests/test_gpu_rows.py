@@ -319,3 +319,46 @@ def test_gradient_rows_of_pairs_without_an_expert_are_zeros(env, order, dims):
         dz, dw2 = mmq.moe_combine_grad(dy, z, plan, E, top_k, w, order=order, stream=stream)
         torch.cuda.synchronize()
         assert dz.shape == z.shape and torch.equal(dz.view(-1, N), want) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("T,top_k,E,N,K,away", [(3, 2, 4, 96, 256, 0.0), (10, 8, 16, 130, 512, 0.2), (70, 3, 8, 97, 256, 0.2)])
+def test_after_the_expert_products(env, T, top_k, E, N, K, away):
+    """The run that the pair order is made for, as a layer makes it: quantise, the experts' products
+    (mmq_gemm_id, of decode and of prefill sizes) into rows of pairs, the weighted sum of these rows
+    as they come, [T, top_k, N], and its gradients; against the oracle's products and 64-bit sums."""
+    torch, mmq = env
+    import gen
+    import oracle
+    oracle.build()
+    print(f"[case] gemm_id and combine T={T} top_k={top_k} E={E} N={N} K={K}", flush=True)
+    raw = gen.moe_weights("q4_0", E, N, K, seed=2, cfg=143)
+    xh = gen.act_f32(T, K, seed=3, cfg=143)
+    ids = _ids(T, top_k, E, away, 13)
+    pb = mmq.packed_bytes("q4_0", N, K)
+    packed = torch.empty(E * pb, dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        mmq.repack_weights("q4_0", torch.from_numpy(np.ascontiguousarray(raw[e])).cuda(), N, K, out=packed[e * pb:(e + 1) * pb])
+    ids_d = torch.from_numpy(ids).cuda()
+    act = mmq.quantize_act(torch.from_numpy(xh).cuda())
+    z = torch.full((T, top_k, N), float("nan"), device="cuda")        # what the products leave unwritten
+    mmq.gemm_id("q4_0", packed, E, act, ids_d, T, top_k, N, K, out=z)
+    plan = mmq.group_rows(ids_d, E)
+    g = torch.Generator().manual_seed(5)
+    w = torch.randn((T, top_k), generator=g).softmax(1).cuda()
+    dy = torch.randn((T, N), generator=g).cuda()
+    y = mmq.moe_combine(z, plan, E, T, top_k, weights=w)
+    dz, dw = mmq.moe_combine_grad(dy, z, plan, E, top_k, w)
+    there = (ids >= 0)[:, :, None]
+    rq, rs, _ = oracle.quantize_q8_1(xh)
+    ref = np.where(there, oracle.moe_f64("q4_0", raw.reshape(E * N, -1), E, N, K, rq, rs, ids), 0.0)
+    zh, wh = np.where(there, _host(z), 0.0), _host(w)[:, :, None]
+    # softmax weights: the sum is off by no more than the products' own gate of their largest value
+    assert np.max(np.abs(_host(y) - (wh * ref).sum(1))) <= 1e-3 * np.max(np.abs(ref))
+    terms = wh * zh
+    assert np.all(np.abs(_host(y) - terms.sum(1)) <= np.abs(terms).sum(1) * top_k * U24 * 1.01)
+    want = np.where(there, wh * _host(dy)[:, None, :], 0.0)
+    got = _host(dz)
+    assert dz.shape == z.shape and np.all((np.abs(got - want) <= np.abs(want) * U24)[ids >= 0])
+    terms = _host(dy)[:, None, :] * zh
+    assert np.all(np.abs(_host(dw) - terms.sum(2)) <= np.abs(terms).sum(2) * (N + 10) * U24 * 1.01)
+    assert not dw.cpu().numpy()[ids < 0].any()
