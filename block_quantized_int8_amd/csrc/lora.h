@@ -337,7 +337,7 @@ __device__ inline void expand_body(const LoraArgs& a, const uint16_t* weights, i
     for (int j = 0; j < 4; ++j) m[j] = row_at(a, unit.y + min(16 * t + 4 * g + j, unit.z - 1));
     f32x4 acc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = 0;
+    for (int i = 0; i < 4; ++i) acc[i] = f32x4(none ? -0.f : 0.f);     // base + -0 is the base, -0 too
     typename Quad<BF16>::Raw base[4];
 #pragma unroll 1
     for (int r0 = 0; r0 < a.R; r0 += LORA_RC) {

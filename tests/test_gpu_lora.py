@@ -491,3 +491,23 @@ def test_two_launches_in_a_graph_and_on_streams(env):
         torch.cuda.synchronize()
         for i, (out, v) in every:
             assert torch.equal(out, got["out"][i][0]) and torch.equal(v, got["out"][i][1]), rep
+
+
+@pytest.mark.parametrize("act,kind,M,N,K,R,E", [
+    ("q8_1", "bf16", 40, 70, 64, 16, 2), ("i8_token", "f16", 40, 68, 64, 16, 2), ("q8_1", "f16", 150, 301, 512, 72, 3),
+    ("i8_token", "bf16", 150, 300, 512, 72, 3), ("q8_1", "bf16", 1100, 132, 64, 72, 3), ("i8_token", "f16", 1100, 130, 64, 72, 3)])
+def test_rows_without_an_adapter_are_the_base_bit_for_bit(env, act, kind, M, N, K, R, E):
+    """In one launch and in two: zeros keep their sign, denormal values and infinities stay."""
+    torch, mmq = env
+    print(f"[case] lora base bits {act} {kind} M={M} N={N} K={K} R={R} E={E}", flush=True)
+    ids = row_ids(M, E, "runs", 3)
+    ids[::3] = -1
+    away = torch.from_numpy((ids < 0) | (ids >= E)).cuda()
+    io, bits = (torch.float32, torch.int32) if act == "q8_1" else (torch.bfloat16, torch.int16)
+    A, B, scale = (t.cuda() for t in adapters(torch, kind, E, R, K, N, 8))
+    buf = torch.from_numpy(activations(mmq, act, M, K, 2)[0]).cuda()
+    base = torch.randn((M, N), generator=torch.Generator().manual_seed(4)).to(io).cuda()
+    for i, value in enumerate((-0.0, 0.0, 1e-40, float("inf"), -float("inf"))):
+        base[:, i::11] = value
+    out, _ = mmq.lora(buf, A, B, scale, mmq.group_rows(torch.from_numpy(ids).cuda(), E), M, atype=act, base=base)
+    assert torch.equal(out[away].view(bits), base[away].view(bits))

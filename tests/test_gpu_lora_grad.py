@@ -373,3 +373,14 @@ def test_no_dx_where_none_is_wanted(env):
     got = mmq.lora_grad(*args, dx=dx, dx_base=dxb.cuda(), want_dx=False)
     assert got[0] is None and torch.equal(got[1], dA) and torch.equal(got[2], dB)
     assert bool((dx == -7.0).all())
+
+
+def test_dx_of_rows_without_an_adapter_is_its_base_bit_for_bit(env):
+    torch, mmq = env
+    ids, buf, _, A, B, scale, dy, v, dxb = problem(torch, mmq, "q8_1", "bf16", 90, 70, 96, 16, 3, "mixed")
+    away = torch.from_numpy((ids < 0) | (ids >= 3))
+    for i, value in enumerate((-0.0, 0.0, 1e-40, float("inf"), -float("inf"))):
+        dxb[:, i::11] = value
+    dx, _, _ = mmq.lora_grad(*(t.cuda() for t in (torch.from_numpy(buf), A, B, scale)),
+                             mmq.group_rows(torch.from_numpy(ids).cuda(), 3), v.cuda(), dy.cuda(), dx_base=dxb.cuda())
+    assert bool(away.any()) and torch.equal(dx.cpu()[away].view(torch.int32), dxb[away].view(torch.int32))
