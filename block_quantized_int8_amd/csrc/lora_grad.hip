@@ -8,8 +8,8 @@
 //   1. u (16 rows, its eight waves share N) and dB_e (64 columns of N a workgroup or a wave);
 //      u is left in f32 and as bf16 terms in operand order;
 //   2. dA_e (one block of K a workgroup or a wave) and dx (expand_body).
-// 2048 rows of 4 adapters 4096 x 4096, rank 16: 17.8 + 19.1 us. The first launch reads dy twice (71 MB
-// of L2 misses, 4.0 TB/s); the second moves 84 MB (4.4 TB/s), most of it dx's base and dx.
+// 2048 rows of 4 adapters 4096 x 4096, rank 16: 17.8 + 19.4 us. The first launch reads dy twice (71 MB
+// of L2 misses, 4.0 TB/s); the second moves 84 MB (4.3 TB/s), most of it dx's base and dx.
 // The workgroups that sum over rows own their output tile, so nothing is added across
 // workgroups and the sums have one order.
 #include <algorithm>
@@ -108,7 +108,15 @@ constexpr int MAX_U_PARTS = 8;
 // blocks enough for the chip. Measured, all alone against all shared (us a call): 41 rows of 4
 // adapters, N = 10342, rank 64: first launch 11.8, 27.4; 800 rows of 8, 4096 x 4096, rank 64: 31.4,
 // 42.8; 200 rows of 2: 26.8, 23.8; 1200 rows of 8: 42.2, 52.0; 4096 rows of 8, rank 16: 94.6, 69.4.
+// Enough are FULL_B of dB's blocks and FULL_A of dA's. Measured by the launch (us; 100, 160 and 240 rows
+// an adapter, several adapters of N = K): sharing against alone. dB, rank 64, 256 blocks: 18.7 20.6 21.4
+// against 21.2 24.1 33.2; 512: 27.7 30.2 31.3, 23.0 26.3 35.5; 1024: 46.6 55.0 61.4, 31.9 36.7
+// 53.1; rank 16, 512: 15.0 16.4 17.8, 14.7 17.1 22.7; 1792: 27.7 39.4 47.7, 30.7 39.0 51.4. dA, rank 64,
+// 1024: 9.1 10.9 11.6, 10.0 11.9 16.3; 1792: 14.0 16.2 17.7, 11.1 13.0 17.3; rank 16, 1024: 6.0 6.7
+// 7.0, 6.4 7.5 10.1; 1792: 9.1 9.7 10.3, 7.1 7.8 10.5. (So at rank 16 dB, and at 1024 blocks dA, the
+// sharing would still be the faster.)
 constexpr int FEW = 64, FEW_FULL = 256;
+constexpr int FULL_B = 512, FULL_A = 1024;
 constexpr int MANY_MAX = 512;       // workgroups that share rows, where the plan has such adapters
 
 // four ranks of a row's u, in f32 and as terms
@@ -257,6 +265,8 @@ template <typename Body> __device__ inline void each_sum(const LoraArgs& a, cons
         const int2 r = rows_of_group(a, e);
         return r.y - r.x;
     };
+    // `few` is chosen by the adapters in use among the first 64: one load, while all of 4096 would be
+    // 64 one after another in every workgroup. Where only later ones are in use it is FEW.
     int e0 = 0, few;
     uint64_t big;                                          // which of 64 adapters from e0 on have many rows
     {
@@ -498,7 +508,7 @@ __global__ __launch_bounds__(GW * 64) void lora_grad2_kernel(LoraArgs a, int kti
 
 constexpr int DX_COLS = 16 * GW;                           // columns of a dx workgroup
 
-// `blocks` of an adapter's output, and where they count as enough to fill the chip with a wave each
+// `blocks` of an adapter's output, and how many of all adapters in use are enough for the chip
 SumGrid sum_grid(const LoraArgs& a, int64_t blocks, int full) {
     const int64_t big = std::min<int64_t>(a.E, a.M / (FEW + 1));       // adapters of many rows at most
     return SumGrid{(int)blocks, (int)ceil_div(blocks, GW), (int)std::min<int64_t>(MANY_MAX, big * blocks), full};
@@ -507,7 +517,7 @@ SumGrid sum_grid(const LoraArgs& a, int64_t blocks, int full) {
 template <int RT>
 void launch_grads(const LoraArgs& a, bool f16, bool q81, hipStream_t s) {
     const unsigned rc = (unsigned)ceil_div(a.R, LORA_RC);
-    const SumGrid sb = sum_grid(a, ceil_div(a.N, 64), 512), sa = sum_grid(a, a.KB, 1024);
+    const SumGrid sb = sum_grid(a, ceil_div(a.N, 64), FULL_B), sa = sum_grid(a, a.KB, FULL_A);
     const int kt = (int)ceil_div(a.K, DX_COLS);
     const dim3 g1((unsigned)(4 * a.nunits * a.S + sb.many + a.E * sb.one), rc);
     const dim3 g2((unsigned)(sa.many + a.E * sa.one + (a.dx ? a.nunits * kt : 0)), rc);
