@@ -362,3 +362,33 @@ def test_after_the_expert_products(env, T, top_k, E, N, K, away):
     terms = _host(dy)[:, None, :] * zh
     assert np.all(np.abs(_host(dw) - terms.sum(2)) <= np.abs(terms).sum(2) * (N + 10) * U24 * 1.01)
     assert not dw.cpu().numpy()[ids < 0].any()
+
+
+@pytest.mark.parametrize("order", ["pair", "sorted"])
+def test_gradient_rows_are_zeros_on_every_replay(env, order):
+    """A captured call fills its dz again on each replay, where other ids leave other rows out."""
+    torch, mmq = env
+    T, top_k, E, N = 60, 3, 5, 130
+    ids = torch.from_numpy(_ids(T, top_k, E, 0.3, 30)).cuda()
+    z, dy, w = torch.randn((T, top_k, N), device="cuda"), torch.randn((T, N), device="cuda"), torch.randn((T, top_k), device="cuda")
+
+    def path():
+        return mmq.moe_combine_grad(dy, z, mmq.group_rows(ids, E), E, top_k, w, order=order)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        path()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dz, dw = path()
+    for rep in range(4):
+        ids.copy_(torch.from_numpy(_ids(T, top_k, E, 0.3, 31 + rep)))
+        for t in (z, dy, w):
+            t.normal_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, dww = mmq.moe_combine_grad(dy, z, mmq.group_rows(ids, E), E, top_k, w, order=order, dz=torch.zeros_like(z))
+        assert torch.equal(dz, want) and torch.equal(dw, dww), rep
