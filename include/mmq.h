@@ -328,11 +328,12 @@ mmq_status mmq_moe_combine_grad(mmq_otype o, const void* dy, int64_t lddy, const
  * x^ are the values that the act buffer stands for: xs * xq (MMQ_ACT_Q8_1) or sa * a
  * (MMQ_ACT_I8_TOKEN), so the adapters see the same quantised activations as the projection.
  * A row without an adapter gets v = 0 and out = base. No operand is rounded to fewer bits: a
- * product is the sum of exact products of its factors' terms, all of them but what is below 2^-30
- * of it. Sums are f32; v, and scale[e] * v where that is taken before the second product, are f32
- * values; `out` is rounded once to its type. Results repeat bit for bit. Adapters and scales must be finite. Where a row's other inputs are not, or a sum
- * overflows, what depends on it by these formulas is not finite either (an infinity may come out
- * as NaN), and nothing else changes.
+ * product is the sum of exact products of its factors' terms, all of them but what is below
+ * 2^-30 of it. Sums are f32; v, and scale[e] * v where that is taken before the second product,
+ * are f32 values; `out` is rounded once to its type. Results repeat bit for bit. Adapters and
+ * scales must be finite. Where a row's other inputs are not, or a sum overflows, what depends
+ * on it by these formulas is not finite either (an infinity may come out as NaN), and nothing
+ * else changes.
  * --------------------------------------------------------------------------------------- */
 typedef enum { MMQ_ADAPTER_BF16 = 0, MMQ_ADAPTER_F16 = 1 } mmq_adtype;
 
