@@ -9,9 +9,11 @@ The functions mirror include/mmq.h one to one (same names without the `mmq_` pre
     act_bytes, act_region_offsets, quantize_act, packed_bytes, repack_weights, gemm,
     gemm_id_workspace_bytes, gemm_id, gemm_id_noalloc, gemm_id_noalloc_max_workspace_bytes,
     group_bytes, group_region_offsets, group_rows, moe_gather, moe_combine, moe_combine_grad,
-    lora_workspace_bytes, lora, lora_grad_workspace_bytes, lora_grad, status_string
+    lora_workspace_bytes, lora, lora_grad_workspace_bytes, lora_grad, cache_bytes, cache_write,
+    cache_read, cache_attn_workspace_bytes, cache_attn, status_string
 
-plus `group_views` (the regions of a plan as tensors) and host-side encoders/decoders of the
+plus `group_views` (the regions of a plan as tensors), `cache_shape` (a cache's records as a
+tensor's shape) and host-side encoders/decoders of the
 documented act layouts (`act_to_host`, `act_q8_1_pack_host` and friends for q8_1,
 `act_i8_pack_host` / `act_i8_to_host` for the per-token int8 form), used by tests and the bench
 to fill or read act buffers.
@@ -95,6 +97,17 @@ def lib() -> ctypes.CDLL:
     L.mmq_lora_grad_workspace_bytes.restype = S
     L.mmq_lora_grad.argtypes = [e, P, e, P, P, P, I, I, P, I, I, I, P, P, I, P, I, P, I, P, P, P, S, P]
     L.mmq_lora_grad.restype = e
+    L.mmq_cache_bytes.argtypes = [e, I, I, I, I]
+    L.mmq_cache_bytes.restype = S
+    L.mmq_cache_write.argtypes = [e, P, I, P, I, P, I, e, P, e, P, I, I, I, I, P]
+    L.mmq_cache_write.restype = e
+    L.mmq_cache_read.argtypes = [e, P, I, e, P, e, P, I, I, I, I, P, I, P, I, P]
+    L.mmq_cache_read.restype = e
+    L.mmq_cache_attn_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
+    L.mmq_cache_attn_workspace_bytes.restype = S
+    L.mmq_cache_attn.argtypes = [e, P, I, I, I, e, P, e, P, I, I, I, I, P, I, I, P, P, I, I, P, ctypes.c_float,
+                                 P, I, P, S, P]
+    L.mmq_cache_attn.restype = e
     _lib = L
     return L
 
@@ -572,6 +585,152 @@ def lora_grad(act, A, B, scale, plan, v, dy, atype="q8_1", dx_base=None, dx=None
                                _ptr(dx), lddx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), _scratch(fn, workspace),
                                _raw_stream(stream, at)))
     return dx, dA, dB
+
+
+# ------------------------------------------------------- the quantised key/value cache
+
+CACHE_BLOCK = {"q8_0": 34, "q4_0": 18}      # bytes of 32 values
+
+
+def cache_bytes(ctype, pages: int, page: int, heads: int, D: int) -> int:
+    return int(lib().mmq_cache_bytes(_wt(ctype), pages, page, heads, D))
+
+
+def cache_shape(ctype, pages: int, page: int, heads: int, D: int) -> tuple[int, int, int, int]:
+    """The shape of a cache of keys or of values as a uint8 tensor: [pages, heads, page / 32, bytes of
+    a record of 32 tokens], as the calls below take it. Allocated by the caller; nothing needs to be
+    filled in."""
+    nbytes = cache_bytes(ctype, pages, page, heads, D)
+    if nbytes == 0:
+        raise MMQError("mmq_cache_bytes", MMQ_EINVAL)
+    return pages, heads, page // 32, nbytes // (pages * heads * (page // 32))
+
+
+def _cache_type(fn: str, name: str, t) -> int:
+    if t not in CACHE_BLOCK:
+        raise ValueError(f"{fn}: {name} must be one of {list(CACHE_BLOCK)}, got {t!r}")
+    return WTYPE[t]
+
+
+def _caches(fn: str, kcache, vcache, ktype, vtype):
+    """(key type, value type, pages, page, heads, D) of two caches."""
+    import torch
+    tk, tv = _cache_type(fn, "ktype", ktype), _cache_type(fn, "vtype", vtype)
+    for name, c, t in (("kcache", kcache, ktype), ("vcache", vcache, vtype)):
+        if c.dtype is not torch.uint8 or c.dim() != 4 or not c.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous uint8 of cache_shape's shape, got {c.dtype} {tuple(c.shape)}")
+    pages, heads, tiles, rec = kcache.shape
+    D = rec // CACHE_BLOCK[ktype]
+    if rec != D * CACHE_BLOCK[ktype] or vcache.shape != (pages, heads, tiles, D * CACHE_BLOCK[vtype]):
+        raise ValueError(f"{fn}: the caches' records must be of one size of head, got {tuple(kcache.shape)} of {ktype} and "
+                         f"{tuple(vcache.shape)} of {vtype}")
+    return tk, tv, pages, 32 * tiles, heads, D
+
+
+def _heads_ld(fn: str, name: str, t, heads: int, D: int, dtype) -> tuple[int, int]:
+    """(rows, row stride) of a [rows, heads, D] or [rows, heads * D] tensor whose heads lie one after another."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not dtype or (shape[1:] != (heads, D) and shape[1:] != (heads * D,)):
+        raise ValueError(f"{fn}: {name} must be {dtype} [rows, {heads}, {D}] or [rows, {heads * D}], got {t.dtype} {tuple(shape)}")
+    if strides[-1] != 1 or (len(shape) == 3 and heads != 1 and strides[1] != D):
+        raise ValueError(f"{fn}: {name}'s heads must lie one after another, got strides {strides}")
+    return shape[0], strides[0] if shape[0] > 1 else max(strides[0], heads * D)
+
+
+def cache_write(k, v, slots, kcache, vcache, ktype="q8_0", vtype="q8_0", stream=None):
+    """Quantises rows of keys and values (CUDA float32 or bfloat16 [rows, heads, D] or [rows, heads * D],
+    any row stride: a projection's output as it is) into the caches' slots (int32 [rows]: page * tokens
+    of a page + place). Rows whose slot is -1, or outside the caches, are not written."""
+    import torch
+    fn = "cache_write"
+    at = _gpu(fn, k, v, slots, kcache, vcache)
+    tk, tv, pages, page, heads, D = _caches(fn, kcache, vcache, ktype, vtype)
+    o = _row_otype(fn, k)
+    rows, ldk = _heads_ld(fn, "k", k, heads, D, k.dtype)
+    vrows, ldv = _heads_ld(fn, "v", v, heads, D, k.dtype)
+    if vrows != rows:
+        raise ValueError(f"{fn}: k and v must have as many rows, got {rows} and {vrows}")
+    _flat(fn, "slots", slots, (rows,), torch.int32)
+    _check("mmq_cache_write", lib().mmq_cache_write(o, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), rows, tk,
+                                                    kcache.data_ptr(), tv, vcache.data_ptr(), pages, page, heads, D,
+                                                    _raw_stream(stream, at)))
+
+
+def cache_read(slots, kcache, vcache, ktype="q8_0", vtype="q8_0", dtype=None, k=None, v=None, stream=None):
+    """The rows at slots (CUDA int32 [rows]) as values: (k, v), [rows, heads, D] in `dtype` (float32, or
+    bfloat16). Rows whose slot is outside the caches are not written: in tensors made here they hold
+    whatever their memory held. k, v: given together, they name the type."""
+    import torch
+    fn = "cache_read"
+    at = _gpu(fn, slots, kcache, vcache, k, v)
+    tk, tv, pages, page, heads, D = _caches(fn, kcache, vcache, ktype, vtype)
+    if slots.dim() != 1:
+        raise ValueError(f"{fn}: slots must be [rows], got {tuple(slots.shape)}")
+    rows = slots.shape[0]
+    _flat(fn, "slots", slots, (rows,), torch.int32)
+    if (k is None) != (v is None) or (k is not None and dtype not in (None, k.dtype)):
+        raise ValueError(f"{fn}: give k and v together, and no other dtype than theirs")
+    if k is None:
+        dtype = torch.float32 if dtype is None else dtype
+        k = _new(slots, (rows, heads, D), dtype, stream)
+        v = _new(slots, (rows, heads, D), dtype, stream)
+    o = _row_otype(fn, k)
+    krows, ldk = _heads_ld(fn, "k", k, heads, D, k.dtype)
+    vrows, ldv = _heads_ld(fn, "v", v, heads, D, k.dtype)
+    if krows != rows or vrows != rows:
+        raise ValueError(f"{fn}: k and v must have a row for each of the {rows} slots, got {krows} and {vrows}")
+    _check("mmq_cache_read", lib().mmq_cache_read(o, slots.data_ptr(), rows, tk, kcache.data_ptr(), tv, vcache.data_ptr(),
+                                                  pages, page, heads, D, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                                  _raw_stream(stream, at)))
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def cache_attn_workspace_bytes(rows: int, heads_q: int, page: int, heads: int, D: int, width: int, B: int, max_q: int) -> int:
+    return int(lib().mmq_cache_attn_workspace_bytes(rows, heads_q, page, heads, D, width, B, max_q))
+
+
+def cache_attn(q, kcache, vcache, table, lens, starts, max_q: int, ktype="q8_0", vtype="q8_0", mask=None, scale=None,
+               out=None, workspace=None, stream=None):
+    """Attention of the sequences' newest tokens over the cache: q (CUDA float32 or bfloat16 [rows, heads_q, D]
+    or [rows, heads_q * D], any row stride), table int32 [B, width] of pages (columns contiguous), lens int32
+    [B], starts int32 [B + 1]: sequence b's new tokens are its last ones, rows starts[b] .. starts[b + 1] - 1,
+    at most max_q. A new token sees the tokens before the new ones and, of the new ones, those up to itself
+    (mask None), or those whose bit its word of mask (int64 or uint64 [rows], bit j: new token j) has.
+    scale: D ** -0.5 if None. Returns out, like q; rows of no sequence are not written."""
+    import torch
+    fn = "cache_attn"
+    at = _gpu(fn, q, kcache, vcache, table, lens, starts, mask, out, workspace)
+    tk, tv, pages, page, heads, D = _caches(fn, kcache, vcache, ktype, vtype)
+    o = _row_otype(fn, q)
+    rows = q.shape[0] if q.dim() else 0
+    heads_q = q.shape[1] if q.dim() == 3 else q.shape[1] // D if q.dim() == 2 else 0
+    if heads_q == 0 or heads_q % heads:
+        raise ValueError(f"{fn}: q must have a multiple of {heads} heads of {D} values, got {tuple(q.shape)}")
+    rows, ldq = _heads_ld(fn, "q", q, heads_q, D, q.dtype)
+    if lens.dim() != 1 or table.dim() != 2:
+        raise ValueError(f"{fn}: table must be [B, width] and lens [B], got {tuple(table.shape)} and {tuple(lens.shape)}")
+    B, width = lens.shape[0], table.shape[1]
+    ldt = _ld(fn, "table", table, B, width, torch.int32)
+    _flat(fn, "lens", lens, (B,), torch.int32)
+    _flat(fn, "starts", starts, (B + 1,), torch.int32)
+    if mask is not None and (mask.dtype not in (torch.int64, torch.uint64) or mask.shape != (rows,) or not mask.is_contiguous()):
+        raise ValueError(f"{fn}: mask must be contiguous int64 or uint64 [{rows}], got {mask.dtype} {tuple(mask.shape)}")
+    if out is None:
+        out = _new(q, tuple(q.shape), q.dtype, stream)
+    orows, ldo = _heads_ld(fn, "out", out, heads_q, D, q.dtype)
+    if orows != rows:
+        raise ValueError(f"{fn}: out must have {rows} rows, got {orows}")
+    if workspace is None:
+        nbytes = cache_attn_workspace_bytes(rows, heads_q, page, heads, D, width, B, max_q)
+        if nbytes:
+            workspace = _new(kcache, nbytes, torch.uint8, stream)
+    _check("mmq_cache_attn",
+           lib().mmq_cache_attn(o, q.data_ptr(), ldq, rows, heads_q, tk, kcache.data_ptr(), tv, vcache.data_ptr(), pages,
+                                page, heads, D, table.data_ptr(), ldt, width, lens.data_ptr(), starts.data_ptr(), B, max_q,
+                                _ptr(mask), D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(workspace),
+                                0 if workspace is None else _scratch(fn, workspace), _raw_stream(stream, at)))
+    return out
 
 
 # -------------------------------------------------------------------------- host helpers

@@ -3,6 +3,8 @@
 #include "mmq_internal.h"
 #include "rows.h"
 #include "lora.h"
+#include "cache.h"
+#include <cmath>
 
 using namespace mmq;
 
@@ -316,6 +318,97 @@ mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void*
     if (!aligned16(workspace)) return MMQ_EALIGN;
     return from_hip(launch_lora_grad(a, d == MMQ_ADAPTER_F16, act, A, B, scale, E, R, plan, M, N, K, v, dy, lddy,
                                      dx_base, ldxb, dx, lddx, dA, dB, workspace, as_stream(stream)));
+}
+
+namespace {
+bool cache_shape_ok(int64_t pages, int64_t page, int64_t heads, int64_t D) {
+    return pages >= 1 && (page == 32 || page == 64 || page == 128 || page == 256) &&
+           pages <= ((int64_t(1) << 31) - 1) / page && heads >= 1 && heads <= 1024 &&
+           (D == 64 || D == 128 || D == 192 || D == 256);
+}
+CacheShape cache_shape(int64_t pages, int64_t page, int64_t heads, int64_t D) {
+    return {(int)pages, (int)(page / CACHE_TILE), (int)heads, (int)D};
+}
+bool cache_rows_ok(int64_t rows, int64_t heads, int64_t D) {
+    return rows >= 1 && rows <= MAX_DIM && product_le(rows, heads, D, (int64_t(1) << 35) - 1);
+}
+// The checks that writing and reading share; the pointers are checked by both.
+mmq_status cache_rows_args(mmq_otype o, int64_t ldk, int64_t ldv, int64_t rows, mmq_wtype tk, mmq_wtype tv,
+                           int64_t pages, int64_t page, int64_t heads, int64_t D) {
+    if (!valid_otype(o) || !valid_wtype(tk) || !valid_wtype(tv)) return MMQ_EINVAL;
+    if (!cache_shape_ok(pages, page, heads, D) || !cache_rows_ok(rows, heads, D)) return MMQ_EINVAL;
+    if (ldk < heads * D || ldv < heads * D) return MMQ_EINVAL;
+    if (!row_type(o) || !cache_type(tk) || !cache_type(tv)) return MMQ_EUNSUPPORTED;
+    return MMQ_OK;
+}
+bool attn_sizes_ok(int64_t rows, int64_t heads_q, int64_t page, int64_t heads, int64_t D, int64_t width, int64_t B,
+                   int64_t max_q) {
+    return cache_shape_ok(1, page, heads, D) && rows >= 1 && rows <= MAX_DIM && heads_q >= heads && heads_q <= 4096 &&
+           heads_q % heads == 0 && width >= 1 && width <= (int64_t(1) << 22) && B >= 1 && B <= CACHE_MAX_SEQS &&
+           max_q >= 1 && max_q <= rows &&
+           cache_attn_grid_ok(cache_shape(1, page, heads, D), {rows, B, max_q, width, (int)heads_q});
+}
+}  // namespace
+
+size_t mmq_cache_bytes(mmq_wtype t, int64_t pages, int64_t page, int64_t heads, int64_t D) {
+    if (!valid_wtype(t) || !cache_type(t) || !cache_shape_ok(pages, page, heads, D)) return 0;
+    return (size_t)pages * heads * (page / CACHE_TILE) * cache_record(t == MMQ_Q8_0, (int)D);
+}
+
+mmq_status mmq_cache_write(mmq_otype o, const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* slots,
+                           int64_t rows, mmq_wtype tk, void* kcache, mmq_wtype tv, void* vcache, int64_t pages,
+                           int64_t page, int64_t heads, int64_t D, void* stream) {
+    const mmq_status st = cache_rows_args(o, ldk, ldv, rows, tk, tv, pages, page, heads, D);
+    if (st == MMQ_EINVAL) return st;
+    if (!k || !v || !slots || !kcache || !vcache) return MMQ_EINVAL;
+    if (st != MMQ_OK) return st;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(kcache) || !aligned16(vcache))
+        return MMQ_EALIGN;
+    return from_hip(launch_cache_write(o, k, ldk, v, ldv, slots, rows, tk, kcache, tv, vcache,
+                                       cache_shape(pages, page, heads, D), as_stream(stream)));
+}
+
+mmq_status mmq_cache_read(mmq_otype o, const int32_t* slots, int64_t rows, mmq_wtype tk, const void* kcache,
+                          mmq_wtype tv, const void* vcache, int64_t pages, int64_t page, int64_t heads, int64_t D,
+                          void* k, int64_t ldk, void* v, int64_t ldv, void* stream) {
+    const mmq_status st = cache_rows_args(o, ldk, ldv, rows, tk, tv, pages, page, heads, D);
+    if (st == MMQ_EINVAL) return st;
+    if (!k || !v || !slots || !kcache || !vcache) return MMQ_EINVAL;
+    if (st != MMQ_OK) return st;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(kcache) || !aligned16(vcache))
+        return MMQ_EALIGN;
+    return from_hip(launch_cache_read(o, slots, rows, tk, kcache, tv, vcache, cache_shape(pages, page, heads, D), k,
+                                      ldk, v, ldv, as_stream(stream)));
+}
+
+size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t page, int64_t heads, int64_t D,
+                                      int64_t width, int64_t B, int64_t max_q) {
+    if (!attn_sizes_ok(rows, heads_q, page, heads, D, width, B, max_q)) return 0;
+    return cache_attn_workspace_bytes(cache_shape(1, page, heads, D), {rows, B, max_q, width, (int)heads_q});
+}
+
+mmq_status mmq_cache_attn(mmq_otype o, const void* q, int64_t ldq, int64_t rows, int64_t heads_q, mmq_wtype tk,
+                          const void* kcache, mmq_wtype tv, const void* vcache, int64_t pages, int64_t page,
+                          int64_t heads, int64_t D, const int32_t* table, int64_t ldt, int64_t width,
+                          const int32_t* lens, const int32_t* starts, int64_t B, int64_t max_q, const uint64_t* mask,
+                          float scale, void* out, int64_t ldo, void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_otype(o) || !valid_wtype(tk) || !valid_wtype(tv) || !cache_shape_ok(pages, page, heads, D))
+        return MMQ_EINVAL;
+    if (!attn_sizes_ok(rows, heads_q, page, heads, D, width, B, max_q) || (mask && max_q > 64)) return MMQ_EINVAL;
+    if (ldq < heads_q * D || ldo < heads_q * D || ldt < width || !std::isfinite(scale) || !(scale > 0.f))
+        return MMQ_EINVAL;
+    if (!q || !kcache || !vcache || !table || !lens || !starts || !out) return MMQ_EINVAL;
+    if (!row_type(o) || !cache_type(tk) || !cache_type(tv)) return MMQ_EUNSUPPORTED;
+    if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(table) || !aligned16(lens) ||
+        !aligned16(starts) || !aligned16(mask) || !aligned16(out))
+        return MMQ_EALIGN;
+    const CacheShape c = cache_shape(pages, page, heads, D);
+    const AttnShape a = {rows, B, max_q, width, (int)heads_q};
+    const size_t need = cache_attn_workspace_bytes(c, a);
+    if (need && (!workspace || ws_bytes < need)) return MMQ_EWORKSPACE;
+    if (!aligned16(workspace)) return MMQ_EALIGN;
+    return from_hip(launch_cache_attn(o, q, ldq, tk, kcache, tv, vcache, c, table, ldt, lens, starts, a, mask, scale,
+                                      out, ldo, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -394,6 +394,99 @@ mmq_status mmq_lora_grad(mmq_atype a, const void* act, mmq_adtype d, const void*
                          int64_t ldxb, float* dx, int64_t lddx, float* dA, float* dB, void* workspace,
                          size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Key/value cache: a paged cache of attention keys and values, held as MMQ_Q8_0 or MMQ_Q4_0 blocks
+ * (32 values of a token's head, an f16 scale), keys and values each of their own type. It takes
+ * the projection's rows as mmq_gemm writes them (f32, or bf16 for per-channel weights), and
+ * mmq_cache_attn returns rows that mmq_quantize_act takes for the next projection.
+ *
+ * A cache is `pages` pages of `page` tokens (32, 64, 128 or 256; pages * page < 2^31) with 1 to
+ * 1024 heads of D values (64, 128, 192 or 256). Token `slot` lies in page slot / page at place
+ * slot % page. Per page and head it holds page / 32 records of 32 tokens:
+ *     record (p, head, i) at ((p * heads + head) * (page / 32) + i) * rec,
+ *     rec = 34 * D bytes (MMQ_Q8_0) or 18 * D (MMQ_Q4_0): first the values, then 2 * D bytes of scales.
+ * Inside a record, for token t (0..31) and value 32b + i of the head (i in 0..31), with
+ * r = t % 16, h = t / 16, a = (t % 16) / 4, s = 4 * (t / 16) + t % 4:
+ *   keys, q8_0    byte ((h * D/64 + b/2) * 64 + (i/8) * 16 + r) * 16 + (b%2) * 8 + i%8 holds q + 128
+ *   keys, q4_0    the 4 bytes at (((b/2) * 64 + (i/8) * 16 + r) * 2 + h) * 8 + (b%2) * 4 hold q + 8 of
+ *                 values 8(i/8)..: value i in bits 4n..4n+3 with n = (i%8)/2 + 4 * (i%2)
+ *   values, q8_0  byte (b * 64 + a * 16 + i%16) * 16 + (i/16) * 8 + s holds q + 128
+ *   values, q4_0  byte ((b/2) * 64 + a * 16 + i%16) * 16 + (b%2) * 8 + 4 * (t/16) + (t%4)/2 + 2 * (t%2)
+ *                 holds q + 8, in its low four bits for i < 16, in its high ones else
+ *   scale (both)  the f16 at 2 * ((a * D/32 + b) * 8 + s) of the record's scales
+ * (operand order of the matrix cores, as the packed weights). A token's value is scale * q.
+ * Quantisation is that of MMQ_ACT_Q8_1 for MMQ_Q8_0 (its q and stored scale, bit for bit); MMQ_Q4_0:
+ * d = peak / -8 (f32; peak: the block's first value of largest magnitude), di = 1/d in f32 (0 if
+ * d = 0, +-FLT_MAX where 1/d overflows), q = clamp(round-half-even(x * di), -8, 7), the stored scale
+ * d rounded to f16. The inputs must be finite; where they are not, or a scale exceeds f16's range
+ * (magnitudes from 8.3e6, or 5.2e5 for MMQ_Q4_0), that block's contents mean nothing.
+ *
+ * Rows of queries, keys, values and results hold their heads one after another, D values each, f32
+ * (MMQ_OUT_F32) or bf16 (MMQ_OUT_BF16; MMQ_OUT_I32_PARTIALS is MMQ_EUNSUPPORTED). Row strides ld* are
+ * in elements, at least a row's values and otherwise free. Outputs must not overlap inputs.
+ * Other weight types than MMQ_Q8_0 and MMQ_Q4_0 are MMQ_EUNSUPPORTED.
+ * --------------------------------------------------------------------------------------- */
+
+/* Total bytes of a cache of keys, or of values, of type t; 0 if the arguments are invalid. (host) */
+size_t mmq_cache_bytes(mmq_wtype t, int64_t pages, int64_t page, int64_t heads, int64_t D);
+
+/* Quantise rows of keys k [rows][ldk] and values v [rows][ldv] (device, type o) into the slots
+ * slots [rows] (device, int32). A row whose slot is outside [0, pages * page) (-1, say) is not
+ * written: of a tree of drafted tokens the accepted ones can be written to their places so. No byte of
+ * another slot changes. Slots inside the range must differ from each other (where two are the same,
+ * that slot's contents mean nothing). rows <= 2^24, rows * heads * D < 2^35. */
+mmq_status mmq_cache_write(mmq_otype o, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                           const int32_t* slots, int64_t rows, mmq_wtype tk, void* kcache, mmq_wtype tv,
+                           void* vcache, int64_t pages, int64_t page, int64_t heads, int64_t D, void* stream);
+
+/* The rows at slots [rows] back as values: k [rows][ldk], v [rows][ldv] (device, type o; f32 exactly,
+ * bf16 rounded once). A row whose slot is outside the range is left untouched; a slot may be
+ * named more than once. Sizes as for mmq_cache_write. */
+mmq_status mmq_cache_read(mmq_otype o, const int32_t* slots, int64_t rows, mmq_wtype tk, const void* kcache,
+                          mmq_wtype tv, const void* vcache, int64_t pages, int64_t page, int64_t heads,
+                          int64_t D, void* k, int64_t ldk, void* v, int64_t ldv, void* stream);
+
+/* Workspace bytes of mmq_cache_attn; 0 if the call needs none (short tables), or if the arguments are
+ * invalid (see mmq_cache_attn). (host) */
+size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t page, int64_t heads, int64_t D,
+                                      int64_t width, int64_t B, int64_t max_q);
+
+/* Attention of B sequences' newest tokens over the cache. Sequence b has lens[b] tokens in the
+ * cache, at table[b][0..width) pages in order; the last n = starts[b+1] - starts[b] of them are its new
+ * tokens, whose queries are the rows starts[b].. of q (their keys and values are written first).
+ * New token i of n sees the lens[b] - n tokens before the new ones, and of the new ones
+ *   - tokens 0..i, if mask is NULL (one token, or a chain: a piece of a prompt);
+ *   - token j where bit j of mask[starts[b] + i] is set (a tree of drafted tokens: its ancestors and
+ *     itself). Then max_q <= 64.
+ *     out[row][h] = sum_t softmax_t(scale * <q[row][h], k[t][h/G]>) v[t][h/G],  G = heads_q / heads,
+ * over the tokens t that the row sees; zeros for a row that sees none.
+ *  q, out  (device) [rows][ldq], [rows][ldo] of type o: heads_q heads a row, heads_q a multiple of
+ *          heads, at most 4096
+ *  table   (device) int32 [B][ldt], ldt >= width >= 1. Tokens of a page outside [0, pages), and
+ *          tokens past width * page, are not seen. Pages may be shared by sequences.
+ *  lens    (device) int32 [B]; a negative length is 0
+ *  starts  (device) int32 [B + 1], rising, in [0, rows]; a sequence whose starts are not has no
+ *          rows. Rows outside every sequence are left untouched.
+ *  max_q   the largest n: rows of a sequence past its max_q are left untouched
+ *  mask    (device) uint64 [rows] or NULL
+ *  scale   finite and > 0 (D^-0.5, as a rule)
+ *  workspace (device) >= mmq_cache_attn_workspace_bytes(...) bytes (NULL if that is 0); needs no
+ *          initialisation. Two calls that overlap in time must not share one.
+ * Numbers: whole numbers of the cache enter the products exactly; q in f32 rows, and softmax
+ * weights times value scales, as two f16 terms (22 bits of the largest of a row; 35 bits below the
+ * largest weight times the largest scale), in bf16 rows as one (q exactly, weights to 11 bits).
+ * Sums, maxima and scores are f32; the result is rounded once. It repeats bit for bit. Slots past
+ * a sequence's length may hold anything; a scale that is not finite in a token that a row does not
+ * see changes nothing for that row.
+ * Limits (MMQ_EINVAL): rows <= 2^24, 1 <= B <= 4096, 1 <= max_q <= rows, width <= 2^22, and
+ * ceil(max_q * G / 16) * heads < 65536, with the launch below 2^24 workgroups. */
+mmq_status mmq_cache_attn(mmq_otype o, const void* q, int64_t ldq, int64_t rows, int64_t heads_q, mmq_wtype tk,
+                          const void* kcache, mmq_wtype tv, const void* vcache, int64_t pages, int64_t page,
+                          int64_t heads, int64_t D, const int32_t* table, int64_t ldt, int64_t width,
+                          const int32_t* lens, const int32_t* starts, int64_t B, int64_t max_q,
+                          const uint64_t* mask, float scale, void* out, int64_t ldo, void* workspace,
+                          size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code (host). */
 const char* mmq_status_string(mmq_status s);
 

@@ -1,0 +1,500 @@
+"""The key/value cache on the GPU, through the public binding: what is written byte for byte against
+the model of the layout, what is read back bit for bit, and attention against 64-bit sums.
+
+Tolerances of attention, from the number formats (u = 2^-24, half a step of f32). With T the largest
+sum of magnitudes of a score's terms, N the tokens and |o| the sum of p |v|:
+  - a score is off by the split of q (2^-22 of each term, f32 rows) and by at most 2D + 24 additions
+    and products of 2u each:                                             ds = (2D + 24) 2u T + 2^-22 T
+  - its exponent is three roundings of numbers up to 2T + 10, the exponential 2^-22 of itself:
+                                                                         e = ds + 6u (2T + 10) + 2^-22
+  - numerator and denominator follow, each over N + 32 additions:        2 e + 4u (N + 32)
+  - weights enter the second product to 2^-22 (two terms) or 2^-11 (one), and to 2^-25 where the
+    largest weight times the largest scale is at least 2^10:             N 2^-28 max|v|
+  - the result is rounded once, bf16 by at most 2^-8 of itself."""
+import numpy as np
+import pytest
+
+import cachemodel
+import rowmodel
+
+pytestmark = pytest.mark.gpu
+
+U24 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    import block_quantized_int8_amd as mmq
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mmq.lib()
+    return torch, mmq
+
+
+def _dtype(torch, name):
+    return {"f32": torch.float32, "bf16": torch.bfloat16}[name]
+
+
+def _rows(r, rows, heads, D, dt):
+    """Rows of very different sizes: of ordinary ones, of one value, zeros, ties of both signs."""
+    x = r.standard_normal((rows, heads, D)).astype(np.float32)
+    x *= np.exp2(r.integers(-6, 7, (rows, heads, D // 32, 1))).repeat(32, 3).reshape(rows, heads, D).astype(np.float32)
+    if rows > 3:
+        x[1] = 0.0
+        x[2, :, ::2] = 1.5
+        x[2, :, 1::2] = -1.5
+        x[3, :, 5] = 3e4
+    return x if dt == "f32" else rowmodel.bf16(x)
+
+
+def _garbage(r, shape):
+    """Records of slots that were never written: any bytes, among the scales NaN and infinities."""
+    c = r.integers(0, 256, shape).astype(np.uint8)
+    c[..., -8:] = 0xFF
+    return c
+
+
+ROWS = [("f32", "q8_0", "q8_0", 1, 1, 64, 32, 2), ("bf16", "q4_0", "q8_0", 5, 3, 128, 64, 3),
+        ("f32", "q8_0", "q4_0", 77, 2, 192, 32, 5), ("bf16", "q4_0", "q4_0", 130, 5, 256, 128, 2),
+        ("f32", "q4_0", "q4_0", 64, 4, 128, 256, 2), ("bf16", "q8_0", "q8_0", 300, 1, 64, 64, 8),
+        ("f32", "q8_0", "q8_0", 259, 3, 128, 32, 12)]
+
+
+def _slots(r, rows, pages, page, how):
+    total = pages * page
+    if how == "run":                        # a sequence from the middle of a page on, its pages anywhere
+        first = 3 if rows + 3 <= total else 0
+        pos = first + np.arange(rows)
+        slots = r.permutation(pages)[pos // page] * page + pos % page
+    elif how == "tile":                     # whole records
+        slots = np.arange(rows)
+    else:                                   # anywhere, and nowhere
+        slots = r.permutation(total)[:rows]
+        slots[r.random(rows) < 0.2] = -1
+        slots[r.random(rows) < 0.05] = total
+        slots[r.random(rows) < 0.05] = np.iinfo(np.int32).max
+        slots[r.random(rows) < 0.05] = np.iinfo(np.int32).min
+    return slots.astype(np.int32)
+
+
+@pytest.mark.parametrize("how", ["run", "tile", "any"])
+@pytest.mark.parametrize("dt,kt,vt,rows,heads,D,page,pages", ROWS)
+def test_write_and_read(env, dt, kt, vt, rows, heads, D, page, pages, how):
+    torch, mmq = env
+    print(f"[case] cache {dt} {kt} {vt} rows={rows} heads={heads} D={D} page={page} {how}", flush=True)
+    r = np.random.default_rng([rows, D, len(how)])
+    slots = _slots(r, rows, pages, page, how)
+    sd = torch.from_numpy(slots).cuda()
+    want, dev, rest = {}, {}, {}
+    qkv = np.concatenate([_rows(r, rows, heads, D, dt) for _ in range(3)], 1)
+    x = torch.from_numpy(qkv).to(_dtype(torch, dt)).cuda()               # a projection's rows: q, k, v
+    for i, (side, kind) in enumerate((("k", kt), ("v", vt))):
+        c = _garbage(r, mmq.cache_shape(kind, pages, page, heads, D))
+        dev[side] = torch.from_numpy(c.copy()).cuda()
+        cachemodel.write(c, qkv[:, (i + 1) * heads:(i + 2) * heads], slots, kind, side)
+        want[side] = c
+    k, v = x[:, heads:2 * heads], x[:, 2 * heads:]
+    mmq.cache_write(k, v, sd, dev["k"], dev["v"], kt, vt)
+    for side in "kv":
+        assert np.array_equal(dev[side].cpu().numpy(), want[side]), side
+    there = (slots >= 0) & (slots < pages * page)
+    for out in ("f32", "bf16"):
+        back = [torch.full((rows, heads * D + 3), -7.0, dtype=_dtype(torch, out), device="cuda") for _ in range(2)]
+        got = mmq.cache_read(sd, dev["k"], dev["v"], kt, vt, k=back[0][:, :heads * D], v=back[1][:, :heads * D])
+        assert got[0].data_ptr() == back[0].data_ptr()
+        for side, kind, b in (("k", kt, back[0]), ("v", vt, back[1])):
+            b = b.float().cpu().numpy()
+            assert np.all(b[:, heads * D:] == -7.0) and np.all(b[~there] == -7.0)
+            values = cachemodel.load(want[side], kind, side)[slots[there]].astype(np.float32)
+            if out == "bf16":
+                values = rowmodel.bf16(values)
+            assert np.array_equal(b[there, :heads * D], values.reshape(-1, heads * D)), (side, out)
+
+
+def test_read_names_a_slot_twice(env):
+    torch, mmq = env
+    r = np.random.default_rng(8)
+    c = torch.from_numpy(r.integers(0, 100, mmq.cache_shape("q8_0", 2, 32, 2, 64)).astype(np.uint8)).cuda()
+    slots = torch.tensor([5, 5, 63, 5, 0, 63], dtype=torch.int32, device="cuda")
+    k, v = mmq.cache_read(slots, c, c, dtype=torch.float32)
+    assert k.shape == (6, 2, 64)
+    host = c.cpu().numpy()
+    assert np.array_equal(k.cpu().numpy(), cachemodel.load(host, "q8_0", "k")[slots.cpu().numpy()].astype(np.float32))
+    assert np.array_equal(v.cpu().numpy(), cachemodel.load(host, "q8_0", "v")[slots.cpu().numpy()].astype(np.float32))
+
+
+def test_quantisation_is_the_act_buffers(env):
+    """q8_0 blocks hold what quantize_act makes of the same rows."""
+    torch, mmq = env
+    r = np.random.default_rng(9)
+    x = _rows(r, 37, 2, 128, "f32")
+    xd = torch.from_numpy(x).cuda()
+    cache = [torch.zeros(mmq.cache_shape("q8_0", 2, 32, 2, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    mmq.cache_write(xd, xd, torch.arange(37, dtype=torch.int32, device="cuda"), *cache)
+    act = mmq.quantize_act(xd.view(37, 256))
+    xq, xs, _ = mmq.act_to_host(act.cpu().numpy(), 37, 256)
+    want = xq.astype(np.float64) * np.repeat(xs.astype(np.float64), 32, 1)
+    for side, c in zip("kv", cache):
+        got = cachemodel.load(c.cpu().numpy(), "q8_0", side)[:37].reshape(37, 256)
+        assert np.array_equal(got, want)
+
+
+# ------------------------------------------------------------------------------ attention
+
+class Case:
+    """A batch: caches with garbage in unwritten slots, tables with pages of none past the lengths."""
+
+    def __init__(self, env, dt="f32", kt="q8_0", vt="q8_0", D=128, heads=2, G=4, page=32, lens=(70,), news=(1,), width=None,
+                 tree=False, seed=1, std=1.0):
+        self.torch, self.mmq = env
+        torch, mmq = env
+        r = self.r = np.random.default_rng([seed, D, page, sum(lens)])
+        self.dt, self.kt, self.vt, self.page, self.heads, self.G, self.D = dt, kt, vt, page, heads, G, D
+        need = [-(-n // page) for n in lens]
+        self.width = width or max(need) + 1
+        self.pages = sum(need) + 2
+        perm = r.permutation(self.pages)
+        table = np.full((len(lens), self.width), -1, np.int32)
+        used = 0
+        for b, n in enumerate(need):
+            n = min(n, self.width)
+            table[b, :n] = perm[used:used + n]
+            used += n
+        self.table, self.lens, self.news = table, np.array(lens, np.int32), list(news)
+        self.starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        self.rows, self.max_q = int(sum(news)), max(1, max(news))
+        self.host = {}
+        for side, kind in (("k", kt), ("v", vt)):
+            c = _garbage(r, mmq.cache_shape(kind, self.pages, page, heads, D))
+            slots = np.concatenate([table[b, np.arange(min(n, self.width * page)) // page] * page +
+                                    np.arange(min(n, self.width * page)) % page for b, n in enumerate(lens)])
+            x = (r.standard_normal((len(slots), heads, D)) * std).astype(np.float32)
+            x[:, :, 3] *= 8
+            cachemodel.write(c, x, slots, kind, side)
+            self.host[side] = c
+        q = r.standard_normal((self.rows, heads * G + 1, D)).astype(np.float32)
+        self.qh = (q if dt == "f32" else rowmodel.bf16(q))[:, :heads * G]
+        self.mask = None
+        if tree:
+            m = []
+            for n in news:
+                seen = []
+                for i in range(n):
+                    p = int(r.integers(-1, i))
+                    seen.append((seen[p] if p >= 0 else 0) | 1 << i)
+                m += seen
+            self.mask = np.array(m, np.uint64)
+        self.scale = D ** -0.5
+
+    def device(self):
+        torch = self.torch
+        pad = torch.zeros((self.rows, self.heads * self.G + 1, self.D), dtype=_dtype(torch, self.dt), device="cuda")
+        pad[:, :self.heads * self.G] = torch.from_numpy(self.qh).to(pad.dtype).cuda()
+        self.q = pad[:, :self.heads * self.G]
+        self.kc, self.vc = (torch.from_numpy(self.host[s]).cuda() for s in "kv")
+        self.td, self.ld, self.sd = (torch.from_numpy(a).cuda() for a in (self.table, self.lens, self.starts))
+        self.md = None if self.mask is None else torch.from_numpy(self.mask.view(np.int64)).cuda()
+        return self
+
+    def run(self, **kw):
+        return self.mmq.cache_attn(self.q, self.kc, self.vc, self.td, self.ld, self.sd, self.max_q, self.kt, self.vt,
+                                   mask=self.md, scale=self.scale, **kw)
+
+    def want(self):
+        k, v = (cachemodel.load(self.host[s], t, s) for s, t in (("k", self.kt), ("v", self.vt)))
+        with np.errstate(invalid="ignore"):
+            out, mag, terms = cachemodel.attn(self.qh.astype(np.float64), k, v, self.table, self.lens, self.starts, self.page,
+                                              self.pages, self.max_q, self.mask, self.scale)
+        N = int(self.lens.max(initial=0))
+        T = terms[:, :, None]
+        ds = (2 * self.D + 24) * 2 * U24 * T + 2.0 ** -22 * T
+        e = ds + 6 * U24 * (2 * T + 10) + 2.0 ** -22
+        used = [p * self.page + j for b, n in enumerate(self.lens) for i, p in enumerate(self.table[b]) if 0 <= p < self.pages
+                for j in range(self.page) if i * self.page + j < n]
+        vmax = np.abs(v[used]).max(initial=0)
+        weight = 2.0 ** -22 if self.dt == "f32" else 2.0 ** -11
+        bound = mag * (2 * e + 4 * U24 * (N + 32) + weight) * 1.01 + N * 2.0 ** -28 * vmax
+        bound += np.abs(out) * (U24 if self.dt == "f32" else 2.0 ** -8)
+        return out, bound
+
+    def check(self, got=None, fill=None):
+        if got is None:
+            buf = self.torch.full((self.rows + 2, self.heads * self.G * self.D + 5), -7.0, dtype=_dtype(self.torch, self.dt),
+                                  device="cuda")
+            self.run(out=buf[:self.rows, :self.heads * self.G * self.D])
+            b = buf.float().cpu().numpy().astype(np.float64)
+            assert np.all(b[self.rows:] == -7.0) and np.all(b[:, self.heads * self.G * self.D:] == -7.0)
+            got, fill = b[:self.rows, :-5].reshape(self.qh.shape), -7.0
+        want, bound = self.want()
+        none = np.isnan(want)
+        assert np.all(np.isfinite(got))
+        if fill is not None:
+            assert np.all(got[none] == fill)
+        off = np.abs(got - want)[~none]
+        worst = float((off / np.maximum(bound[~none], 1e-300)).max(initial=0))
+        print(f"[case]   error at most {worst:.4f} of the bound", flush=True)
+        assert np.all(off <= bound[~none])
+        return got
+
+
+ATTN = [
+    dict(lens=(1,), news=(1,)),
+    dict(lens=(70,), news=(1,), kt="q4_0", vt="q4_0"),
+    dict(lens=(32, 33, 31, 64), news=(1, 1, 1, 1), dt="bf16"),
+    dict(lens=(0, 5), news=(1, 1)),                                       # a sequence without tokens: zeros
+    dict(lens=(129, 200), news=(3, 7), D=64, G=7, heads=3, vt="q4_0"),
+    dict(lens=(129, 200, 90), news=(40, 1, 64), D=64, G=1, heads=2, kt="q4_0", dt="bf16"),
+    dict(lens=(100, 64), news=(33, 64), tree=True, page=64),
+    dict(lens=(100, 64, 65), news=(5, 64, 2), tree=True, page=128, D=192, G=2, dt="bf16", vt="q4_0"),
+    dict(lens=(300,), news=(9,), tree=True, page=256, D=256, G=5, heads=1, kt="q4_0"),
+    dict(lens=(3, 70), news=(5, 1)),                                       # fewer tokens than rows
+    dict(lens=(3, 70), news=(5, 2), tree=True, D=64),
+    dict(lens=(200, 10), news=(2, 1), width=3),                            # longer than the table
+    dict(lens=(1500,), news=(2,), page=64),                                # split over chunks
+    dict(lens=(900, 40, 1300, 0), news=(1, 2, 3, 1), page=64, dt="bf16", kt="q4_0", vt="q4_0", D=64),
+    dict(lens=(700, 1100), news=(30, 64), tree=True, page=32, G=8, heads=1, D=64),
+    dict(lens=(500,), news=(300,), D=64, heads=1, G=3, page=64),           # a piece of a prompt
+    dict(lens=tuple(range(1, 300, 3)), news=(1,) * 100, D=64, heads=1, G=2),
+    dict(lens=tuple((i * 37) % 97 for i in range(300)), news=tuple(i % 3 for i in range(300)), D=64, heads=1, G=1),
+]
+
+
+@pytest.mark.parametrize("case", ATTN, ids=lambda c: "-".join(f"{k}{v if not isinstance(v, tuple) or len(v) < 5 else len(v)}"
+                                                              for k, v in c.items()).replace(" ", ""))
+def test_attention(env, case):
+    print(f"[case] attn {case if len(case['lens']) < 9 else {**case, 'lens': '..', 'news': '..'}}", flush=True)
+    c = Case(env, **case).device()
+    first = c.check()
+    assert np.array_equal(c.run().float().cpu().numpy().reshape(first.shape).astype(np.float64)[~np.isnan(c.want()[0])],
+                          first[~np.isnan(c.want()[0])])                  # the same bits again
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("std", [1e-4, 1e3])
+def test_attention_of_small_and_large_values(env, dt, std):
+    """Scales far from one: keys and values of 1e-4 (scales below f16's normal numbers) and of 1e3."""
+    print(f"[case] attn {dt} std={std}", flush=True)
+    c = Case(env, dt=dt, lens=(130, 60), news=(2, 1), D=64, std=std, seed=3)
+    c.scale = 0.125 / std
+    c.device().check()
+
+
+def test_attention_when_value_scales_grow_and_shrink_along_the_sequence(env):
+    """The products' exponent follows the largest scale so far: tiles of 1e-3, then 1, 1e3, 1."""
+    c = Case(env, lens=(128 * 4,), news=(1,), D=64, heads=1, G=2, page=128, seed=4)
+    x = c.r.standard_normal((512, 1, 64)).astype(np.float32) * np.repeat([1e-3, 1.0, 1e3, 1.0], 128)[:, None, None].astype(np.float32)
+    slots = c.table[0, np.arange(512) // 128] * 128 + np.arange(512) % 128
+    cachemodel.write(c.host["v"], x, slots, "q8_0", "v")
+    c.device().check()
+
+
+def test_masks_that_leave_a_row_empty_and_bits_past_the_tree(env):
+    c = Case(env, lens=(6, 40), news=(6, 5), tree=True, D=64, seed=5)
+    c.mask[0] = 0                                   # nothing before it, nothing of the tree: zeros
+    c.mask[2] = 2 ** 64 - 1                         # bits past the sequence's tokens count nothing
+    c.mask[3] = 1 << 4                              # a token that does not see itself
+    c.mask[8] = 0                                   # sees what is before the tree
+    got = c.device().check()
+    assert np.all(got[0] == 0.0) and np.all(got[8] != 0.0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_hidden_tokens_that_are_not_finite_change_nothing(env, dt):
+    """A drafted token with infinite and NaN scales, seen by two rows of the tree only, which are not
+    finite then; the other rows stay within the bound of what they are without it (the exponent that
+    a tile's products share may differ, so not the same bits)."""
+    torch, mmq = env
+    c = Case(env, dt=dt, lens=(100,), news=(8,), tree=True, D=64, seed=6)
+    c.mask[:] = [1 | 1 << i for i in range(8)]
+    c.mask[5] |= np.uint64(1 << 3)
+    c.device()
+    want, bound = c.want()
+    c.check()
+    pos = 100 - 8 + 3
+    slot = c.table[0, pos // 32] * 32 + pos % 32
+    t, a = slot % 32, (slot % 16) // 4
+    for cache, bits in ((c.kc, 0x7E00), (c.vc, 0x7C00)):
+        rec = cache.cpu().numpy()
+        for b in range(2):
+            at = 64 * 32 + 2 * ((a * 2 + b) * 8 + 4 * (t // 16) + t % 4)
+            rec[slot // 32, :, 0, at:at + 2] = np.frombuffer(np.uint16(bits).tobytes(), np.uint8)
+        cache.copy_(torch.from_numpy(rec))
+    after = c.run().float().cpu().numpy().astype(np.float64)
+    others = [0, 1, 2, 4, 6, 7]
+    assert np.all(np.abs(after - want)[others] <= bound[others])
+    assert not np.isfinite(after[3]).any() and not np.isfinite(after[5]).any()
+
+
+def test_pages_outside_the_cache_and_starts_out_of_order(env):
+    """Tokens of no page are not seen; a sequence whose rows are not in the batch has none."""
+    c = Case(env, lens=(100, 100, 100, 100), news=(2, 3, 2, 2), D=64, seed=7)
+    c.table[0, 1], c.table[0, 0] = c.pages, -5
+    c.table[1, :] = np.iinfo(np.int32).max
+    c.device().check()
+    for starts in ([0, 2, 1, 7, 9], [-1, 2, 5, 7, 9], [0, 2, 5, 7, 10], [0, 2, 5, 9, 7]):
+        c.starts = np.array(starts, np.int32)
+        c.sd = c.torch.from_numpy(c.starts).cuda()
+        c.check()
+    c.lens = np.array([-3, 100, np.iinfo(np.int32).max, np.iinfo(np.int32).min], np.int32)
+    c.starts = np.array([0, 2, 5, 7, 9], np.int32)
+    c.ld, c.sd = c.torch.from_numpy(c.lens).cuda(), c.torch.from_numpy(c.starts).cuda()
+    got = c.run().cpu().numpy()
+    assert np.all(got[:2] == 0.0) and np.all(got[7:] == 0.0)
+
+
+def test_rows_past_max_q_are_left(env):
+    c = Case(env, lens=(100, 50), news=(6, 2), D=64, seed=8)
+    c.max_q = 2
+    c.device().check()
+
+
+def test_pages_shared_by_sequences(env):
+    c = Case(env, lens=(90, 70), news=(2, 3), D=64, seed=9)
+    c.table[1, :2] = c.table[0, :2]
+    c.device().check()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_a_graph_replays_other_lengths(env, dt):
+    """Captured once, replayed while lengths, tables and queries change in place: every replay gives
+    the bits of an eager call; two graphs with workspaces of their own, and eager work between them."""
+    torch, mmq = env
+    cases = [Case(env, dt=dt, lens=(700, 300), news=(1, 1), D=64, page=64, seed=s, width=30).device() for s in (10, 11)]
+    graphs, outs = [], []
+    for c in cases:
+        need = mmq.cache_attn_workspace_bytes(c.rows, c.heads * c.G, 64, c.heads, 64, 30, 2, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        out = torch.empty(c.q.shape, dtype=c.q.dtype, device="cuda")
+        slots = torch.tensor([c.table[b, (n - 1) // 64] * 64 + (n - 1) % 64 for b, n in enumerate(c.lens)], dtype=torch.int32,
+                             device="cuda")
+        new = torch.randn(2, 2, c.heads, 64, device="cuda").to(c.q.dtype)
+        def step(c=c, ws=ws, out=out, slots=slots, new=new):
+            mmq.cache_write(new[0], new[1], slots, c.kc, c.vc)
+            c.run(out=out, workspace=ws)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+        outs.append(out)
+    for turn in range(4):
+        for c, g, out in zip(cases, graphs, outs):
+            c.ld[0] = 700 - 150 * turn
+            c.q.copy_(torch.randn(c.q.shape, device="cuda"))
+            g.replay()
+        torch.cuda.synchronize()
+        for c, out in zip(cases, outs):
+            assert torch.equal(c.run().view(torch.uint8), out.view(torch.uint8))
+
+
+def test_another_stream(env):
+    torch, mmq = env
+    c = Case(env, lens=(700, 300), news=(1, 1), D=64, page=64, seed=12).device()
+    want = c.run().cpu()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = c.run(stream=s)
+    slots = torch.arange(40, dtype=torch.int32, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    k, v = mmq.cache_read(slots, c.kc, c.vc, stream=s)
+    s.synchronize()
+    assert torch.equal(got.cpu(), want)
+    k1, v1 = mmq.cache_read(slots, c.kc, c.vc)
+    assert np.array_equal(k.cpu().numpy(), k1.cpu().numpy(), equal_nan=True)
+    assert np.array_equal(v.cpu().numpy(), v1.cpu().numpy(), equal_nan=True)
+
+
+def test_a_step_from_projection_to_projection(env):
+    """Tokens quantised, projected to queries, keys and values, the cache written, attended to, and the
+    result quantised and projected, against the same step in 64 bits from the quantised values."""
+    torch, mmq = env
+    import gen
+    import oracle
+    oracle.build()
+    r = np.random.default_rng(20)
+    hidden, heads, G, D, page, T = 256, 2, 2, 64, 32, 45
+    N = (heads * G + 2 * heads) * D
+    raw, raw_o = gen.weights_q8_0(N, hidden, seed=1, std=0.1), gen.weights_q4_0(hidden, heads * G * D, seed=2)
+    wq = mmq.repack_weights("q8_0", torch.from_numpy(raw).cuda(), N, hidden)
+    wo = mmq.repack_weights("q4_0", torch.from_numpy(raw_o).cuda(), hidden, heads * G * D)
+    kc = torch.zeros(mmq.cache_shape("q8_0", 4, page, heads, D), dtype=torch.uint8, device="cuda")
+    vc = torch.zeros(mmq.cache_shape("q4_0", 4, page, heads, D), dtype=torch.uint8, device="cuda")
+    pages = r.permutation(4).astype(np.int32)
+    table = torch.from_numpy(pages[None]).cuda()
+    seen = 0
+    for n in (T, 1, 1):                                    # a prompt, then two tokens
+        x = r.standard_normal((n, hidden)).astype(np.float32)
+        act = mmq.quantize_act(torch.from_numpy(x).cuda())
+        qkv = mmq.gemm("q8_0", wq, act, n, N, hidden).view(n, -1, D)
+        q, k, v = qkv[:, :heads * G], qkv[:, heads * G:heads * G + heads], qkv[:, heads * G + heads:]
+        pos = seen + np.arange(n)
+        slots = (pages[pos // page] * page + pos % page).astype(np.int32)
+        mmq.cache_write(k, v, torch.from_numpy(slots).cuda(), kc, vc, vtype="q4_0")
+        seen += n
+        out = mmq.cache_attn(q, kc, vc, table, torch.tensor([seen], dtype=torch.int32, device="cuda"),
+                             torch.tensor([0, n], dtype=torch.int32, device="cuda"), n, vtype="q4_0")
+        y = mmq.gemm("q4_0", wo, mmq.quantize_act(out.view(n, -1)), n, hidden, heads * G * D)
+        kv = [cachemodel.load(c.cpu().numpy(), t, s) for c, t, s in ((kc, "q8_0", "k"), (vc, "q4_0", "v"))]
+        want, mag, terms = cachemodel.attn(q.cpu().numpy().astype(np.float64), *kv, pages[None], [seen], [0, n], page, 4, n,
+                                           None, D ** -0.5)
+        assert np.all(np.abs(out.cpu().numpy() - want) <= mag * 2e-4)      # coarse: the parts are tested alone
+        rq, rs, _ = oracle.quantize_q8_1(out.cpu().numpy().reshape(n, -1))
+        ref = oracle.gemm_f64("q4_0", raw_o, hidden, heads * G * D, rq, rs)
+        assert np.max(np.abs(y.cpu().numpy() - ref)) <= 1e-3 * np.max(np.abs(ref))
+
+
+def test_accepted_tokens_of_a_tree_are_written_to_their_places(env):
+    """A tree is written behind the sequence; the accepted path's rows are written again, to the places
+    that follow it, the others to none: the cache then reads as if only the path had been there."""
+    torch, mmq = env
+    heads, D, page = 2, 64, 32
+    shape = mmq.cache_shape("q8_0", 3, page, heads, D)
+    x = torch.randn(2, 60 + 8, heads, D, device="cuda")
+    def slots(v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    tree = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    mmq.cache_write(x[0], x[1], slots(list(range(68))), *tree)
+    path = [0, 2, 5]
+    to = [-1] * 8
+    for j, p in enumerate(path):
+        to[p] = 60 + j
+    mmq.cache_write(x[0, 60:], x[1, 60:], slots(to), *tree)
+    plain = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    rows = list(range(60)) + [60 + p for p in path]
+    mmq.cache_write(x[0][rows], x[1][rows], slots(list(range(63))), *plain)
+    got, want = (mmq.cache_read(slots(list(range(63))), *c) for c in (tree, plain))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
+def test_a_row_that_sees_one_token_gets_its_values(env, kind, dt):
+    """Weight 1: an 11-bit scale times a whole number, exact in every step (rounded once to bf16)."""
+    torch, mmq = env
+    c = Case(env, dt=dt, kt=kind, vt=kind, lens=(70, 1, 33), news=(5, 1, 3), tree=True, D=64, seed=13)
+    c.lens[0], c.lens[2] = 5, 3                     # nothing but the new tokens
+    c.mask[:] = [1 << i for i in (4, 3, 2, 1, 0, 0, 2, 2, 0)]
+    got = c.device().run().float().cpu().numpy()
+    v = cachemodel.load(c.host["v"], kind, "v").astype(np.float32)
+    v = v if dt == "f32" else rowmodel.bf16(v)
+    for row, (b, pos) in enumerate([(0, 4), (0, 3), (0, 2), (0, 1), (0, 0), (1, 0), (2, 2), (2, 2), (2, 0)]):
+        slot = c.table[b, pos // 32] * 32 + pos % 32
+        assert np.array_equal(got[row], v[slot].repeat(4, 0)), row
+
+
+@pytest.mark.parametrize("n", [33, 777, 1900])
+def test_equal_scores_give_the_mean(env, n):
+    """q = 0: every weight is 1, and whole numbers with scale 1 sum exactly; the quotient is off by
+    two roundings."""
+    torch, mmq = env
+    c = Case(env, lens=(n,), news=(1,), D=64, page=64, seed=14)
+    x = c.r.integers(-127, 128, (n, 2, 64)).astype(np.float32)
+    x[:, :, ::32] = 127.0                           # every block's scale is 1
+    slots = c.table[0, np.arange(n) // 64] * 64 + np.arange(n) % 64
+    cachemodel.write(c.host["v"], x, slots, "q8_0", "v")
+    c.device().q.zero_()
+    got = c.run().cpu().numpy().astype(np.float64)[0]
+    want = x.astype(np.float64).sum(0).repeat(4, 0) / n
+    assert np.all(np.abs(got - want) <= np.abs(want) * 2 * U24 * 1.01)
