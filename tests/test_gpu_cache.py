@@ -471,23 +471,27 @@ def test_accepted_tokens_of_a_tree_are_written_to_their_places(env):
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
 def test_a_row_that_sees_one_token_gets_its_values(env, kind, dt):
-    """Weight 1: an 11-bit scale times a whole number, exact in every step (rounded once to bf16)."""
+    """One weight p, the same in the sum of weights and in the product. Its f16 terms are off by 2^-22 of it
+    (bf16 rows, one term: 2^-11), and so are those of p times the scale; the product's two additions are
+    off by 2^-23 each, the reciprocal and the last product by 2^-24 each: together 7 * 2^-23 of the
+    value (2^-10 + 3 * 2^-23), and a bf16 result is rounded once more, by 2^-8."""
     torch, mmq = env
     c = Case(env, dt=dt, kt=kind, vt=kind, lens=(70, 1, 33), news=(5, 1, 3), tree=True, D=64, seed=13)
     c.lens[0], c.lens[2] = 5, 3                     # nothing but the new tokens
     c.mask[:] = [1 << i for i in (4, 3, 2, 1, 0, 0, 2, 2, 0)]
     got = c.device().run().float().cpu().numpy()
     v = cachemodel.load(c.host["v"], kind, "v").astype(np.float32)
-    v = v if dt == "f32" else rowmodel.bf16(v)
+    rel = 7 * 2.0 ** -23 if dt == "f32" else 2.0 ** -10 + 3 * 2.0 ** -23 + 2.0 ** -8
     for row, (b, pos) in enumerate([(0, 4), (0, 3), (0, 2), (0, 1), (0, 0), (1, 0), (2, 2), (2, 2), (2, 0)]):
         slot = c.table[b, pos // 32] * 32 + pos % 32
-        assert np.array_equal(got[row], v[slot].repeat(4, 0)), row
+        want = v[slot].repeat(4, 0).astype(np.float64)
+        assert np.all(np.abs(got[row] - want) <= rel * 1.01 * np.abs(want)), row
 
 
 @pytest.mark.parametrize("n", [33, 777, 1900])
 def test_equal_scores_give_the_mean(env, n):
-    """q = 0: every weight is 1, and whole numbers with scale 1 sum exactly; the quotient is off by
-    two roundings."""
+    """q = 0: every weight is the same power of two, and whole numbers with scale 1 sum exactly; the quotient
+    is off by two roundings."""
     torch, mmq = env
     c = Case(env, lens=(n,), news=(1,), D=64, page=64, seed=14)
     x = c.r.integers(-127, 128, (n, 2, 64)).astype(np.float32)
@@ -498,3 +502,16 @@ def test_equal_scores_give_the_mean(env, n):
     got = c.run().cpu().numpy().astype(np.float64)[0]
     want = x.astype(np.float64).sum(0).repeat(4, 0) / n
     assert np.all(np.abs(got - want) <= np.abs(want) * 2 * U24 * 1.01)
+
+
+@pytest.mark.parametrize("n", [40, 1500])
+def test_a_query_that_is_not_a_number_gives_none(env, n):
+    """And its neighbours, in the same products, are bit for bit what they are without it."""
+    torch, mmq = env
+    c = Case(env, lens=(n,), news=(3,), D=64, page=64, seed=15).device()
+    before = c.run()
+    c.q[1, 2, 5] = float("nan")
+    after = c.run()
+    assert torch.isnan(after[1, 2]).all()
+    after[1, 2] = before[1, 2]
+    assert torch.equal(after, before)
