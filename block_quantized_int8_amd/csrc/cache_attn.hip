@@ -24,8 +24,9 @@ namespace mmq {
 namespace {
 
 constexpr int WAVES = 4, THREADS = WAVES * 64;
-constexpr int CHUNK_MIN = 4;                // tiles of a chunk at least
-constexpr int TARGET = 1024;                // workgroups aimed at
+constexpr int STEP_MIN = 4;                 // tiles of a workgroup's part at least
+constexpr int BEGIN = 6;                    // what beginning an item costs, in tiles
+constexpr int64_t WHOLE = 8;                // tiles of a table's row up to which items are not cut
 constexpr float P_BITS = 10.f;              // p is held times 2^10,
 constexpr float P_SLACK = 4.f;              // and the maximum may rise by 4 before it is taken anew
 
@@ -39,6 +40,12 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
+// Where a workgroup's range of tiles ends inside an item, for the second launch.
+struct Cut {
+    int64_t start, end, step;               // the item's range; tiles of a workgroup (0: no item is cut here)
+    int first, rows, h, qg;                 // first row of the sequence, its rows, the item's head and group of rows
+};
+
 struct AttnArgs {
     const void* q;
     void* out;
@@ -46,11 +53,12 @@ struct AttnArgs {
     const int32_t *table, *lens, *starts;
     const uint64_t* mask;
     float *part_o, *part_m, *part_l;        // parts: [part][rows][D], [part][rows] twice
-    int4* list;                             // split sequences: their number, then (first row, rows, chunks, first part)
+    Cut* cuts;                              // of each workgroup's end
     int64_t ldq, ldo, ldt;
     CacheShape c;
     float scale;
-    int rows, B, max_q, G, QG, cap, units, splits;        // cap: tokens a table row can hold
+    int rows, B, max_q, G, cap;             // cap: tokens a table row can hold
+    int even, spare;                        // how work is counted; even: workgroups beyond one an item (0: no cuts)
 };
 
 __device__ inline h2 as_h2(uint32_t x) { return __builtin_bit_cast(h2, x); }
@@ -60,6 +68,9 @@ __device__ inline uint32_t as_u32(h2 x) { return __builtin_bit_cast(uint32_t, x)
 // A value that is the same in every lane, in a scalar register: what comes from LDS or an integer
 // division would be kept, with all that follows from it (loop counts, buffer descriptors), in lanes.
 __device__ inline int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t scalar(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)scalar((int)(v >> 32)) << 32 | (uint32_t)scalar((int)v));
+}
 
 // Sequence b: its new tokens (0 if its rows are not in the batch) and its tokens in the cache.
 struct Seq {
@@ -78,86 +89,161 @@ __device__ inline int seq_tiles(const AttnArgs& a, const Seq& s) {
     return s.n == 0 ? 0 : max(1, (min(s.len, a.cap) + CACHE_TILE - 1) / CACHE_TILE);
 }
 
-// What a unit (a chunk of one sequence's tiles) is, found by every workgroup from the sequences'
-// lengths: chunks are as long as keeps the launch at TARGET workgroups.
-struct Unit {
-    int b, chunk, chunks, tiles, split, part;     // tiles of a chunk; split: number among split sequences
+// The launch's work is one range: for every sequence, head and group of RQ rows (an item) a cost, by its tiles.
+// Each workgroup takes an equal part of the range, whatever the sequences' lengths, and finds its place
+// from them by itself. An item that is cut leaves parts in the workspace. Two ways to count:
+//   even: an item costs 1 for each of its parts, which are equal and at most `share` tiles long. For
+//         items few enough that the parts' ends do not matter. (Short ones have one part: no second launch.)
+//   tiles: an item costs its tiles and BEGIN more, what beginning an item takes; workgroups end anywhere.
+struct Found {
+    int64_t start;                          // of the sequence
+    int b, first, n, len, cost, groups;     // cost of an item; groups of rows
 };
-__device__ inline int64_t wave_total(int64_t v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor((long long)v, o);
-    return v;
-}
-__device__ inline int wave_scan(int v, int lane) {          // inclusive sum over the lanes
+__device__ inline int64_t wave_scan(int64_t v, int lane) {          // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o);
+        const int64_t u = __shfl_up((long long)v, o);
         if (lane >= o) v += u;
     }
     return v;
 }
-__device__ inline bool find_unit(const AttnArgs& a, int unit, int tid, Unit& u, int* splits) {
-    __shared__ int64_t total[WAVES];
-    __shared__ int sums[3][WAVES];
-    __shared__ Unit found;
-    __shared__ int any;
-    const int lane = tid & 63, wave = tid >> 6;
-    const int per = (a.B + THREADS - 1) / THREADS;
-    if (tid == 0) any = 0;
-    int64_t tiles = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < a.B) tiles += seq_tiles(a, seq_of(a, b));
+__device__ inline int64_t quotient_up(int64_t x, int64_t n) {       // ceil(x / n), x < 2^60, n < 2^31
+    int64_t q = (int64_t)((double)x / (double)n);                   // within 2^8 of it
+    while (q * n >= x + n) --q;
+    while (q * n < x) ++q;
+    return scalar(q);
+}
+template <int RQ> struct Work {
+    struct Shared {
+        int64_t start[THREADS], total[WAVES];           // of a thread's sequences
+        Found found;
+    };
+    const AttnArgs& a;
+    Shared& sh;
+    int tid, per;                                       // per: sequences of a thread
+    int share;
+    Seq own;                                            // the thread's first sequence
+    __device__ Seq seq(int i) const { return i == 0 ? own : seq_of(a, tid * per + i); }
+    __device__ int cost(const Seq& s) const {
+        const int tiles = seq_tiles(a, s);
+        return !a.even ? (tiles ? tiles + BEGIN : 0) : tiles <= share ? min(tiles, 1) : (tiles + share - 1) / share;
     }
-    tiles = wave_total(tiles);
-    if (lane == 0) total[wave] = tiles;
-    __syncthreads();
-    int64_t work = 0;
-    for (int i = 0; i < WAVES; ++i) work += total[i];
-    const int aim = max(1, TARGET / (a.c.heads * a.QG));
-    // (a sequence has fewer than 2^26 tiles)
-    const int chunk = max(CHUNK_MIN, (int)min((work + aim - 1) / aim, (int64_t)1 << 26));
-    int mine[3] = {0, 0, 0};                                // units, parts of split sequences, those
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b >= a.B) break;
-        const int n = (seq_tiles(a, seq_of(a, b)) + chunk - 1) / chunk;
-        mine[0] += n;
-        mine[1] += n > 1 ? n : 0;
-        mine[2] += n > 1;
-    }
-    int before[3];
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        const int s = wave_scan(mine[j], lane);
-        if (lane == 63) sums[j][wave] = s;
-        before[j] = s - mine[j];
-    }
-    __syncthreads();
-    *splits = 0;
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-        for (int i = 0; i < WAVES; ++i) {
-            if (i < wave) before[j] += sums[j][i];
-            if (j == 2) *splits += sums[j][i];
+    __device__ int groups(const Seq& s) const { return (min(s.n, a.max_q) * a.G + RQ - 1) / RQ; }
+    template <typename F> __device__ int64_t sum_up(F f, int64_t& before) {
+        int64_t mine = 0;
+        for (int i = 0; i < per && tid * per + i < a.B; ++i) {
+            const Seq s = seq(i);
+            mine += (int64_t)f(s) * groups(s) * a.c.heads;
         }
-    if (unit >= before[0] && unit < before[0] + mine[0]) {  // one thread's
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            const int n = (seq_tiles(a, seq_of(a, b)) + chunk - 1) / chunk;
-            if (unit < before[0] + n) {
-                found = {b, unit - before[0], n, chunk, before[2], before[1]};
-                any = 1;
+        const int64_t sum = wave_scan(mine, tid & 63);
+        if ((tid & 63) == 63) sh.total[tid >> 6] = sum;
+        __syncthreads();
+        before = sum - mine;
+        int64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            if (w < tid >> 6) before += sh.total[w];
+            all += sh.total[w];
+        }
+        return scalar(all);
+    }
+    // the whole range; every thread calls it once, before find()
+    __device__ Work(const AttnArgs& args, Shared& shared, int64_t& all) : a(args), sh(shared), tid(threadIdx.x), own{0, 0, 0} {
+        per = (a.B + THREADS - 1) / THREADS;
+        if (tid * per < a.B) own = seq_of(a, tid * per);
+        int64_t before;
+        share = 1 << 30;
+        if (a.spare) {
+            // sum of ceil(tiles / share) <= spare + items = the workgroups
+            const int64_t tiles = sum_up([&](const Seq& s) { return seq_tiles(a, s); }, before);
+            share = (int)min(max(quotient_up(tiles, a.spare), (int64_t)STEP_MIN), (int64_t)1 << 30);
+            __syncthreads();
+        }
+        all = sum_up([&](const Seq& s) { return cost(s); }, before);
+        sh.start[tid] = before;
+    }
+    // the sequence at `pos` of the range
+    __device__ Found find(int64_t pos) {
+        __syncthreads();
+        int64_t at = sh.start[tid];
+        for (int i = 0; i < per && at <= pos && tid * per + i < a.B; ++i) {
+            const Seq s = seq(i);
+            const int n = groups(s), c = cost(s);
+            const int64_t size = (int64_t)c * n * a.c.heads;
+            if (pos < at + size) {                      // one thread's
+                sh.found = {at, tid * per + i, s.first, s.n, s.len, c, n};
                 break;
             }
-            before[0] += n;
-            before[1] += n > 1 ? n : 0;
-            before[2] += n > 1;
+            at += size;
+        }
+        __syncthreads();
+        const Found& f = sh.found;
+        return {scalar(f.start), scalar(f.b), scalar(f.first), scalar(f.n), scalar(f.len), scalar(f.cost), scalar(f.groups)};
+    }
+};
+
+// One item's part: tiles [t0, t1) for the rows row0.. of a sequence's head.
+struct Segment {
+    Found f;
+    int h, qg, row0, nrows, ctx, len, t0, t1;
+    int part;                               // -1: the whole item
+};
+
+// The thread's number, new to the compiler at each segment: what follows from it would else be computed once
+// for all of them and held in registers that the main loop has not.
+__device__ inline int thread_here() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// Calls one(segment) for each item in the workgroup's part of the range.
+template <int RQ, typename F> __device__ inline void each_segment(const AttnArgs& a, F one) {
+    __shared__ typename Work<RQ>::Shared shared;
+    int64_t all;
+    Work<RQ> work(a, shared, all);
+    // neighbours in the range on the same die, behind one L2 (the items of one head read the same cache)
+    const int per_die = (int)gridDim.x >> 3, w = ((int)blockIdx.x & 7) * per_die + ((int)blockIdx.x >> 3);
+    const int64_t step = max(quotient_up(all, gridDim.x), (int64_t)(a.even ? 1 : STEP_MIN));
+    const int64_t begin = w * step, end = min(all, begin + step);
+    if (a.cuts && threadIdx.x == 0) a.cuts[w].step = 0;
+    int64_t pos = begin;
+    while (pos < end) {
+        Segment s;
+        s.f = work.find(pos);
+        const int64_t seq_end = s.f.start + (int64_t)s.f.cost * s.f.groups * a.c.heads;
+        int item = (int)((float)(pos - s.f.start) / (float)s.f.cost);        // fewer than 2^20: within one of the quotient
+        while ((int64_t)item * s.f.cost > pos - s.f.start) --item;
+        while ((int64_t)(item + 1) * s.f.cost <= pos - s.f.start) ++item;
+        item = scalar(item);
+        for (; pos < end && pos < seq_end; ++item) {
+            const int64_t start = s.f.start + (int64_t)item * s.f.cost;
+            const int from = (int)(pos - start), to = (int)min((int64_t)s.f.cost, end - start);
+            pos = start + to;
+            s.h = scalar(item / s.f.groups);
+            s.qg = item - s.h * s.f.groups;
+            s.row0 = s.qg * RQ;
+            s.nrows = min(min(s.f.n, a.max_q) * a.G - s.row0, RQ);
+            s.ctx = s.f.len - s.f.n;
+            s.len = min(s.f.len, a.cap);
+            const int tiles = (s.len + CACHE_TILE - 1) / CACHE_TILE;
+            if (a.even) {
+                s.t0 = (int)((int64_t)tiles * from / s.f.cost);
+                s.t1 = (int)((int64_t)tiles * to / s.f.cost);
+            } else {
+                s.t0 = max(from - BEGIN, 0);
+                s.t1 = max(to - BEGIN, 0);
+            }
+            // the tiles that any of the rows can see
+            const int seen = a.mask ? s.len : min(s.len, s.ctx + (s.row0 + s.nrows - 1) / a.G + 1);
+            s.t0 = scalar(s.t0);
+            s.t1 = scalar(min(s.t1, (max(seen, 0) + CACHE_TILE - 1) / CACHE_TILE));
+            s.part = from == 0 && to == s.f.cost ? -1 : start + from == begin ? 2 * w : 2 * w + 1;
+            if (to < s.f.cost && threadIdx.x == 0)
+                a.cuts[w] = {start, start + s.f.cost, step, s.f.first, min(s.f.n, a.max_q) * a.G, s.h, s.qg};
+            one(s);
         }
     }
-    __syncthreads();
-    u = {scalar(found.b), scalar(found.chunk), scalar(found.chunks), scalar(found.tiles), scalar(found.split), scalar(found.part)};
-    return scalar(any) != 0;
 }
 
 // Eight whole numbers of the cache as f16
@@ -173,9 +259,15 @@ __device__ inline h8 from_bytes(uint32_t x, uint32_t y) {
                 as_h2(__builtin_amdgcn_perm(e, y, 0x04010400u)) - off, as_h2(__builtin_amdgcn_perm(e, y, 0x04030402u)) - off);
 }
 // q4_0: nibbles q + 8, 16 bits apart in x >> s
-__device__ inline h2 from_nibbles(uint32_t x, int s) {
+__device__ inline h2 two_nibbles(uint32_t x, int s) {
     const h2 off = {(_Float16)1032.f, (_Float16)1032.f};
     return as_h2(((x >> s) & 0x000F000Fu) | 0x64006400u) - off;
+}
+__device__ inline h8 from_nibbles(uint32_t x) {             // keys
+    return join(two_nibbles(x, 0), two_nibbles(x, 4), two_nibbles(x, 8), two_nibbles(x, 12));
+}
+__device__ inline h8 from_nibbles(uint32_t x, uint32_t y, int s) {      // values: s = 0, or 4 for the upper ones
+    return join(two_nibbles(x, s), two_nibbles(x, 8 + s), two_nibbles(y, s), two_nibbles(y, 8 + s));
 }
 
 // A record as a buffer: of no bytes where there is none to load, which loads nothing and returns zeros.
@@ -185,6 +277,9 @@ struct Record {
     __device__ Record(const uint8_t* base, uint64_t n, int bytes, bool there)
         : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + n * (uint64_t)bytes), 0, there ? bytes : 0, 0x00020000)) {}
     __device__ u32x4 at(int offset) const { return __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0); }
+    __device__ u32x2 at2(int offset) const { return __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0); }
+    __device__ uint32_t word(int offset) const { return __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0); }
+    __device__ uint32_t half(int offset) const { return __builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0); }
 };
 
 template <bool Q8, int NB> struct Keys {
@@ -202,7 +297,7 @@ template <bool Q8, int NB> struct Keys {
             return from_bytes(r[(b & 1) * 2], r[(b & 1) * 2 + 1]);
         } else {
             const uint32_t x = w[b / 2][h * 2 + (b & 1)];
-            return join(from_nibbles(x, 0), from_nibbles(x, 4), from_nibbles(x, 8), from_nibbles(x, 12));
+            return from_nibbles(x);
         }
     }
 };
@@ -219,7 +314,7 @@ template <bool Q8, int NB> struct Values {
         if constexpr (Q8) return from_bytes(w[b][2 * u], w[b][2 * u + 1]);
         else {
             const uint32_t x = w[b / 2][(b & 1) * 2], y = w[b / 2][(b & 1) * 2 + 1];
-            return join(from_nibbles(x, 4 * u), from_nibbles(x, 8 + 4 * u), from_nibbles(y, 4 * u), from_nibbles(y, 8 + 4 * u));
+            return from_nibbles(x, y, 4 * u);
         }
     }
 };
@@ -246,6 +341,13 @@ template <bool F32> __device__ inline void store4(const AttnArgs& a, int64_t row
     }
 }
 
+// Whether new token i, of mask `bits`, sees the token at `pos`; ctx tokens lie before the new ones.
+__device__ inline bool sees(const AttnArgs& a, uint64_t bits, int i, int pos, int ctx, int limit) {
+    const int ahead = pos - ctx;
+    if (pos >= limit) return false;
+    return ahead < 0 || (a.mask ? ahead < 64 && (bits >> ahead & 1) : ahead <= i);
+}
+
 // The 16 rows of one product's columns: q's terms and the running sums.
 template <int TERMS, int NB> struct Rows {
     h8 q[TERMS][NB];
@@ -257,10 +359,10 @@ template <int TERMS, int NB> struct Rows {
 };
 
 template <int TERMS, int NB>
-__device__ inline void load_rows(const AttnArgs& a, const Seq& s, int h, int row, int g, Rows<TERMS, NB>& r) {
+__device__ inline void load_rows(const AttnArgs& a, int first, int h, int row, int g, Rows<TERMS, NB>& r) {
     constexpr bool F32 = TERMS == 2;
     r.i = row / a.G;
-    r.bits = a.mask ? a.mask[s.first + r.i] : 0;
+    r.bits = a.mask ? a.mask[first + r.i] : 0;
     r.m = -__builtin_inff();
     r.off = P_BITS;
     r.l = 0.f;
@@ -268,7 +370,7 @@ __device__ inline void load_rows(const AttnArgs& a, const Seq& s, int h, int row
     for (int j = 0; j < 2 * NB; ++j) r.o[j] = 0.f;
     float v[NB][8];
     float top = 0.f;
-    const int64_t at = (int64_t)(s.first + r.i) * a.ldq + (int64_t)(h * a.G + row % a.G) * (NB * 32) + 8 * g;
+    const int64_t at = (int64_t)(first + r.i) * a.ldq + (int64_t)(h * a.G + row % a.G) * (NB * 32) + 8 * g;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         if constexpr (F32) {
@@ -306,8 +408,42 @@ __device__ inline void load_rows(const AttnArgs& a, const Seq& s, int h, int row
     r.c = fmaxf(__builtin_amdgcn_ldexpf(a.scale * 1.44269504088896340736f, -e), 1e-37f);
 }
 
-// Waves of a SIMD that the registers are dealt out for.
-constexpr int waves_of(int NB, int NQ) { return NB * NQ <= 4 ? 3 : NB * NQ <= 8 ? 2 : 1; }
+// Waves of a SIMD that the registers are dealt out for, and so workgroups of a compute unit.
+constexpr int waves_of(int NB) { return NB <= 6 ? 2 : 1; }
+
+// The weights p of a lane's 8 scores, as f16 terms, from a maximum that is taken anew where a score is
+// far above it; and their sum.
+template <bool F32, typename R> __device__ inline void weights(const float (&sc)[8], R& r, uint32_t (&ph)[4], uint32_t (&pl)[4]) {
+    float top = sc[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i]);
+    top *= r.c;
+    if (__any(top > r.m + P_SLACK)) {
+        const float m1 = fmaxf(r.m, xor_max(top));
+        const float base = m1 == -__builtin_inff() ? 0.f : m1;
+        const float fall = __builtin_amdgcn_exp2f(r.m - base);
+        r.m = m1;
+        r.off = P_BITS - base;
+        r.l *= fall;
+#pragma unroll
+        for (auto& o : r.o) o *= fall;
+    }
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], r.c, r.off));
+        r.l += p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const h2 hi = {(_Float16)p[2 * i], (_Float16)p[2 * i + 1]};
+        ph[i] = as_u32(hi);
+        if constexpr (F32) {
+            const h2 lo = {(_Float16)(p[2 * i] - (float)hi[0]), (_Float16)(p[2 * i + 1] - (float)hi[1])};
+            pl[i] = as_u32(lo);
+        }
+    }
+}
 
 // What a wave knows of a tile's value scales: their exponent, and the f16 bits from which it must fall.
 struct Exponent {
@@ -317,45 +453,21 @@ struct Exponent {
 
 // F32: rows of f32 (two terms), or bf16 (one). NQ: groups of 16 rows of a workgroup.
 template <bool F32, bool K8, bool V8, int NB, int NQ>
-__global__ __launch_bounds__(THREADS, waves_of(NB, NQ)) void cache_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnArgs a) {
     constexpr int D = NB * 32, TERMS = F32 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) float sh_o[WAVES][16][D + 4];
     __shared__ float sh_m[WAVES][16], sh_l[WAVES][16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
-    const int col = lane & 15, g = lane >> 4;
-    // workgroups that share a chunk (one per QG) are 8 apart: on the same die, behind one L2
-    const int gx = scalar(((int)blockIdx.x >> 3) / a.QG), qg = ((int)blockIdx.x >> 3) - gx * a.QG;
-    const int x = gx * 8 + ((int)blockIdx.x & 7);
-    const int unit = scalar(x / a.c.heads), h = x - unit * a.c.heads;
-    if (unit >= a.units) return;
-    Unit u;
-    int splits;
-    const bool there = find_unit(a, unit, tid, u, &splits);
-    const bool first_of = a.list && h == 0 && qg == 0 && tid == 0;
-    if (first_of && unit == 0) a.list[0] = {min(splits, a.splits), 0, 0, 0};
-    if (!there) return;
-    Seq s = seq_of(a, u.b);
-    s = {scalar(s.first), scalar(s.n), scalar(s.len)};
-    if (first_of && u.chunks > 1 && u.chunk == 0 && u.split < a.splits)
-        a.list[1 + u.split] = {s.first, min(s.n, a.max_q), u.chunks, u.part};
-    const int row0 = qg * NQ * 16;
-    const int nrows = min(min(s.n, a.max_q) * a.G - row0, NQ * 16);    // this workgroup's
-    if (nrows <= 0) return;
-    const int ctx = s.len - s.n, len = min(s.len, a.cap);
-
-    // the tiles that any of the rows can see
-    int seen = len;
-    if (!a.mask) seen = min(seen, ctx + (row0 + nrows - 1) / a.G + 1);
-    const int t0 = u.chunk * u.tiles;
-    const int t1 = scalar(min(t0 + u.tiles, (max(seen, 0) + CACHE_TILE - 1) / CACHE_TILE));
+    each_segment<NQ * 16>(a, [&](const Segment& s) __attribute__((always_inline)) {
+    const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int h = s.h, row0 = s.row0, nrows = s.nrows, ctx = s.ctx, len = s.len, t0 = s.t0, t1 = s.t1;
 
     Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) load_rows<TERMS, NB>(a, s, h, row0 + min(n * 16 + col, nrows - 1), g, r[n]);
+    for (int n = 0; n < NQ; ++n) load_rows<TERMS, NB>(a, s.f.first, h, row0 + min(n * 16 + col, nrows - 1), g, r[n]);
 
     Exponent ex = {15, 0};                                  // no scale yet
     // pages by scalar loads: a vector load would be waited for with every load before it
-    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)u.b * a.ldt);
+    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)s.f.b * a.ldt);
     const int shift = __builtin_ctz(a.c.tiles);
     const auto record = [&](int t, uint32_t page) {
         return ((uint64_t)page * a.c.heads + h) * a.c.tiles + (t & (a.c.tiles - 1));
@@ -428,13 +540,10 @@ __global__ __launch_bounds__(THREADS, waves_of(NB, NQ)) void cache_attn_kernel(A
         if (CACHE_TILE * (t + 1) > min(ctx, limit)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3), ahead = pos - ctx;
+                const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    bool v = pos < limit;
-                    if (ahead >= 0) v = v && (a.mask ? ahead < 64 && (r[n].bits >> ahead & 1) : ahead <= r[n].i);
-                    if (!v) sc[n][i] = -__builtin_inff();
-                }
+                for (int n = 0; n < NQ; ++n)
+                    if (!sees(a, r[n].bits, r[n].i, pos, ctx, limit)) sc[n][i] = -__builtin_inff();
                 if (pos >= limit) {
 #pragma unroll
                     for (int b = 0; b < NB; ++b) vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
@@ -494,35 +603,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB, NQ)) void cache_attn_kernel(A
         uint32_t ph[NQ][4], pl[NQ][4];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            float top = sc[n][0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[n][i]);
-            top *= r[n].c;
-            if (__any(top > r[n].m + P_SLACK)) {
-                const float m1 = fmaxf(r[n].m, xor_max(top));
-                const float base = m1 == -__builtin_inff() ? 0.f : m1;
-                const float fall = __builtin_amdgcn_exp2f(r[n].m - base);
-                r[n].m = m1;
-                r[n].off = P_BITS - base;
-                r[n].l *= fall;
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i) r[n].o[i] *= fall;
-            }
-            float p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(fmaf(sc[n][i], r[n].c, r[n].off));
-                r[n].l += p[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const h2 hi = {(_Float16)p[2 * i], (_Float16)p[2 * i + 1]};
-                ph[n][i] = as_u32(hi);
-                if constexpr (F32) {
-                    const h2 lo = {(_Float16)(p[2 * i] - (float)hi[0]), (_Float16)(p[2 * i + 1] - (float)hi[1])};
-                    pl[n][i] = as_u32(lo);
-                }
-            }
+            weights<F32>(sc[n], r[n], ph[n], pl[n]);
         }
 
         const _Float16 two_k = (_Float16)__builtin_amdgcn_ldexpf(1.f, ex.k);
@@ -561,12 +642,12 @@ __global__ __launch_bounds__(THREADS, waves_of(NB, NQ)) void cache_attn_kernel(A
     }
 
     // the waves' sums
-    const bool split = u.chunks > 1;
-    const int64_t part = split ? (((int64_t)(u.part + u.chunk) * a.c.heads + h) * a.QG + qg) * (NQ * 16) : 0;
+    const bool split = s.part >= 0;
+    const int64_t part = (int64_t)s.part * (NQ * 16);
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         if (n * 16 >= nrows) break;
-        if (n) __syncthreads();
+        __syncthreads();
         const float l = xor_sum(r[n].l);
         if (g == 0) {
             sh_m[wave][col] = r[n].m;
@@ -605,113 +686,411 @@ __global__ __launch_bounds__(THREADS, waves_of(NB, NQ)) void cache_attn_kernel(A
                 }
             } else {
                 const int row = row0 + n * 16 + rr;
-                store4<F32>(a, s.first + row / a.G, h * a.G + row % a.G, D, d, y * (sum == 0.f ? 0.f : 1.f / sum));
+                store4<F32>(a, s.f.first + row / a.G, h * a.G + row % a.G, D, d, y * (sum == 0.f ? 0.f : 1.f / sum));
             }
         }
     }
+    });
 }
 
-// Joins the chunks of the split sequences, a workgroup a row: thread i takes four values of every
-// (THREADS / (D/4))th chunk, and the threads of a place are joined in LDS.
-template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
-    constexpr int D = NB * 32, PLACES = D / 4, WAYS = THREADS / PLACES, AT_ONCE = 4;
-    __shared__ float sh_f[WAYS * AT_ONCE * 8];
-    __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS][PLACES];
-    __shared__ float sh_w[WAVES], sh_s[WAVES];
-    constexpr int MOST = WAYS * AT_ONCE * 8;            // chunks whose factors are kept at once
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int h = (int)blockIdx.y / a.QG, qg = (int)blockIdx.y % a.QG;
-    if ((int)blockIdx.z >= a.list[0].x) return;
-    const int4 seq = a.list[1 + blockIdx.z];
-    const int row = qg * rq + (int)blockIdx.x, chunks = seq.z;
-    if (row >= seq.y * a.G) return;
-    const int64_t step = (int64_t)a.c.heads * a.QG * rq;
-    const int64_t at = ((int64_t)seq.w * a.c.heads + h) * a.QG * rq + row;
-    float top = -__builtin_inff();
-    for (int c = tid; c < chunks; c += THREADS) top = fmaxf(top, a.part_m[at + c * step]);
+// The same for many rows: each of a workgroup's waves has NQ * 16 rows of its own, and all share the tiles,
+// which are turned into f16 operands in LDS once. There a scale can go into its values before the
+// products: keys and values as two f16 terms of d q 2^e for f32 rows (three products: 2^-22 of them is
+// left out), as one for bf16 rows (rounded by 2^-12, where the result is rounded by 2^-9). A row's
+// share of a tile is then its exponentials and nothing else on the vector unit.
+template <bool F32, bool K8, bool V8, int NB, int NQ>
+__global__ __launch_bounds__(THREADS, 2) void cache_attn_rows_kernel(AttnArgs a) {
+    constexpr int D = NB * 32, TERMS = F32 ? 2 : 1, ITEMS = 2 * NB / WAVES;
+    static_assert(NB == 2 || NB == 4, "a wave's pieces of a tile's keys, then of its values; a lane's two scales");
+    // [buffer][term][keys: half, block; values: block, half][lane], 8 f16 each: the products' operands
+    __shared__ __attribute__((aligned(16))) h8 sh[2][TERMS][4 * NB][64];
+    each_segment<WAVES * NQ * 16>(a, [&](const Segment& p) __attribute__((always_inline)) {
+    const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int row_w = wave * NQ * 16;                       // of the workgroup's rows
+    Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    if (lane == 0) sh_w[wave] = top;
-    __syncthreads();
+    for (int n = 0; n < NQ; ++n)
+        load_rows<TERMS, NB>(a, p.f.first, p.h, p.row0 + min(row_w + n * 16 + col, p.nrows - 1), g, r[n]);
+    float c_row[NQ];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sh_w[w]);
-    const int place = tid % PLACES, way = tid / PLACES;
-    float sum = 0.f;
-    f32x4 y = 0.f;
-    for (int c0 = 0; c0 < chunks; c0 += MOST) {
-        if (c0) __syncthreads();
-        for (int c = tid; c < MOST; c += THREADS) {
-            float f = 0.f;
-            if (c0 + c < chunks) {
-                const float m = a.part_m[at + (c0 + c) * step];
-                f = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
-                sum = fmaf(a.part_l[at + (c0 + c) * step], f, sum);
+    for (int n = 0; n < NQ; ++n) c_row[n] = r[n].c;
+
+    Exponent ek = {15, 0}, ev = {15, 0};
+    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)p.f.b * a.ldt);
+    const int shift = __builtin_ctz(a.c.tiles);
+    const auto record = [&](int t, uint32_t page) {
+        return ((uint64_t)page * a.c.heads + p.h) * a.c.tiles + (t & (a.c.tiles - 1));
+    };
+    // A wave's pieces: 16 values of a lane each. Keys (half, pair of blocks): 8 of two blocks of a token;
+    // values (block): 8 tokens of two values. q4_0 pieces are 8 bytes.
+    u32x4 raw[ITEMS], scale[ITEMS];
+    uint32_t all_k = 0, all_v = 0;                          // the tile's scales, two (or one) a lane
+    const auto is_key = [&](int i) { return NB == WAVES ? i == 0 : wave + WAVES * i < NB; };
+    const auto load = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
+        const Record kr(a.kc, rec, cache_record(K8, D), there), vr(a.vc, rec, cache_record(V8, D), there);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int j = wave + WAVES * i;
+            if (is_key(i)) {
+                const int hh = j / (NB / 2), bp = j % (NB / 2);
+                if constexpr (K8) {
+                    raw[i] = kr.at(lane * 16 + j * 1024);
+                } else {
+                    const u32x2 w = kr.at2(lane * 16 + bp * 1024 + hh * 8);
+                    raw[i] = u32x4{w[0], w[1], 0, 0};
+                }
+                const int at = ((col >> 2) * NB * 8 + (col & 3)) * 2;
+                scale[i][0] = kr.half(at + cache_values(K8, D) + bp * 32 + hh * 8);
+                scale[i][1] = kr.half(at + cache_values(K8, D) + bp * 32 + hh * 8 + 16);
+            } else {
+                const int b = j - NB;
+                if constexpr (V8) {
+                    raw[i] = vr.at(lane * 16 + b * 1024);
+                } else {
+                    const u32x2 w = vr.at2(lane * 16 + (b >> 1) * 1024 + (b & 1) * 8);
+                    raw[i] = u32x4{w[0], w[1], 0, 0};
+                }
+                scale[i] = vr.at(g * NB * 16 + cache_values(V8, D) + b * 16);
             }
-            sh_f[c] = f;
+        }
+        if constexpr (NB == 4) {
+            all_k = kr.word(lane * 4 + cache_values(K8, D));
+            all_v = vr.word(lane * 4 + cache_values(V8, D));
+        } else {
+            all_k = kr.half(lane * 2 + cache_values(K8, D));
+            all_v = vr.half(lane * 2 + cache_values(V8, D));
+        }
+    };
+    // An exponent for scales up to one of f16 bits `top` (finite): the largest times 2^k in [2^6, 2^7).
+    const auto anew = [&](uint32_t top, Exponent& e) __attribute__((always_inline)) {
+        const int k = min(15, 7 - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)top)));
+        e.k = k;
+        // the largest f16 below 2^(7 - k); for k = 15 below 2^-8
+        e.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, 6 - k)) | 0x3FF;
+    };
+    const auto largest = [&](uint32_t x) __attribute__((always_inline)) {      // of the finite ones of all lanes
+        uint32_t lo = x & 0x7FFF, hi = x >> 16 & 0x7FFF;
+        if (lo >= 0x7C00) lo = 0;
+        if (hi >= 0x7C00) hi = 0;
+        uint32_t v = max(lo, hi);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+        return (uint32_t)scalar((int)v);
+    };
+    const auto over = [&](uint32_t x, uint32_t limit) __attribute__((always_inline)) {
+        return __any((x & 0x7FFF) > limit || (x >> 16 & 0x7FFF) > limit);
+    };
+
+    int t = p.t0;
+    bool ok = false;
+    uint64_t rec = 0;
+    if (t < p.t1) {
+        const uint32_t page = (uint32_t)table[t >> shift];
+        ok = page < (uint32_t)a.c.pages;
+        rec = record(t, ok ? page : 0);
+        load(rec, true);
+    }
+    int buf = 0;
+#pragma unroll 1
+    for (; t < p.t1; ++t, buf ^= 1) {
+        const int limit = ok ? p.len : 0;
+        const bool more = t + 1 < p.t1, masked = CACHE_TILE * (t + 1) > min(p.ctx, limit);
+        const uint32_t page = (uint32_t)table[(more ? t + 1 : t) >> shift];
+
+        // scales of slots past the sequence are not read as numbers
+        if (CACHE_TILE * (t + 1) > limit) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int e = NB == 4 ? 2 * lane + w : lane;        // entry of the scales: (group, block, token)
+                const int tok = (e / (8 * NB)) * 4 + (e & 3) + ((e >> 2) & 1) * 16;
+                if (CACHE_TILE * t + tok >= limit) {
+                    all_k &= w ? 0x0000FFFFu : 0xFFFF0000u;
+                    all_v &= w ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (!is_key(i)) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (CACHE_TILE * t + 16 * (j >> 2) + 4 * g + (j & 3) >= limit)
+                            scale[i][j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+        }
+        // the exponents, the same in every wave
+        if (over(all_k, ek.limit)) {
+            const uint32_t top = largest(all_k);
+            if (top > ek.limit) {
+                anew(top, ek);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) r[n].c = fmaxf(__builtin_amdgcn_ldexpf(c_row[n], -ek.k), 1e-37f);
+            }
+        }
+        const bool odd = over(all_v, 0x7BFF);               // some value's scale is not finite
+        if (over(all_v, ev.limit)) {
+            const uint32_t top = largest(all_v);
+            if (top > ev.limit) {
+                const int before = ev.k;
+                anew(top, ev);
+                const float fall = __builtin_amdgcn_ldexpf(1.f, ev.k - before);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (auto& o : r[n].o) o *= fall;
+            }
+        }
+        const _Float16 k2 = (_Float16)__builtin_amdgcn_ldexpf(1.f, ek.k), v2 = (_Float16)__builtin_amdgcn_ldexpf(1.f, ev.k);
+
+        // the pieces as operands
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int j = wave + WAVES * i;
+            const auto put = [&](int at, h8 w, h8 d) __attribute__((always_inline)) {
+                const h8 hi = w * d;
+                sh[buf][0][at][lane] = hi;
+                if constexpr (F32) sh[buf][1][at][lane] = __builtin_elementwise_fma(w, d, -hi);
+            };
+            if (is_key(i)) {
+                const int hh = j / (NB / 2), bp = j % (NB / 2);
+#pragma unroll
+                for (int par = 0; par < 2; ++par) {
+                    h8 w;
+                    if constexpr (K8) w = from_bytes(raw[i][2 * par], raw[i][2 * par + 1]);
+                    else w = from_nibbles(raw[i][par]);
+                    const _Float16 d = __builtin_bit_cast(_Float16, (uint16_t)scale[i][par]) * k2;
+                    put(hh * NB + 2 * bp + par, w, h8{d, d, d, d, d, d, d, d});
+                }
+            } else {
+                u32x4 sv = scale[i];
+                if (odd) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        if ((sv[w] & 0x7FFF) >= 0x7C00) sv[w] &= 0xFFFF0000u;
+                        if ((sv[w] >> 16 & 0x7FFF) >= 0x7C00) sv[w] &= 0x0000FFFFu;
+                    }
+                }
+                const h8 d = __builtin_bit_cast(h8, sv) * h8{v2, v2, v2, v2, v2, v2, v2, v2};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    h8 w;
+                    if constexpr (V8) w = from_bytes(raw[i][2 * half], raw[i][2 * half + 1]);
+                    else w = from_nibbles(raw[i][0], raw[i][1], 4 * half);
+                    put(2 * NB + 2 * (j - NB) + half, w, d);
+                }
+            }
         }
         __syncthreads();
-        const int n = min(chunks - c0, MOST);
-        if (way < WAYS) {
-            for (int c = way; c < n; c += WAYS * AT_ONCE) {
-                f32x4 v[AT_ONCE];
+        const uint64_t here = rec;
+        ok = page < (uint32_t)a.c.pages;
+        rec = record(t + 1, ok ? page : 0);                 // (not loaded from where there is none)
+        load(rec, more);
+        if (row_w >= p.nrows) continue;                     // a wave without rows
+
+        // scores
+        float sc[NQ][8];
 #pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i) {
-                    v[i] = 0.f;
-                    if (c + i * WAYS < n)
-                        v[i] = *reinterpret_cast<const f32x4*>(a.part_o + (at + (c0 + c + i * WAYS) * step) * D + place * 4);
+        for (int hh = 0; hh < 2; ++hh) {
+            f32x4 y[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) y[n] = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const h8 kh = sh[buf][0][hh * NB + b][lane];
+                h8 kl;
+                if constexpr (F32) kl = sh[buf][1][hh * NB + b][lane];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    y[n] = mfma(kh, r[n].q[0][b], y[n]);
+                    if constexpr (F32) {
+                        y[n] = mfma(kh, r[n].q[1][b], y[n]);
+                        y[n] = mfma(kl, r[n].q[0][b], y[n]);
+                    }
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i) {
-                    const float f = c + i * WAYS < n ? sh_f[c + i * WAYS] : 0.f;
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = fmaf(v[i][j], f, y[j]);
+                for (int i = 0; i < 4; ++i) sc[n][4 * hh + i] = y[n][i];
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    if (!sees(a, r[n].bits, r[n].i, pos, p.ctx, limit)) sc[n][i] = -__builtin_inff();
+            }
+        }
+        if (odd) {
+            const Record vr(a.vc, here, cache_record(V8, D), true);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                u32x4 d = vr.at(g * NB * 16 + cache_values(V8, D) + b * 16);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    float bad = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if ((d[i >> 1] >> (16 * (i & 1)) & 0x7FFF) >= 0x7C00 && sc[n][i] != -__builtin_inff()) bad = 1.f;
+                    if (xor_max(bad) != 0.f) r[n].o[2 * b] = r[n].o[2 * b + 1] = __builtin_nanf("");
+                }
+            }
+        }
+        uint32_t ph[NQ][4], pl[NQ][4];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) weights<F32>(sc[n], r[n], ph[n], pl[n]);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) {
+            const h8 vh = sh[buf][0][2 * NB + i][lane];
+            h8 vl;
+            if constexpr (F32) vl = sh[buf][1][2 * NB + i][lane];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const h8 hi = __builtin_bit_cast(h8, u32x4{ph[n][0], ph[n][1], ph[n][2], ph[n][3]});
+                r[n].o[i] = mfma(vh, hi, r[n].o[i]);
+                if constexpr (F32) {
+                    const h8 lo = __builtin_bit_cast(h8, u32x4{pl[n][0], pl[n][1], pl[n][2], pl[n][3]});
+                    r[n].o[i] = mfma(vh, lo, r[n].o[i]);
+                    r[n].o[i] = mfma(vl, hi, r[n].o[i]);
                 }
             }
         }
     }
+
+    __syncthreads();                                        // the next segment's operands take the place of these
+    const bool split = p.part >= 0;
+    const int64_t part = (int64_t)p.part * (WAVES * NQ * 16);
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-    if (lane == 0) sh_s[wave] = sum;
-    if (way < WAYS) sh_y[way][place] = y;
-    __syncthreads();
-    if (tid >= PLACES) return;
-    sum = 0.f;
+    for (int n = 0; n < NQ; ++n) {
+        const int rr = row_w + n * 16 + col;
+        const float l = xor_sum(r[n].l);
+        if (rr >= p.nrows) continue;
+        const float back = __builtin_amdgcn_ldexpf(1.f, -ev.k);
+        if (split) {
+            const int64_t to = part + rr;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += sh_s[w];
-    y = 0.f;
+            for (int i = 0; i < 2 * NB; ++i)
+                *reinterpret_cast<f32x4*>(a.part_o + to * D + 16 * i + 4 * g) = r[n].o[i] * back;
+            if (g == 0) {
+                a.part_m[to] = r[n].m;
+                a.part_l[to] = l;
+            }
+        } else {
+            const int row = p.row0 + rr;
+            const float inv = l == 0.f ? 0.f : back / l;
 #pragma unroll
-    for (int w = 0; w < WAYS; ++w) y += sh_y[w][tid];
-    store4<F32>(a, seq.x + row / a.G, h * a.G + row % a.G, D, tid * 4, y * (sum == 0.f ? 0.f : 1.f / sum));
+            for (int i = 0; i < 2 * NB; ++i)
+                store4<F32>(a, p.f.first + row / a.G, p.h * a.G + row % a.G, D, 16 * i + 4 * g, r[n].o[i] * inv);
+        }
+    }
+    });
 }
 
-// Sizes that the host knows: groups of rows, units at most, split sequences and their parts at most.
+// Joins the parts of cut items. Workgroups (x, w): the item that is cut where workgroup w's range ends, if that is its
+// first cut; ROWS of its rows. A row has D/4 threads, four values each, and WAYS such groups of threads,
+// which take its parts in turn and are joined in LDS.
+template <bool F32, int NB, int WAYS> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
+    constexpr int D = NB * 32, PLACES = D / 4, ROWS = THREADS / PLACES / WAYS, AT_ONCE = 4;
+    __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS > 1 ? WAYS : 1][PLACES];
+    __shared__ float sh_m[WAYS], sh_l[WAYS];
+    const int place = (int)threadIdx.x % PLACES, group = (int)threadIdx.x / PLACES;
+    const int way = group % WAYS, w = blockIdx.y;
+    const Cut cut = a.cuts[w];
+    if (cut.step == 0 || w * cut.step > cut.start) return;
+    const int r = (int)blockIdx.x * ROWS + group / WAYS, row = cut.qg * rq + r;
+    const bool live = group < ROWS * WAYS && r < rq && row < cut.rows;
+    // parts: the first is w's, its first segment or its last; then the first segments of the workgroups up to the item's end
+    const int head = w * cut.step == cut.start ? 2 * w : 2 * w + 1;
+    const int chunks = (int)((cut.end - 1) / cut.step) - w + 1;
+    const auto part_at = [&](int c) { return (int64_t)(c == 0 ? head : 2 * (w + c)) * rq + r; };
+    float m = -__builtin_inff(), l = 0.f;
+    f32x4 y = 0.f;
+    for (int c0 = way; live && c0 < chunks; c0 += WAYS * AT_ONCE) {
+        float pm[AT_ONCE], pl[AT_ONCE];
+        f32x4 py[AT_ONCE];
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t p = part_at(min(c0 + i * WAYS, chunks - 1));
+            pm[i] = a.part_m[p];
+            pl[i] = a.part_l[p];
+            py[i] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + place * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+            if (c0 + i * WAYS < chunks) top = fmaxf(top, pm[i]);
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        const float fall = __builtin_amdgcn_exp2f(m - base);
+        m = top;
+        l *= fall;
+        y *= fall;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            if (c0 + i * WAYS >= chunks) break;
+            const float f = __builtin_amdgcn_exp2f(pm[i] - base);
+            l = fmaf(pl[i], f, l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaf(py[i][j], f, y[j]);
+        }
+    }
+    if constexpr (WAYS > 1) {
+        if (live) sh_y[way][place] = y;
+        if (live && place == 0) {
+            sh_m[way] = m;
+            sh_l[way] = l;
+        }
+        __syncthreads();
+        if (!live || way) return;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < WAYS; ++w) top = fmaxf(top, sh_m[w]);
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        l = 0.f;
+        y = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAYS; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sh_m[w] - base);
+            l = fmaf(sh_l[w], f, l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaf(sh_y[w][place][j], f, y[j]);
+        }
+    }
+    if (live) store4<F32>(a, cut.first + row / a.G, cut.h * a.G + row % a.G, D, place * 4, y * (l == 0.f ? 0.f : 1.f / l));
+}
+
+// What the host knows: the kernel, its rows, and workgroups at most.
 struct Plan {
-    int64_t NQ, QG, units, splits, parts;
+    int64_t NQ, RQ, blocks;
+    int64_t spare;
+    bool shared, even, cut, wide;       // the kernel: waves with rows of their own; the join: a workgroup a row
 };
 Plan plan_of(const CacheShape& c, const AttnShape& a) {
     Plan p;
-    const int64_t G = a.Hq / c.heads;
-    p.NQ = a.max_q * G <= 16 || c.D > 128 ? 1 : 2;
-    p.QG = ceil_div(a.max_q * G, p.NQ * 16);
-    const int64_t tiles = std::max<int64_t>(1, a.width * c.tiles);      // of a sequence, at most
-    const int64_t aim = std::max<int64_t>(1, TARGET / (c.heads * p.QG));
-    // sum over b of ceil(tiles_b / chunk) <= aim + B, and a split sequence has at most twice its share
-    const int64_t most = ceil_div(tiles, CHUNK_MIN);
-    p.units = std::min(aim + a.B, a.B * most);
-    p.splits = most > 1 ? std::min(aim, a.B) : 0;
-    p.parts = most > 1 ? std::min(2 * aim, a.B * most) : 0;
+    const int64_t rows = a.max_q * (a.Hq / c.heads);
+    p.shared = rows > 48 && c.D <= 128;
+    p.NQ = rows <= (p.shared ? 64 : 16) || c.D > 128 ? 1 : 2;
+    p.RQ = p.NQ * 16 * (p.shared ? WAVES : 1);
+    const int64_t most = std::max<int64_t>(1, a.width * c.tiles);      // tiles of a sequence
+    const int64_t items = a.B * ceil_div(rows, p.RQ) * c.heads;
+    const int64_t card = 256 * waves_of((int)c.D / 32);                 // workgroups that run at once
+    p.cut = most > WHOLE;
+    p.even = !p.cut || items <= card / 4;
+    p.spare = p.cut && p.even ? card - items : 0;
+    const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * STEP_MIN), STEP_MIN) : 1);
+    p.blocks = std::min(p.cut ? card : 2 * card, round_up(parts, 8));
+    p.wide = p.RQ < 64;
     return p;
 }
 
 struct Workspace {
-    int64_t list, m, l, o, bytes;
+    int64_t cuts, m, l, o, bytes;
 };
 Workspace workspace_of(const CacheShape& c, const Plan& p) {
     Workspace w = {};
-    if (!p.splits) return w;
-    const int64_t rows = p.parts * c.heads * p.QG * p.NQ * 16;
-    w.list = 0;
-    w.m = round_up((p.splits + 1) * 16, REGION_ALIGN);
+    if (!p.cut) return w;
+    const int64_t rows = 2 * p.blocks * p.RQ;
+    w.cuts = 0;
+    w.m = round_up(p.blocks * (int64_t)sizeof(Cut), REGION_ALIGN);
     w.l = w.m + round_up(rows * 4, REGION_ALIGN);
     w.o = w.l + round_up(rows * 4, REGION_ALIGN);
     w.bytes = w.o + rows * c.D * 4;
@@ -742,10 +1121,9 @@ template <typename F> void by_shape(mmq_otype o, mmq_wtype tk, mmq_wtype tv, int
 
 }  // namespace
 
-// the first launch's workgroups stay below 2^24, the second's rows of the grid below 2^16
+// an item's number stays an int32
 bool cache_attn_grid_ok(const CacheShape& c, const AttnShape& a) {
-    const Plan p = plan_of(c, a);
-    return p.QG * round_up(p.units * c.heads, 8) < (int64_t(1) << 24) && c.heads * p.QG < 65536;
+    return ceil_div(a.max_q * (a.Hq / c.heads), 16) * c.heads < (int64_t(1) << 20);
 }
 
 size_t cache_attn_workspace_bytes(const CacheShape& c, const AttnShape& a) {
@@ -777,28 +1155,33 @@ hipError_t launch_cache_attn(mmq_otype o, const void* q, int64_t ldq, mmq_wtype 
     a.B = (int)s.B;
     a.max_q = (int)s.max_q;
     a.G = s.Hq / c.heads;
-    a.QG = (int)p.QG;
     a.cap = (int)std::min<int64_t>(s.width * c.tiles * CACHE_TILE, (int64_t(1) << 31) - CACHE_TILE);
-    a.units = (int)p.units;
-    a.splits = (int)p.splits;
-    if (p.splits) {
-        a.list = reinterpret_cast<int4*>(base + w.list);
+    a.even = p.even;
+    a.spare = (int)p.spare;
+    if (p.cut) {
+        a.cuts = reinterpret_cast<Cut*>(base + w.cuts);
         a.part_m = reinterpret_cast<float*>(base + w.m);
         a.part_l = reinterpret_cast<float*>(base + w.l);
         a.part_o = reinterpret_cast<float*>(base + w.o);
     }
-    const dim3 grid((unsigned)(p.QG * round_up(p.units * c.heads, 8)));
+    const dim3 grid((unsigned)p.blocks);
     by_shape(o, tk, tv, c.D, [&](auto f32, auto k8, auto v8, auto nb) {
         constexpr bool F = decltype(f32)::value, K = decltype(k8)::value, V = decltype(v8)::value;
         constexpr int NB = decltype(nb)::value;
-        if (p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, dim3(THREADS), 0, stream, a);
-        if constexpr (NB <= 4)
-            if (p.NQ == 2) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 2>), grid, dim3(THREADS), 0, stream, a);
-        if (p.splits)
-            hipLaunchKernelGGL((cache_join_kernel<F, NB>),
-                               dim3((unsigned)std::min<int64_t>(p.NQ * 16, s.max_q * a.G), (unsigned)(c.heads * p.QG),
-                                    (unsigned)p.splits),
-                               dim3(THREADS), 0, stream, a, (int)p.NQ * 16);
+        const dim3 threads(THREADS);
+        if constexpr (NB <= 4) {
+            if (p.shared && p.NQ == 1) hipLaunchKernelGGL((cache_attn_rows_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
+            else if (p.shared) hipLaunchKernelGGL((cache_attn_rows_kernel<F, K, V, NB, 2>), grid, threads, 0, stream, a);
+            else if (p.NQ == 2) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 2>), grid, threads, 0, stream, a);
+        }
+        if (!p.shared && p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
+        const int64_t rows = std::min<int64_t>(p.RQ, s.max_q * a.G);
+        constexpr int WAYS = THREADS / (NB * 8);
+        if (p.cut && p.wide)
+            hipLaunchKernelGGL((cache_join_kernel<F, NB, WAYS>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a, (int)p.RQ);
+        else if (p.cut)
+            hipLaunchKernelGGL((cache_join_kernel<F, NB, 1>), dim3((unsigned)ceil_div(rows, WAYS), (unsigned)p.blocks), threads, 0, stream,
+                               a, (int)p.RQ);
     });
     return hipGetLastError();
 }

@@ -466,7 +466,8 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  *          tokens past width * page, are not seen. Pages may be shared by sequences.
  *  lens    (device) int32 [B]; a negative length is 0
  *  starts  (device) int32 [B + 1], rising, in [0, rows]; a sequence whose starts are not has no
- *          rows. Rows outside every sequence are left untouched.
+ *          rows. Rows outside every sequence are left untouched; a row of two sequences holds the
+ *          result of one of them.
  *  max_q   the largest n: rows of a sequence past its max_q are left untouched
  *  mask    (device) uint64 [rows] or NULL
  *  scale   finite and > 0 (D^-0.5, as a rule)
@@ -479,7 +480,7 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  * a sequence's length may hold anything; a scale that is not finite in a token that a row does not
  * see changes nothing for that row.
  * Limits (MMQ_EINVAL): rows <= 2^24, 1 <= B <= 4096, 1 <= max_q <= rows, width <= 2^22, and
- * ceil(max_q * G / 16) * heads < 65536, with the launch below 2^24 workgroups. */
+ * ceil(max_q * G / 16) * heads < 2^20. */
 mmq_status mmq_cache_attn(mmq_otype o, const void* q, int64_t ldq, int64_t rows, int64_t heads_q, mmq_wtype tk,
                           const void* kcache, mmq_wtype tv, const void* vcache, int64_t pages, int64_t page,
                           int64_t heads, int64_t D, const int32_t* table, int64_t ldt, int64_t width,

@@ -94,15 +94,16 @@ def load(cache, kind, side):
     return x.transpose(0, 2, 3, 1, 4, 5).reshape(pages * tiles * 32, heads, D)
 
 
-def attn(q, k, v, table, lens, starts, page, pages, max_q, mask, scale):
+def attn(q, k, v, table, lens, starts, page, pages, max_q, mask, scale, backwards=False):
     """(out, bound) of attention: out [rows, heads_q, D] in 64 bits, NaN for rows that are not computed,
     from q [rows, heads_q, D] and the slots' values k, v [slots, heads, D]; and the sums of magnitudes
-    that the bounds of errors are made of: (sum p |v|, max |score|'s terms sum |q k| scale)."""
+    that the bounds of errors are made of: (sum p |v|, max |score|'s terms sum |q k| scale). backwards: of two
+    sequences with a row in common the first has it, not the last."""
     rows, heads_q, D = q.shape
     G = heads_q // k.shape[1]
     out = np.full(q.shape, np.nan)
     mag, terms = np.zeros(q.shape), np.zeros(q.shape[:2])
-    for b in range(len(lens)):
+    for b in sorted(range(len(lens)), reverse=backwards):
         first, end = int(starts[b]), int(starts[b + 1])
         if not 0 <= first <= end <= rows:
             continue

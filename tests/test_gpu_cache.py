@@ -201,11 +201,11 @@ class Case:
         return self.mmq.cache_attn(self.q, self.kc, self.vc, self.td, self.ld, self.sd, self.max_q, self.kt, self.vt,
                                    mask=self.md, scale=self.scale, **kw)
 
-    def want(self):
+    def want(self, backwards=False):
         k, v = (cachemodel.load(self.host[s], t, s) for s, t in (("k", self.kt), ("v", self.vt)))
         with np.errstate(invalid="ignore"):
             out, mag, terms = cachemodel.attn(self.qh.astype(np.float64), k, v, self.table, self.lens, self.starts, self.page,
-                                              self.pages, self.max_q, self.mask, self.scale)
+                                              self.pages, self.max_q, self.mask, self.scale, backwards)
         N = int(self.lens.max(initial=0))
         T = terms[:, :, None]
         ds = (2 * self.D + 24) * 2 * U24 * T + 2.0 ** -22 * T
@@ -327,7 +327,8 @@ def test_hidden_tokens_that_are_not_finite_change_nothing(env, dt):
 
 
 def test_pages_outside_the_cache_and_starts_out_of_order(env):
-    """Tokens of no page are not seen; a sequence whose rows are not in the batch has none."""
+    """Tokens of no page are not seen; a sequence whose rows are not in the batch has none; a row that two
+    sequences have holds the result of one of them."""
     c = Case(env, lens=(100, 100, 100, 100), news=(2, 3, 2, 2), D=64, seed=7)
     c.table[0, 1], c.table[0, 0] = c.pages, -5
     c.table[1, :] = np.iinfo(np.int32).max
@@ -335,7 +336,11 @@ def test_pages_outside_the_cache_and_starts_out_of_order(env):
     for starts in ([0, 2, 1, 7, 9], [-1, 2, 5, 7, 9], [0, 2, 5, 7, 10], [0, 2, 5, 9, 7]):
         c.starts = np.array(starts, np.int32)
         c.sd = c.torch.from_numpy(c.starts).cuda()
-        c.check()
+        got = c.run().cpu().numpy().astype(np.float64)
+        (last, near), (first, near1) = c.want(), c.want(backwards=True)
+        none = np.isnan(last)
+        assert np.array_equal(none, np.isnan(first))
+        assert np.all((np.abs(got - last) <= near)[~none] | (np.abs(got - first) <= near1)[~none])
     c.lens = np.array([-3, 100, np.iinfo(np.int32).max, np.iinfo(np.int32).min], np.int32)
     c.starts = np.array([0, 2, 5, 7, 9], np.int32)
     c.ld, c.sd = c.torch.from_numpy(c.lens).cuda(), c.torch.from_numpy(c.starts).cuda()
