@@ -330,7 +330,7 @@ CacheShape cache_shape(int64_t pages, int64_t page, int64_t heads, int64_t D) {
     return {(int)pages, (int)(page / CACHE_TILE), (int)heads, (int)D};
 }
 bool cache_rows_ok(int64_t rows, int64_t heads, int64_t D) {
-    return rows >= 1 && rows <= MAX_DIM && product_le(rows, heads, D, (int64_t(1) << 35) - 1);
+    return rows >= 1 && rows <= MAX_DIM && product_le(rows, heads, D, (int64_t(1) << 34) - 1);
 }
 // The checks that writing and reading share; the pointers are checked by both.
 mmq_status cache_rows_args(mmq_otype o, int64_t ldk, int64_t ldv, int64_t rows, mmq_wtype tk, mmq_wtype tv,

@@ -58,13 +58,42 @@ def store(record, t, q, d16, kind, side):
 
 
 def write(cache, x, slots, kind, side):
-    """Rows x [rows, heads, D] into a cache [pages, heads, page/32, record] (uint8, changed in place)."""
-    pages, heads, tiles, _ = cache.shape
-    q, d = quantize(x, kind)
-    for row, slot in enumerate(slots):
-        if 0 <= slot < pages * tiles * 32:
-            for h in range(heads):
-                store(cache[slot // (32 * tiles), h, slot // 32 % tiles], slot % 32, q[row, h], d[row, h], kind, side)
+    """Rows x [rows, heads, D] into a cache [pages, heads, page/32, record] (uint8, changed in place): store() of
+    every row whose slot is in the cache, all at once."""
+    pages, heads, tiles, rec = cache.shape
+    D = x.shape[2]
+    slots = np.asarray(slots, np.int64)
+    keep = np.nonzero((slots >= 0) & (slots < pages * tiles * 32))[0]
+    if keep.size == 0:
+        return
+    q, d = quantize(np.asarray(x)[keep], kind)
+    slot, head = slots[keep][:, None, None, None], np.arange(heads)[None, :, None, None]
+    base = ((slot // (32 * tiles) * heads + head) * tiles + slot // 32 % tiles) * rec
+    t = slot % 32
+    b, i = np.arange(D // 32)[None, None, :, None], np.arange(32)[None, None, None, :]
+    r, h, a, s = t % 16, t // 16, (t % 16) // 4, 4 * (t // 16) + t % 4
+    n = D * (32 if kind == "q8_0" else 16)
+    flat = cache.reshape(-1)
+    if kind == "q8_0":
+        if side == "k":
+            at = ((h * (D // 64) + b // 2) * 64 + (i // 8) * 16 + r) * 16 + (b % 2) * 8 + i % 8
+        else:
+            at = (b * 64 + a * 16 + i % 16) * 16 + (i // 16) * 8 + s
+        flat[base + at] = (q + 128).astype(np.uint8)
+    else:
+        if side == "k":
+            at = (((b // 2) * 64 + (i // 8) * 16 + r) * 2 + h) * 8 + (b % 2) * 4 + _nibble(i) // 2
+            shift = 4 * (_nibble(i) % 2)
+        else:
+            at = ((b // 2) * 64 + a * 16 + i % 16) * 16 + (b % 2) * 8 + 4 * (t // 16) + (t % 4) // 2 + 2 * (t % 2)
+            shift = 4 * (i // 16)
+        at, shift = np.broadcast_to(base + at, q.shape), np.broadcast_to(shift, q.shape)
+        for half in (0, 4):                             # the lower nibbles, then the upper
+            of = shift == half
+            flat[at[of]] = (flat[at[of]] & (240 if half == 0 else 15)) | ((q[of] + 8) << half).astype(np.uint8)
+    at = (base + n)[..., 0] + 2 * ((a[..., 0] * (D // 32) + b[..., 0]) * 8 + s[..., 0])
+    bits = np.ascontiguousarray(d).view(np.uint16)
+    flat[at], flat[at + 1] = (bits & 255).astype(np.uint8), (bits >> 8).astype(np.uint8)
 
 
 def load(cache, kind, side):

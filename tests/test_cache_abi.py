@@ -71,6 +71,14 @@ def test_the_model_reads_what_it_writes(kind, side):
     cachemodel.write(cache, x, slots, kind, side)
     got = cachemodel.load(cache, kind, side)[slots]
     assert np.array_equal(got, cachemodel.value_of(*cachemodel.quantize(x, kind)))
+    one = np.zeros_like(cache)                              # and writes what store() does, one by one
+    all_ = np.zeros_like(cache)
+    q, d = cachemodel.quantize(x, kind)
+    for row, slot in enumerate(slots):
+        for h in range(2):
+            cachemodel.store(one[slot // 64, h, slot // 32 % 2], slot % 32, q[row, h], d[row, h], kind, side)
+    cachemodel.write(all_, x, slots, kind, side)
+    assert np.array_equal(one, all_)
 
 
 def _calls(mmq):

@@ -58,7 +58,11 @@ def _garbage(r, shape):
 ROWS = [("f32", "q8_0", "q8_0", 1, 1, 64, 32, 2), ("bf16", "q4_0", "q8_0", 5, 3, 128, 64, 3),
         ("f32", "q8_0", "q4_0", 77, 2, 192, 32, 5), ("bf16", "q4_0", "q4_0", 130, 5, 256, 128, 2),
         ("f32", "q4_0", "q4_0", 64, 4, 128, 256, 2), ("bf16", "q8_0", "q8_0", 300, 1, 64, 64, 8),
-        ("f32", "q8_0", "q8_0", 259, 3, 128, 32, 12)]
+        ("f32", "q8_0", "q8_0", 259, 3, 128, 32, 12),
+        # rows enough for windows of 32, and of 64
+        ("f32", "q8_0", "q4_0", 1700, 8, 128, 64, 40), ("bf16", "q4_0", "q8_0", 2200, 3, 256, 32, 80),
+        ("f32", "q4_0", "q8_0", 4101, 2, 192, 128, 40), ("bf16", "q8_0", "q8_0", 8200, 16, 64, 256, 40),
+        ("f32", "q4_0", "q4_0", 8199, 16, 64, 64, 140)]
 
 
 def _slots(r, rows, pages, page, how):
