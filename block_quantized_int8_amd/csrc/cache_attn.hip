@@ -25,7 +25,7 @@ namespace {
 
 constexpr int WAVES = 4, THREADS = WAVES * 64;
 constexpr int STEP_MIN = 4;                 // tiles of a workgroup's part at least
-constexpr int BEGIN = 6;                    // what beginning an item costs, in tiles
+constexpr int BEGIN = 10;                   // what beginning an item costs, in tiles
 constexpr int64_t WHOLE = 8;                // tiles of a table's row up to which items are not cut
 constexpr float P_BITS = 10.f;              // p is held times 2^10,
 constexpr float P_SLACK = 4.f;              // and the maximum may rise by 4 before it is taken anew
@@ -277,9 +277,6 @@ struct Record {
     __device__ Record(const uint8_t* base, uint64_t n, int bytes, bool there)
         : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + n * (uint64_t)bytes), 0, there ? bytes : 0, 0x00020000)) {}
     __device__ u32x4 at(int offset) const { return __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0); }
-    __device__ u32x2 at2(int offset) const { return __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0); }
-    __device__ uint32_t word(int offset) const { return __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0); }
-    __device__ uint32_t half(int offset) const { return __builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0); }
 };
 
 template <bool Q8, int NB> struct Keys {
@@ -457,6 +454,9 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     constexpr int D = NB * 32, TERMS = F32 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) float sh_o[WAVES][16][D + 4];
     __shared__ float sh_m[WAVES][16], sh_l[WAVES][16];
+    // f32 rows in twos: q's terms would take 64 registers that the main loop has not, and are the same in every wave
+    constexpr bool Q_LDS = F32 && NQ == 2;
+    __shared__ __attribute__((aligned(16))) h8 sh_q[Q_LDS ? NQ * TERMS * NB : 1][64];
     each_segment<NQ * 16>(a, [&](const Segment& s) __attribute__((always_inline)) {
     const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
     const int h = s.h, row0 = s.row0, nrows = s.nrows, ctx = s.ctx, len = s.len, t0 = s.t0, t1 = s.t1;
@@ -464,6 +464,17 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) load_rows<TERMS, NB>(a, s.f.first, h, row0 + min(n * 16 + col, nrows - 1), g, r[n]);
+    if constexpr (Q_LDS) {
+        if (wave == 0) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) sh_q[(n * TERMS + i) * NB + b][lane] = r[n].q[i][b];
+        }
+        __syncthreads();
+    }
 
     Exponent ex = {15, 0};                                  // no scale yet
     // pages by scalar loads: a vector load would be waited for with every load before it
@@ -502,29 +513,31 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
         // 1. the products of scores
         float sc[NQ][8];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            f32x4 acc[NQ];
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) acc[n] = 0.f;
+            for (int i = 0; i < 8; ++i) sc[n][i] = 0.f;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < NB; ++b) {
+            h8 q[NQ][TERMS];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) q[n][i] = Q_LDS ? sh_q[(n * TERMS + i) * NB + b][lane] : r[n].q[i][b];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
                 const h8 kv = kw.get(hh, b);
                 const h2 d0 = as_h2(kw.d[b][2 * hh]), d1 = as_h2(kw.d[b][2 * hh + 1]);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     f32x4 y = 0.f;
 #pragma unroll
-                    for (int i = 0; i < TERMS; ++i) y = mfma(kv, r[n].q[i][b], y);
-                    acc[n][0] = fmaf(y[0], (float)d0[0], acc[n][0]);
-                    acc[n][1] = fmaf(y[1], (float)d0[1], acc[n][1]);
-                    acc[n][2] = fmaf(y[2], (float)d1[0], acc[n][2]);
-                    acc[n][3] = fmaf(y[3], (float)d1[1], acc[n][3]);
+                    for (int i = 0; i < TERMS; ++i) y = mfma(kv, q[n][i], y);
+                    sc[n][4 * hh] = fmaf(y[0], (float)d0[0], sc[n][4 * hh]);
+                    sc[n][4 * hh + 1] = fmaf(y[1], (float)d0[1], sc[n][4 * hh + 1]);
+                    sc[n][4 * hh + 2] = fmaf(y[2], (float)d1[0], sc[n][4 * hh + 2]);
+                    sc[n][4 * hh + 3] = fmaf(y[3], (float)d1[1], sc[n][4 * hh + 3]);
                 }
             }
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sc[n][4 * hh + i] = acc[n][i];
         }
 
         // (the scores are finished before the loads, whose registers the products' operands leave)
@@ -557,8 +570,8 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dtop = __builtin_elementwise_max(dtop, as_u16(vw.d[b][i] & 0x7FFF7FFFu));
-        uint32_t dmax = max(dtop[0], dtop[1]);
+            for (int i = 0; i < 4; ++i) dtop = __builtin_elementwise_max(dtop, as_u16(V8 ? vw.d[b][i] : vw.d[b][i] & 0x7FFF7FFFu));
+        uint32_t dmax = max(dtop[0], dtop[1]);              // (scales of q8_0 are not negative, or look large)
         if (__any(dmax > ex.limit)) {
             if (__any(dmax >= 0x7C00)) {
                 dmax = 0;
@@ -693,312 +706,18 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     });
 }
 
-// The same for many rows: each of a workgroup's waves has NQ * 16 rows of its own, and all share the tiles,
-// which are turned into f16 operands in LDS once. There a scale can go into its values before the
-// products: keys and values as two f16 terms of d q 2^e for f32 rows (three products: 2^-22 of them is
-// left out), as one for bf16 rows (rounded by 2^-12, where the result is rounded by 2^-9). A row's
-// share of a tile is then its exponentials and nothing else on the vector unit.
-template <bool F32, bool K8, bool V8, int NB, int NQ>
-__global__ __launch_bounds__(THREADS, 2) void cache_attn_rows_kernel(AttnArgs a) {
-    constexpr int D = NB * 32, TERMS = F32 ? 2 : 1, ITEMS = 2 * NB / WAVES;
-    static_assert(NB == 2 || NB == 4, "a wave's pieces of a tile's keys, then of its values; a lane's two scales");
-    // [buffer][term][keys: half, block; values: block, half][lane], 8 f16 each: the products' operands
-    __shared__ __attribute__((aligned(16))) h8 sh[2][TERMS][4 * NB][64];
-    each_segment<WAVES * NQ * 16>(a, [&](const Segment& p) __attribute__((always_inline)) {
-    const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int row_w = wave * NQ * 16;                       // of the workgroup's rows
-    Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-        load_rows<TERMS, NB>(a, p.f.first, p.h, p.row0 + min(row_w + n * 16 + col, p.nrows - 1), g, r[n]);
-    float c_row[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) c_row[n] = r[n].c;
-
-    Exponent ek = {15, 0}, ev = {15, 0};
-    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)p.f.b * a.ldt);
-    const int shift = __builtin_ctz(a.c.tiles);
-    const auto record = [&](int t, uint32_t page) {
-        return ((uint64_t)page * a.c.heads + p.h) * a.c.tiles + (t & (a.c.tiles - 1));
-    };
-    // A wave's pieces: 16 values of a lane each. Keys (half, pair of blocks): 8 of two blocks of a token;
-    // values (block): 8 tokens of two values. q4_0 pieces are 8 bytes.
-    u32x4 raw[ITEMS], scale[ITEMS];
-    uint32_t all_k = 0, all_v = 0;                          // the tile's scales, two (or one) a lane
-    const auto is_key = [&](int i) { return NB == WAVES ? i == 0 : wave + WAVES * i < NB; };
-    const auto load = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
-        const Record kr(a.kc, rec, cache_record(K8, D), there), vr(a.vc, rec, cache_record(V8, D), there);
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int j = wave + WAVES * i;
-            if (is_key(i)) {
-                const int hh = j / (NB / 2), bp = j % (NB / 2);
-                if constexpr (K8) {
-                    raw[i] = kr.at(lane * 16 + j * 1024);
-                } else {
-                    const u32x2 w = kr.at2(lane * 16 + bp * 1024 + hh * 8);
-                    raw[i] = u32x4{w[0], w[1], 0, 0};
-                }
-                const int at = ((col >> 2) * NB * 8 + (col & 3)) * 2;
-                scale[i][0] = kr.half(at + cache_values(K8, D) + bp * 32 + hh * 8);
-                scale[i][1] = kr.half(at + cache_values(K8, D) + bp * 32 + hh * 8 + 16);
-            } else {
-                const int b = j - NB;
-                if constexpr (V8) {
-                    raw[i] = vr.at(lane * 16 + b * 1024);
-                } else {
-                    const u32x2 w = vr.at2(lane * 16 + (b >> 1) * 1024 + (b & 1) * 8);
-                    raw[i] = u32x4{w[0], w[1], 0, 0};
-                }
-                scale[i] = vr.at(g * NB * 16 + cache_values(V8, D) + b * 16);
-            }
-        }
-        if constexpr (NB == 4) {
-            all_k = kr.word(lane * 4 + cache_values(K8, D));
-            all_v = vr.word(lane * 4 + cache_values(V8, D));
-        } else {
-            all_k = kr.half(lane * 2 + cache_values(K8, D));
-            all_v = vr.half(lane * 2 + cache_values(V8, D));
-        }
-    };
-    // An exponent for scales up to one of f16 bits `top` (finite): the largest times 2^k in [2^6, 2^7).
-    const auto anew = [&](uint32_t top, Exponent& e) __attribute__((always_inline)) {
-        const int k = min(15, 7 - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)top)));
-        e.k = k;
-        // the largest f16 below 2^(7 - k); for k = 15 below 2^-8
-        e.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, 6 - k)) | 0x3FF;
-    };
-    const auto largest = [&](uint32_t x) __attribute__((always_inline)) {      // of the finite ones of all lanes
-        uint32_t lo = x & 0x7FFF, hi = x >> 16 & 0x7FFF;
-        if (lo >= 0x7C00) lo = 0;
-        if (hi >= 0x7C00) hi = 0;
-        uint32_t v = max(lo, hi);
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-        return (uint32_t)scalar((int)v);
-    };
-    const auto over = [&](uint32_t x, uint32_t limit) __attribute__((always_inline)) {
-        return __any((x & 0x7FFF) > limit || (x >> 16 & 0x7FFF) > limit);
-    };
-
-    int t = p.t0;
-    bool ok = false;
-    uint64_t rec = 0;
-    if (t < p.t1) {
-        const uint32_t page = (uint32_t)table[t >> shift];
-        ok = page < (uint32_t)a.c.pages;
-        rec = record(t, ok ? page : 0);
-        load(rec, true);
-    }
-    int buf = 0;
-#pragma unroll 1
-    for (; t < p.t1; ++t, buf ^= 1) {
-        const int limit = ok ? p.len : 0;
-        const bool more = t + 1 < p.t1, masked = CACHE_TILE * (t + 1) > min(p.ctx, limit);
-        const uint32_t page = (uint32_t)table[(more ? t + 1 : t) >> shift];
-
-        // scales of slots past the sequence are not read as numbers
-        if (CACHE_TILE * (t + 1) > limit) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int e = NB == 4 ? 2 * lane + w : lane;        // entry of the scales: (group, block, token)
-                const int tok = (e / (8 * NB)) * 4 + (e & 3) + ((e >> 2) & 1) * 16;
-                if (CACHE_TILE * t + tok >= limit) {
-                    all_k &= w ? 0x0000FFFFu : 0xFFFF0000u;
-                    all_v &= w ? 0x0000FFFFu : 0xFFFF0000u;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                if (!is_key(i)) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (CACHE_TILE * t + 16 * (j >> 2) + 4 * g + (j & 3) >= limit)
-                            scale[i][j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                }
-        }
-        // the exponents, the same in every wave
-        if (over(all_k, ek.limit)) {
-            const uint32_t top = largest(all_k);
-            if (top > ek.limit) {
-                anew(top, ek);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) r[n].c = fmaxf(__builtin_amdgcn_ldexpf(c_row[n], -ek.k), 1e-37f);
-            }
-        }
-        const bool odd = over(all_v, 0x7BFF);               // some value's scale is not finite
-        if (over(all_v, ev.limit)) {
-            const uint32_t top = largest(all_v);
-            if (top > ev.limit) {
-                const int before = ev.k;
-                anew(top, ev);
-                const float fall = __builtin_amdgcn_ldexpf(1.f, ev.k - before);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (auto& o : r[n].o) o *= fall;
-            }
-        }
-        const _Float16 k2 = (_Float16)__builtin_amdgcn_ldexpf(1.f, ek.k), v2 = (_Float16)__builtin_amdgcn_ldexpf(1.f, ev.k);
-
-        // the pieces as operands
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int j = wave + WAVES * i;
-            const auto put = [&](int at, h8 w, h8 d) __attribute__((always_inline)) {
-                const h8 hi = w * d;
-                sh[buf][0][at][lane] = hi;
-                if constexpr (F32) sh[buf][1][at][lane] = __builtin_elementwise_fma(w, d, -hi);
-            };
-            if (is_key(i)) {
-                const int hh = j / (NB / 2), bp = j % (NB / 2);
-#pragma unroll
-                for (int par = 0; par < 2; ++par) {
-                    h8 w;
-                    if constexpr (K8) w = from_bytes(raw[i][2 * par], raw[i][2 * par + 1]);
-                    else w = from_nibbles(raw[i][par]);
-                    const _Float16 d = __builtin_bit_cast(_Float16, (uint16_t)scale[i][par]) * k2;
-                    put(hh * NB + 2 * bp + par, w, h8{d, d, d, d, d, d, d, d});
-                }
-            } else {
-                u32x4 sv = scale[i];
-                if (odd) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        if ((sv[w] & 0x7FFF) >= 0x7C00) sv[w] &= 0xFFFF0000u;
-                        if ((sv[w] >> 16 & 0x7FFF) >= 0x7C00) sv[w] &= 0x0000FFFFu;
-                    }
-                }
-                const h8 d = __builtin_bit_cast(h8, sv) * h8{v2, v2, v2, v2, v2, v2, v2, v2};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    h8 w;
-                    if constexpr (V8) w = from_bytes(raw[i][2 * half], raw[i][2 * half + 1]);
-                    else w = from_nibbles(raw[i][0], raw[i][1], 4 * half);
-                    put(2 * NB + 2 * (j - NB) + half, w, d);
-                }
-            }
-        }
-        __syncthreads();
-        const uint64_t here = rec;
-        ok = page < (uint32_t)a.c.pages;
-        rec = record(t + 1, ok ? page : 0);                 // (not loaded from where there is none)
-        load(rec, more);
-        if (row_w >= p.nrows) continue;                     // a wave without rows
-
-        // scores
-        float sc[NQ][8];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            f32x4 y[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) y[n] = 0.f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const h8 kh = sh[buf][0][hh * NB + b][lane];
-                h8 kl;
-                if constexpr (F32) kl = sh[buf][1][hh * NB + b][lane];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    y[n] = mfma(kh, r[n].q[0][b], y[n]);
-                    if constexpr (F32) {
-                        y[n] = mfma(kh, r[n].q[1][b], y[n]);
-                        y[n] = mfma(kl, r[n].q[0][b], y[n]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sc[n][4 * hh + i] = y[n][i];
-        }
-        if (masked) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    if (!sees(a, r[n].bits, r[n].i, pos, p.ctx, limit)) sc[n][i] = -__builtin_inff();
-            }
-        }
-        if (odd) {
-            const Record vr(a.vc, here, cache_record(V8, D), true);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                u32x4 d = vr.at(g * NB * 16 + cache_values(V8, D) + b * 16);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    float bad = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if ((d[i >> 1] >> (16 * (i & 1)) & 0x7FFF) >= 0x7C00 && sc[n][i] != -__builtin_inff()) bad = 1.f;
-                    if (xor_max(bad) != 0.f) r[n].o[2 * b] = r[n].o[2 * b + 1] = __builtin_nanf("");
-                }
-            }
-        }
-        uint32_t ph[NQ][4], pl[NQ][4];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) weights<F32>(sc[n], r[n], ph[n], pl[n]);
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-            const h8 vh = sh[buf][0][2 * NB + i][lane];
-            h8 vl;
-            if constexpr (F32) vl = sh[buf][1][2 * NB + i][lane];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const h8 hi = __builtin_bit_cast(h8, u32x4{ph[n][0], ph[n][1], ph[n][2], ph[n][3]});
-                r[n].o[i] = mfma(vh, hi, r[n].o[i]);
-                if constexpr (F32) {
-                    const h8 lo = __builtin_bit_cast(h8, u32x4{pl[n][0], pl[n][1], pl[n][2], pl[n][3]});
-                    r[n].o[i] = mfma(vh, lo, r[n].o[i]);
-                    r[n].o[i] = mfma(vl, hi, r[n].o[i]);
-                }
-            }
-        }
-    }
-
-    __syncthreads();                                        // the next segment's operands take the place of these
-    const bool split = p.part >= 0;
-    const int64_t part = (int64_t)p.part * (WAVES * NQ * 16);
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        const int rr = row_w + n * 16 + col;
-        const float l = xor_sum(r[n].l);
-        if (rr >= p.nrows) continue;
-        const float back = __builtin_amdgcn_ldexpf(1.f, -ev.k);
-        if (split) {
-            const int64_t to = part + rr;
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-                *reinterpret_cast<f32x4*>(a.part_o + to * D + 16 * i + 4 * g) = r[n].o[i] * back;
-            if (g == 0) {
-                a.part_m[to] = r[n].m;
-                a.part_l[to] = l;
-            }
-        } else {
-            const int row = p.row0 + rr;
-            const float inv = l == 0.f ? 0.f : back / l;
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-                store4<F32>(a, p.f.first + row / a.G, p.h * a.G + row % a.G, D, 16 * i + 4 * g, r[n].o[i] * inv);
-        }
-    }
-    });
-}
-
-// Joins the parts of cut items. Workgroups (x, w): the item that is cut where workgroup w's range ends, if that is its
-// first cut; ROWS of its rows. A row has D/4 threads, four values each, and WAYS such groups of threads,
-// which take its parts in turn and are joined in LDS.
-template <bool F32, int NB, int WAYS> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
-    constexpr int D = NB * 32, PLACES = D / 4, ROWS = THREADS / PLACES / WAYS, AT_ONCE = 4;
-    __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS > 1 ? WAYS : 1][PLACES];
+// Joins the parts of cut items. Workgroup (r, w): row r of the item that is cut where workgroup w's range ends,
+// if that is its first cut. A row's D/4 threads have four values each, and there are WAYS such groups of
+// threads, which take its parts in turn and are joined in LDS.
+template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
+    constexpr int D = NB * 32, PLACES = D / 4, WAYS = THREADS / PLACES, AT_ONCE = 4;
+    __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS][PLACES];
     __shared__ float sh_m[WAYS], sh_l[WAYS];
-    const int place = (int)threadIdx.x % PLACES, group = (int)threadIdx.x / PLACES;
-    const int way = group % WAYS, w = blockIdx.y;
+    const int place = (int)threadIdx.x % PLACES, way = (int)threadIdx.x / PLACES, w = blockIdx.y;
     const Cut cut = a.cuts[w];
     if (cut.step == 0 || w * cut.step > cut.start) return;
-    const int r = (int)blockIdx.x * ROWS + group / WAYS, row = cut.qg * rq + r;
-    const bool live = group < ROWS * WAYS && r < rq && row < cut.rows;
+    const int r = blockIdx.x, row = cut.qg * rq + r;
+    const bool live = way < WAYS && row < cut.rows;
     // parts: the first is w's, its first segment or its last; then the first segments of the workgroups up to the item's end
     const int head = w * cut.step == cut.start ? 2 * w : 2 * w + 1;
     const int chunks = (int)((cut.end - 1) / cut.step) - w + 1;
@@ -1033,43 +752,40 @@ template <bool F32, int NB, int WAYS> __global__ __launch_bounds__(THREADS) void
             for (int j = 0; j < 4; ++j) y[j] = fmaf(py[i][j], f, y[j]);
         }
     }
-    if constexpr (WAYS > 1) {
-        if (live) sh_y[way][place] = y;
-        if (live && place == 0) {
-            sh_m[way] = m;
-            sh_l[way] = l;
-        }
-        __syncthreads();
-        if (!live || way) return;
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int w = 0; w < WAYS; ++w) top = fmaxf(top, sh_m[w]);
-        const float base = top == -__builtin_inff() ? 0.f : top;
-        l = 0.f;
-        y = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAYS; ++w) {
-            const float f = __builtin_amdgcn_exp2f(sh_m[w] - base);
-            l = fmaf(sh_l[w], f, l);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = fmaf(sh_y[w][place][j], f, y[j]);
-        }
+    if (live) sh_y[way][place] = y;
+    if (live && place == 0) {
+        sh_m[way] = m;
+        sh_l[way] = l;
     }
-    if (live) store4<F32>(a, cut.first + row / a.G, cut.h * a.G + row % a.G, D, place * 4, y * (l == 0.f ? 0.f : 1.f / l));
+    __syncthreads();
+    if (!live || way) return;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) top = fmaxf(top, sh_m[w]);
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    l = 0.f;
+    y = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sh_m[w] - base);
+        l = fmaf(sh_l[w], f, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = fmaf(sh_y[w][place][j], f, y[j]);
+    }
+    store4<F32>(a, cut.first + row / a.G, cut.h * a.G + row % a.G, D, place * 4, y * (l == 0.f ? 0.f : 1.f / l));
 }
 
 // What the host knows: the kernel, its rows, and workgroups at most.
 struct Plan {
     int64_t NQ, RQ, blocks;
     int64_t spare;
-    bool shared, even, cut, wide;       // the kernel: waves with rows of their own; the join: a workgroup a row
+    bool even, cut;
 };
 Plan plan_of(const CacheShape& c, const AttnShape& a) {
     Plan p;
     const int64_t rows = a.max_q * (a.Hq / c.heads);
-    p.shared = rows > 48 && c.D <= 128;
-    p.NQ = rows <= (p.shared ? 64 : 16) || c.D > 128 ? 1 : 2;
-    p.RQ = p.NQ * 16 * (p.shared ? WAVES : 1);
+    p.NQ = rows <= 16 || c.D > 128 ? 1 : 2;
+    p.RQ = p.NQ * 16;
     const int64_t most = std::max<int64_t>(1, a.width * c.tiles);      // tiles of a sequence
     const int64_t items = a.B * ceil_div(rows, p.RQ) * c.heads;
     const int64_t card = 256 * waves_of((int)c.D / 32);                 // workgroups that run at once
@@ -1078,7 +794,6 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     p.spare = p.cut && p.even ? card - items : 0;
     const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * STEP_MIN), STEP_MIN) : 1);
     p.blocks = std::min(p.cut ? card : 2 * card, round_up(parts, 8));
-    p.wide = p.RQ < 64;
     return p;
 }
 
@@ -1170,18 +885,12 @@ hipError_t launch_cache_attn(mmq_otype o, const void* q, int64_t ldq, mmq_wtype 
         constexpr int NB = decltype(nb)::value;
         const dim3 threads(THREADS);
         if constexpr (NB <= 4) {
-            if (p.shared && p.NQ == 1) hipLaunchKernelGGL((cache_attn_rows_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
-            else if (p.shared) hipLaunchKernelGGL((cache_attn_rows_kernel<F, K, V, NB, 2>), grid, threads, 0, stream, a);
-            else if (p.NQ == 2) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 2>), grid, threads, 0, stream, a);
+            if (p.NQ == 2) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 2>), grid, threads, 0, stream, a);
         }
-        if (!p.shared && p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
+        if (p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
         const int64_t rows = std::min<int64_t>(p.RQ, s.max_q * a.G);
-        constexpr int WAYS = THREADS / (NB * 8);
-        if (p.cut && p.wide)
-            hipLaunchKernelGGL((cache_join_kernel<F, NB, WAYS>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a, (int)p.RQ);
-        else if (p.cut)
-            hipLaunchKernelGGL((cache_join_kernel<F, NB, 1>), dim3((unsigned)ceil_div(rows, WAYS), (unsigned)p.blocks), threads, 0, stream,
-                               a, (int)p.RQ);
+        if (p.cut)
+            hipLaunchKernelGGL((cache_join_kernel<F, NB>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a, (int)p.RQ);
     });
     return hipGetLastError();
 }
