@@ -606,25 +606,30 @@ def cache_shape(ctype, pages: int, page: int, heads: int, D: int) -> tuple[int, 
     return pages, heads, page // 32, nbytes // (pages * heads * (page // 32))
 
 
-def _cache_type(fn: str, name: str, t) -> int:
-    if t not in CACHE_BLOCK:
-        raise ValueError(f"{fn}: {name} must be one of {list(CACHE_BLOCK)}, got {t!r}")
-    return WTYPE[t]
+@functools.lru_cache(maxsize=256)
+def _cache_dims(kshape, vshape, ktype, vtype):
+    """(key type, value type, pages, page, heads, D) of caches of these shapes, None if they are not two of one size."""
+    if len(kshape) != 4 or len(vshape) != 4:
+        return None
+    pages, heads, tiles, rec = kshape
+    D = rec // CACHE_BLOCK[ktype]
+    if rec != D * CACHE_BLOCK[ktype] or vshape != (pages, heads, tiles, D * CACHE_BLOCK[vtype]):
+        return None
+    return WTYPE[ktype], WTYPE[vtype], pages, 32 * tiles, heads, D
 
 
 def _caches(fn: str, kcache, vcache, ktype, vtype):
     """(key type, value type, pages, page, heads, D) of two caches."""
     import torch
-    tk, tv = _cache_type(fn, "ktype", ktype), _cache_type(fn, "vtype", vtype)
-    for name, c, t in (("kcache", kcache, ktype), ("vcache", vcache, vtype)):
-        if c.dtype is not torch.uint8 or c.dim() != 4 or not c.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous uint8 of cache_shape's shape, got {c.dtype} {tuple(c.shape)}")
-    pages, heads, tiles, rec = kcache.shape
-    D = rec // CACHE_BLOCK[ktype]
-    if rec != D * CACHE_BLOCK[ktype] or vcache.shape != (pages, heads, tiles, D * CACHE_BLOCK[vtype]):
-        raise ValueError(f"{fn}: the caches' records must be of one size of head, got {tuple(kcache.shape)} of {ktype} and "
-                         f"{tuple(vcache.shape)} of {vtype}")
-    return tk, tv, pages, 32 * tiles, heads, D
+    for name, t in (("ktype", ktype), ("vtype", vtype)):
+        if t not in CACHE_BLOCK:
+            raise ValueError(f"{fn}: {name} must be one of {list(CACHE_BLOCK)}, got {t!r}")
+    dims = _cache_dims(kcache.shape, vcache.shape, ktype, vtype)
+    if dims is None or kcache.dtype is not torch.uint8 or vcache.dtype is not torch.uint8 or not kcache.is_contiguous() or \
+            not vcache.is_contiguous():
+        raise ValueError(f"{fn}: kcache and vcache must be contiguous uint8 of cache_shape's shape with heads of one size, got "
+                         f"{kcache.dtype} {tuple(kcache.shape)} of {ktype} and {vcache.dtype} {tuple(vcache.shape)} of {vtype}")
+    return dims
 
 
 def _heads_ld(fn: str, name: str, t, heads: int, D: int, dtype) -> tuple[int, int]:

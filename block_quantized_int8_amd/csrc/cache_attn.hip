@@ -24,7 +24,9 @@ namespace mmq {
 namespace {
 
 constexpr int WAVES = 4, THREADS = WAVES * 64;
-constexpr int STEP_MIN = 4;                 // tiles of a workgroup's part at least
+// Tiles of a workgroup's part at least: one a wave, or two where beginning costs more. 3 trees of 5 to 13 tokens
+// 17.8 us with 4 and 16.3 with 8, one token of 777 11.4 and 12.2.
+constexpr int step_min(int rq) { return rq == 16 ? 4 : 8; }
 constexpr int BEGIN = 10;                   // what beginning an item costs, in tiles
 constexpr int64_t WHOLE = 8;                // tiles of a table's row up to which items are not cut
 constexpr float P_BITS = 10.f;              // p is held times 2^10,
@@ -99,16 +101,21 @@ struct Found {
     int64_t start;                          // of the sequence
     int b, first, n, len, cost, groups;     // cost of an item; groups of rows
 };
-__device__ inline int64_t wave_scan(int64_t v, int lane) {          // inclusive sum over the lanes
+template <typename T> __device__ inline T lanes_sum_up(T v, int lane) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int64_t u = __shfl_up((long long)v, o);
+        const T u = __shfl_up(v, o);
         if (lane >= o) v += u;
     }
     return v;
 }
+__device__ inline int64_t wave_scan(int64_t v, int lane) {          // inclusive sum over the lanes
+    return __any(v >= 1 << 24) ? lanes_sum_up((long long)v, lane) : lanes_sum_up((int)v, lane);
+}
 __device__ inline int64_t quotient_up(int64_t x, int64_t n) {       // ceil(x / n), x < 2^60, n < 2^31
-    int64_t q = (int64_t)((double)x / (double)n);                   // within 2^8 of it
+    int64_t q;                                                      // within 2^8 of it
+    if (x < 1 << 24) q = (int)((float)x * __builtin_amdgcn_rcpf((float)n));
+    else q = (int64_t)((double)x / (double)n);
     while (q * n >= x + n) --q;
     while (q * n < x) ++q;
     return scalar(q);
@@ -129,7 +136,10 @@ template <int RQ> struct Work {
         return !a.even ? (tiles ? tiles + BEGIN : 0) : tiles <= share ? min(tiles, 1) : (tiles + share - 1) / share;
     }
     __device__ int groups(const Seq& s) const { return (min(s.n, a.max_q) * a.G + RQ - 1) / RQ; }
+    // the sum of f over all items, and that over the sequences before the thread's
     template <typename F> __device__ int64_t sum_up(F f, int64_t& before) {
+        before = 0;
+        if (a.B == 1) return scalar((int64_t)f(own) * groups(own) * a.c.heads);
         int64_t mine = 0;
         for (int i = 0; i < per && tid * per + i < a.B; ++i) {
             const Seq s = seq(i);
@@ -150,20 +160,21 @@ template <int RQ> struct Work {
     // the whole range; every thread calls it once, before find()
     __device__ Work(const AttnArgs& args, Shared& shared, int64_t& all) : a(args), sh(shared), tid(threadIdx.x), own{0, 0, 0} {
         per = (a.B + THREADS - 1) / THREADS;
-        if (tid * per < a.B) own = seq_of(a, tid * per);
+        if (tid * per < a.B || a.B == 1) own = seq_of(a, a.B == 1 ? 0 : tid * per);
         int64_t before;
         share = 1 << 30;
         if (a.spare) {
             // sum of ceil(tiles / share) <= spare + items = the workgroups
             const int64_t tiles = sum_up([&](const Seq& s) { return seq_tiles(a, s); }, before);
-            share = (int)min(max(quotient_up(tiles, a.spare), (int64_t)STEP_MIN), (int64_t)1 << 30);
-            __syncthreads();
+            share = (int)min(max(quotient_up(tiles, a.spare), (int64_t)step_min(RQ)), (int64_t)1 << 30);
+            if (a.B > 1) __syncthreads();
         }
         all = sum_up([&](const Seq& s) { return cost(s); }, before);
         sh.start[tid] = before;
     }
     // the sequence at `pos` of the range
     __device__ Found find(int64_t pos) {
+        if (a.B == 1) return {0, 0, scalar(own.first), scalar(own.n), scalar(own.len), scalar(cost(own)), scalar(groups(own))};
         __syncthreads();
         int64_t at = sh.start[tid];
         for (int i = 0; i < per && at <= pos && tid * per + i < a.B; ++i) {
@@ -204,7 +215,7 @@ template <int RQ, typename F> __device__ inline void each_segment(const AttnArgs
     Work<RQ> work(a, shared, all);
     // neighbours in the range on the same die, behind one L2 (the items of one head read the same cache)
     const int per_die = (int)gridDim.x >> 3, w = ((int)blockIdx.x & 7) * per_die + ((int)blockIdx.x >> 3);
-    const int64_t step = max(quotient_up(all, gridDim.x), (int64_t)(a.even ? 1 : STEP_MIN));
+    const int64_t step = max(quotient_up(all, gridDim.x), (int64_t)(a.even ? 1 : step_min(RQ)));
     const int64_t begin = w * step, end = min(all, begin + step);
     if (a.cuts && threadIdx.x == 0) a.cuts[w].step = 0;
     int64_t pos = begin;
@@ -221,7 +232,9 @@ template <int RQ, typename F> __device__ inline void each_segment(const AttnArgs
             const int from = (int)(pos - start), to = (int)min((int64_t)s.f.cost, end - start);
             pos = start + to;
             s.h = scalar(item / s.f.groups);
-            s.qg = item - s.h * s.f.groups;
+            // first and last groups of rows in turn: the first rows of a chain see fewer tokens than the last
+            const int i = item - s.h * s.f.groups;
+            s.qg = i & 1 ? s.f.groups - 1 - i / 2 : i / 2;
             s.row0 = s.qg * RQ;
             s.nrows = min(min(s.f.n, a.max_q) * a.G - s.row0, RQ);
             s.ctx = s.f.len - s.f.n;
@@ -710,7 +723,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
 // if that is its first cut. A row's D/4 threads have four values each, and there are WAYS such groups of
 // threads, which take its parts in turn and are joined in LDS.
 template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
-    constexpr int D = NB * 32, PLACES = D / 4, WAYS = THREADS / PLACES, AT_ONCE = 4;
+    constexpr int D = NB * 32, PLACES = D / 4, WAYS = THREADS / PLACES, AT_ONCE = 8;
     __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS][PLACES];
     __shared__ float sh_m[WAYS], sh_l[WAYS];
     const int place = (int)threadIdx.x % PLACES, way = (int)threadIdx.x / PLACES, w = blockIdx.y;
@@ -792,7 +805,8 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     p.cut = most > WHOLE;
     p.even = !p.cut || items <= card / 4;
     p.spare = p.cut && p.even ? card - items : 0;
-    const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * STEP_MIN), STEP_MIN) : 1);
+    const int64_t least = step_min((int)p.RQ);
+    const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * least), least) : 1);
     p.blocks = std::min(p.cut ? card : 2 * card, round_up(parts, 8));
     return p;
 }
