@@ -11,6 +11,9 @@
 // token's keys as 8-byte pieces, its values byte by byte (a record holds 8 tokens' values side by side).
 // Many rows go by windows of 32 or 64 through LDS images of the two or three tiles that consecutive
 // slots can touch, so that memory sees whole 16-byte pieces there; rows of other tiles go one by one.
+//
+// Memory bounds many rows: 32768 of 8 heads of 128 values are read from q8_0 as bf16 in 35.6 us (5.8 TB/s of both
+// sides); 2048 of them written from f32 in 8.5 us (2.5 TB/s, and a launch). Few rows are a launch: one 2.9 us.
 #include <algorithm>
 
 #include "cache.h"

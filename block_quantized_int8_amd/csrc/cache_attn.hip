@@ -1,21 +1,31 @@
 // cache_attn.hip - attention over the block-quantised cache, for one new token a sequence, chains of
 // them and trees of drafted ones.
 //
-// Rows are (new token, query head) pairs that share a head of the cache; a workgroup has 16 of them
-// and a chunk of the sequence's tiles of 32 tokens, its waves take the tiles in turn. Per tile:
+// Rows are (new token, query head) pairs that share a head of the cache; a workgroup has 16 or 32 of them
+// and a part of the sequence's tiles of 32 tokens, its waves take the tiles in turn. Per tile:
 //   1. scores, transposed: S^T = K q^T on the matrix core. int8 or 4-bit whole numbers are exact in
 //      f16; a block of 32 values is one product, whose four sums a lane are scaled by their tokens'
-//      f32 scales. q is held as f16 terms of q 2^e (e: the row's exponent), two for f32 rows, one
-//      for bf16 rows (8 significand bits, exact).
-//   2. p = 2^(score - m), m the running maximum; 2^10 of headroom keeps small p away from f16's
-//      subnormals.
+//      scales in f32. q is held as f16 terms of q 2^e (e: the row's exponent, its largest value in
+//      [2^13, 2^14)): two for f32 rows, which leave 2^-22 of a value, one for bf16 rows, whose 8 bits
+//      it holds exactly down to 2^-30 of the row's largest.
+//   2. p = 2^(score - m), m the running maximum, sums of p in f32; 2^10 of headroom keeps small p away
+//      from f16's subnormals.
 //   3. O^T += V^T P^T. The scale of a token's block of values lies along the sum, so it goes into P:
-//      p d_v 2^k, in two f16 terms for f32 rows, one for bf16 rows. k, the wave's running exponent,
-//      keeps the largest d_v 2^k in [1, 2).
+//      p d_v 2^k, for f32 rows in two f16 terms (the rounding of the first is in the second), for bf16
+//      rows in one, two roundings of 2^-11 of a term, where the result's own is 2^-8. k, the wave's
+//      running exponent, keeps the largest d_v 2^k in [1, 2).
 // A lane holds the tokens of S^T's rows that it needs as P^T's k: the cache's order of tokens makes
 // them the same (cache.h).
-// The waves' sums are joined in LDS. A sequence of several chunks leaves its parts in the workspace,
-// and a second launch joins them.
+// The waves' sums are joined in LDS. Work that several workgroups share leaves its parts in the
+// workspace, and a second launch joins them.
+//
+// What bounds it, and what it reaches (8 heads of 128 values, 4 query heads for each, q8_0 unless said):
+//   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 61 us for 270 MB (4.4 TB/s);
+//     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch adds 5 us.
+//   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
+//     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
+//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens 78 us (0.32 PFLOP/s), a chain of
+//     512 behind 3584 105 us (0.3 PFLOP/s; f32, so twice the products).
 #include <algorithm>
 
 #include "cache.h"
@@ -27,8 +37,11 @@ constexpr int WAVES = 4, THREADS = WAVES * 64;
 // Tiles of a workgroup's part at least: one a wave, or two where beginning costs more. 3 trees of 5 to 13 tokens
 // 17.8 us with 4 and 16.3 with 8, one token of 777 11.4 and 12.2.
 constexpr int step_min(int rq) { return rq == 16 ? 4 : 8; }
-constexpr int BEGIN = 10;                   // what beginning an item costs, in tiles
-constexpr int64_t WHOLE = 8;                // tiles of a table's row up to which items are not cut
+// What beginning an item costs, in tiles. 64 sequences of 128 to 8192 tokens 78, 71, 69 and 71 us with 3, 6, 10 and 14.
+constexpr int BEGIN = 10;
+// Tiles of a table's row up to which items are not cut, so that there is no second launch: 32 tokens that see 700
+// each (22 tiles) 21.4 us with 16 and 15.5 with 24; one that sees 777 (25) 11.0 with 24 and 12.0 with 32.
+constexpr int64_t WHOLE = 24;
 constexpr float P_BITS = 10.f;              // p is held times 2^10,
 constexpr float P_SLACK = 4.f;              // and the maximum may rise by 4 before it is taken anew
 
@@ -42,9 +55,9 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// Where a workgroup's range of tiles ends inside an item, for the second launch.
+// Where a workgroup's part of the launch's range ends inside an item, for the second launch.
 struct Cut {
-    int64_t start, end, step;               // the item's range; tiles of a workgroup (0: no item is cut here)
+    int64_t start, end, step;               // the item's range; length of a workgroup's part (0: no item is cut here)
     int first, rows, h, qg;                 // first row of the sequence, its rows, the item's head and group of rows
 };
 
@@ -175,6 +188,7 @@ template <int RQ> struct Work {
     // the sequence at `pos` of the range
     __device__ Found find(int64_t pos) {
         if (a.B == 1) return {0, 0, scalar(own.first), scalar(own.n), scalar(own.len), scalar(cost(own)), scalar(groups(own))};
+        if (tid == 0) sh.found.cost = 0;                // there always is one, unless the lengths change meanwhile
         __syncthreads();
         int64_t at = sh.start[tid];
         for (int i = 0; i < per && at <= pos && tid * per + i < a.B; ++i) {
@@ -222,6 +236,7 @@ template <int RQ, typename F> __device__ inline void each_segment(const AttnArgs
     while (pos < end) {
         Segment s;
         s.f = work.find(pos);
+        if (s.f.cost <= 0 || s.f.groups <= 0) break;
         const int64_t seq_end = s.f.start + (int64_t)s.f.cost * s.f.groups * a.c.heads;
         int item = (int)((float)(pos - s.f.start) / (float)s.f.cost);        // fewer than 2^20: within one of the quotient
         while ((int64_t)item * s.f.cost > pos - s.f.start) --item;
@@ -418,7 +433,10 @@ __device__ inline void load_rows(const AttnArgs& a, int first, int h, int row, i
     r.c = fmaxf(__builtin_amdgcn_ldexpf(a.scale * 1.44269504088896340736f, -e), 1e-37f);
 }
 
-// Waves of a SIMD that the registers are dealt out for, and so workgroups of a compute unit.
+// Waves of a SIMD that the registers are dealt out for, and so workgroups of a compute unit. 8 blocks of values need
+// the 512 registers of one wave: f32, 4 trees of 60 tokens 100 us, with two waves, which spill, 211. 6 blocks
+// with one wave or two: 512 tokens behind 1500 128 and 101 us (though 32 single tokens of 8000 161 and 182).
+// Three waves of 4 blocks and fewer spill as well: 64 sequences of one 86 us, with two 70.
 constexpr int waves_of(int NB) { return NB <= 6 ? 2 : 1; }
 
 // The weights p of a lane's 8 scores, as f16 terms, from a maximum that is taken anew where a score is
@@ -471,251 +489,252 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     constexpr bool Q_LDS = F32 && NQ == 2;
     __shared__ __attribute__((aligned(16))) h8 sh_q[Q_LDS ? NQ * TERMS * NB : 1][64];
     each_segment<NQ * 16>(a, [&](const Segment& s) __attribute__((always_inline)) {
-    const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int h = s.h, row0 = s.row0, nrows = s.nrows, ctx = s.ctx, len = s.len, t0 = s.t0, t1 = s.t1;
+        const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
+        const int h = s.h, row0 = s.row0, nrows = s.nrows, ctx = s.ctx, len = s.len, t0 = s.t0, t1 = s.t1;
 
-    Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
+        Rows<TERMS, NB> r[NQ];                                  // (past the rows: the last one again)
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) load_rows<TERMS, NB>(a, s.f.first, h, row0 + min(n * 16 + col, nrows - 1), g, r[n]);
-    if constexpr (Q_LDS) {
-        if (wave == 0) {
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int i = 0; i < TERMS; ++i)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) sh_q[(n * TERMS + i) * NB + b][lane] = r[n].q[i][b];
-        }
-        __syncthreads();
-    }
-
-    Exponent ex = {15, 0};                                  // no scale yet
-    // pages by scalar loads: a vector load would be waited for with every load before it
-    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)s.f.b * a.ldt);
-    const int shift = __builtin_ctz(a.c.tiles);
-    const auto record = [&](int t, uint32_t page) {
-        return ((uint64_t)page * a.c.heads + h) * a.c.tiles + (t & (a.c.tiles - 1));
-    };
-    Keys<K8, NB> kw;
-    Values<V8, NB> vw;
-    const auto load_k = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
-        kw.load(Record(a.kc, rec, cache_record(K8, D), there), lane);
-    };
-    const auto load_v = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
-        vw.load(Record(a.vc, rec, cache_record(V8, D), there), lane);
-    };
-    // A tile's keys are loaded while the products of values of the one before run, its values while the
-    // next scores do: the registers are free by then. No such page: its tokens are not seen, and the
-    // first page stands in for it.
-    int t = t0 + wave;
-    bool ok = false;
-    uint64_t rec = 0;
-    if (t < t1) {
-        const uint32_t page = (uint32_t)table[t >> shift];
-        ok = page < (uint32_t)a.c.pages;
-        rec = record(t, ok ? page : 0);
-        load_k(rec, true);
-        load_v(rec, true);
-    }
-#pragma unroll 1
-    for (; t < t1; t += WAVES) {
-        const int limit = ok ? len : 0;
-        const bool more = t + WAVES < t1;
-        const uint32_t page = (uint32_t)table[(more ? t + WAVES : t) >> shift];
-
-        // 1. the products of scores
-        float sc[NQ][8];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc[n][i] = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            h8 q[NQ][TERMS];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int i = 0; i < TERMS; ++i) q[n][i] = Q_LDS ? sh_q[(n * TERMS + i) * NB + b][lane] : r[n].q[i][b];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const h8 kv = kw.get(hh, b);
-                const h2 d0 = as_h2(kw.d[b][2 * hh]), d1 = as_h2(kw.d[b][2 * hh + 1]);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    f32x4 y = 0.f;
-#pragma unroll
-                    for (int i = 0; i < TERMS; ++i) y = mfma(kv, q[n][i], y);
-                    sc[n][4 * hh] = fmaf(y[0], (float)d0[0], sc[n][4 * hh]);
-                    sc[n][4 * hh + 1] = fmaf(y[1], (float)d0[1], sc[n][4 * hh + 1]);
-                    sc[n][4 * hh + 2] = fmaf(y[2], (float)d1[0], sc[n][4 * hh + 2]);
-                    sc[n][4 * hh + 3] = fmaf(y[3], (float)d1[1], sc[n][4 * hh + 3]);
-                }
-            }
-        }
-
-        // (the scores are finished before the loads, whose registers the products' operands leave)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sc[n][i]));
-        ok = page < (uint32_t)a.c.pages;
-        rec = record(t + WAVES, ok ? page : 0);           // (not loaded from where there is none)
-        load_k(rec, more);
-
-        // tokens that a row does not see; scales of slots past the sequence are not read as numbers
-        if (CACHE_TILE * (t + 1) > min(ctx, limit)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
+        for (int n = 0; n < NQ; ++n) load_rows<TERMS, NB>(a, s.f.first, h, row0 + min(n * 16 + col, nrows - 1), g, r[n]);
+        if constexpr (Q_LDS) {
+            if (wave == 0) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    if (!sees(a, r[n].bits, r[n].i, pos, ctx, limit)) sc[n][i] = -__builtin_inff();
-                if (pos >= limit) {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                }
+                    for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) sh_q[(n * TERMS + i) * NB + b][lane] = r[n].q[i][b];
             }
+            __syncthreads();
         }
 
-        // The exponent k of the value scales. One that is not finite counts as 0, after the sums that it
-        // goes into, those of the rows that see its token, are made NaN.
-        u16x2 dtop = 0;
+        Exponent ex = {15, 0};                                  // no scale yet
+        // pages by scalar loads: a vector load would be waited for with every load before it
+        const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + (int64_t)s.f.b * a.ldt);
+        const int shift = __builtin_ctz(a.c.tiles);
+        const auto record = [&](int t, uint32_t page) {
+            return ((uint64_t)page * a.c.heads + h) * a.c.tiles + (t & (a.c.tiles - 1));
+        };
+        Keys<K8, NB> kw;
+        Values<V8, NB> vw;
+        const auto load_k = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
+            kw.load(Record(a.kc, rec, cache_record(K8, D), there), lane);
+        };
+        const auto load_v = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
+            vw.load(Record(a.vc, rec, cache_record(V8, D), there), lane);
+        };
+        // A tile's keys are loaded while the products of values of the one before run, its values while the
+        // next scores do: the registers are free by then. No such page: its tokens are not seen, and the
+        // first page stands in for it.
+        int t = t0 + wave;
+        bool ok = false;
+        uint64_t rec = 0;
+        if (t < t1) {
+            const uint32_t page = (uint32_t)table[t >> shift];
+            ok = page < (uint32_t)a.c.pages;
+            rec = record(t, ok ? page : 0);
+            load_k(rec, true);
+            load_v(rec, true);
+        }
+#pragma unroll 1
+        for (; t < t1; t += WAVES) {
+            const int limit = ok ? len : 0;
+            const bool more = t + WAVES < t1;
+            const uint32_t page = (uint32_t)table[(more ? t + WAVES : t) >> shift];
+
+            // 1. the products of scores
+            float sc[NQ][8];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dtop = __builtin_elementwise_max(dtop, as_u16(V8 ? vw.d[b][i] : vw.d[b][i] & 0x7FFF7FFFu));
-        uint32_t dmax = max(dtop[0], dtop[1]);              // (scales of q8_0 are not negative, or look large)
-        if (__any(dmax > ex.limit)) {
-            if (__any(dmax >= 0x7C00)) {
-                dmax = 0;
+                for (int i = 0; i < 8; ++i) sc[n][i] = 0.f;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float bad[NQ] = {};
+            for (int b = 0; b < NB; ++b) {
+                h8 q[NQ][TERMS];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t d = (vw.d[b][i >> 1] >> (16 * (i & 1))) & 0x7FFF;
-                        if (d < 0x7C00) {
-                            dmax = max(dmax, d);
-                        } else {
-                            vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                            for (int n = 0; n < NQ; ++n)
-                                if (sc[n][i] != -__builtin_inff()) bad[n] = 1.f;
-                        }
+                    for (int i = 0; i < TERMS; ++i) q[n][i] = Q_LDS ? sh_q[(n * TERMS + i) * NB + b][lane] : r[n].q[i][b];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const h8 kv = kw.get(hh, b);
+                    const h2 d0 = as_h2(kw.d[b][2 * hh]), d1 = as_h2(kw.d[b][2 * hh + 1]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        f32x4 y = 0.f;
+#pragma unroll
+                        for (int i = 0; i < TERMS; ++i) y = mfma(kv, q[n][i], y);
+                        sc[n][4 * hh] = fmaf(y[0], (float)d0[0], sc[n][4 * hh]);
+                        sc[n][4 * hh + 1] = fmaf(y[1], (float)d0[1], sc[n][4 * hh + 1]);
+                        sc[n][4 * hh + 2] = fmaf(y[2], (float)d1[0], sc[n][4 * hh + 2]);
+                        sc[n][4 * hh + 3] = fmaf(y[3], (float)d1[1], sc[n][4 * hh + 3]);
                     }
+                }
+            }
+
+            // (the scores are finished before the loads, whose registers the products' operands leave)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sc[n][i]));
+            ok = page < (uint32_t)a.c.pages;
+            rec = record(t + WAVES, ok ? page : 0);           // (not loaded from where there is none)
+            load_k(rec, more);
+
+            // tokens that a row does not see; scales of slots past the sequence are not read as numbers
+            if (CACHE_TILE * (t + 1) > min(ctx, limit)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-                        if (xor_max(bad[n]) != 0.f) r[n].o[2 * b] = r[n].o[2 * b + 1] = __builtin_nanf("");
+                        if (!sees(a, r[n].bits, r[n].i, pos, ctx, limit)) sc[n][i] = -__builtin_inff();
+                    if (pos >= limit) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                    }
                 }
             }
-            dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 16));
-            dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 32));
-            dmax = __builtin_amdgcn_readfirstlane(dmax);
-            if (dmax > ex.limit) {
-                // the largest scale times 2^k in [1, 2), as far as 2^k is an f16
-                const int k = min(15, 1 - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)dmax)));
-                const float fall = __builtin_amdgcn_ldexpf(1.f, k - ex.k);
+
+            // The exponent k of the value scales. One that is not finite counts as 0, after the sums that it
+            // goes into, those of the rows that see its token, are made NaN.
+            u16x2 dtop = 0;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i) r[n].o[i] *= fall;
-                ex.k = k;
-                // the largest f16 below 2^(1 - k)
-                ex.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, -k)) | 0x3FF;
+                for (int i = 0; i < 4; ++i)
+                    dtop = __builtin_elementwise_max(dtop, as_u16(V8 ? vw.d[b][i] : vw.d[b][i] & 0x7FFF7FFFu));
+            uint32_t dmax = max(dtop[0], dtop[1]);              // (scales of q8_0 are not negative, or look large)
+            if (__any(dmax > ex.limit)) {
+                if (__any(dmax >= 0x7C00)) {
+                    dmax = 0;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float bad[NQ] = {};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t d = (vw.d[b][i >> 1] >> (16 * (i & 1))) & 0x7FFF;
+                            if (d < 0x7C00) {
+                                dmax = max(dmax, d);
+                            } else {
+                                vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n)
+                                    if (sc[n][i] != -__builtin_inff()) bad[n] = 1.f;
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+                            if (xor_max(bad[n]) != 0.f) r[n].o[2 * b] = r[n].o[2 * b + 1] = __builtin_nanf("");
+                    }
+                }
+                dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 16));
+                dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 32));
+                dmax = __builtin_amdgcn_readfirstlane(dmax);
+                if (dmax > ex.limit) {
+                    // the largest scale times 2^k in [1, 2), as far as 2^k is an f16
+                    const int k = min(15, 1 - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)dmax)));
+                    const float fall = __builtin_amdgcn_ldexpf(1.f, k - ex.k);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i) r[n].o[i] *= fall;
+                    ex.k = k;
+                    // the largest f16 below 2^(1 - k)
+                    ex.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, -k)) | 0x3FF;
+                }
             }
-        }
 
-        // 2. p, from a maximum that is taken anew where a score is far above it
-        uint32_t ph[NQ][4], pl[NQ][4];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            weights<F32>(sc[n], r[n], ph[n], pl[n]);
-        }
-
-        const _Float16 two_k = (_Float16)__builtin_amdgcn_ldexpf(1.f, ex.k);
-
-        // 3. the products of values
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            h2 d[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = as_h2(vw.d[b][i]) * h2{two_k, two_k};
-            h8 pt[NQ][TERMS];
+            // 2. p, from a maximum that is taken anew where a score is far above it
+            uint32_t ph[NQ][4], pl[NQ][4];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h2 y = as_h2(ph[n][i]) * d[i];
-                    hi[i] = as_u32(y);
-                    if constexpr (F32)
-                        lo[i] = as_u32(__builtin_elementwise_fma(as_h2(pl[n][i]), d[i],
-                                                                 __builtin_elementwise_fma(as_h2(ph[n][i]), d[i], -y)));
-                }
-                pt[n][0] = __builtin_bit_cast(h8, u32x4{hi[0], hi[1], hi[2], hi[3]});
-                if constexpr (F32) pt[n][1] = __builtin_bit_cast(h8, u32x4{lo[0], lo[1], lo[2], lo[3]});
+                weights<F32>(sc[n], r[n], ph[n], pl[n]);
             }
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const h8 vv = vw.get(b, v);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int i = 0; i < TERMS; ++i) r[n].o[2 * b + v] = mfma(vv, pt[n][i], r[n].o[2 * b + v]);
-            }
-        }
-        load_v(rec, more);
-    }
 
-    // the waves' sums
-    const bool split = s.part >= 0;
-    const int64_t part = (int64_t)s.part * (NQ * 16);
+            const _Float16 two_k = (_Float16)__builtin_amdgcn_ldexpf(1.f, ex.k);
+
+            // 3. the products of values
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        if (n * 16 >= nrows) break;
-        __syncthreads();
-        const float l = xor_sum(r[n].l);
-        if (g == 0) {
-            sh_m[wave][col] = r[n].m;
-            sh_l[wave][col] = l;
-        }
-        __syncthreads();
-        float top = -__builtin_inff();
+            for (int b = 0; b < NB; ++b) {
+                h2 d[4];
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sh_m[w][col]);
-        // (a wave that saw nothing counts 0, one whose scores are all NaN, NaN)
-        const float mine = r[n].m == -__builtin_inff() ? 0.f
-                           : __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(r[n].m - top), -ex.k);
+                for (int i = 0; i < 4; ++i) d[i] = as_h2(vw.d[b][i]) * h2{two_k, two_k};
+                h8 pt[NQ][TERMS];
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i)
-            *reinterpret_cast<f32x4*>(&sh_o[wave][col][16 * i + 4 * g]) = r[n].o[i] * mine;
-        __syncthreads();
-        const int left = min(nrows - n * 16, 16);
-        for (int e = tid; e < left * (D / 4); e += THREADS) {
-            const int rr = e / (D / 4), d = e % (D / 4) * 4;
-            float big = -__builtin_inff(), sum = 0.f;
+                for (int n = 0; n < NQ; ++n) {
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) big = fmaxf(big, sh_m[w][rr]);
-            f32x4 y = 0.f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                y += *reinterpret_cast<const f32x4*>(&sh_o[w][rr][d]);
-                const float m = sh_m[w][rr];
-                sum += sh_l[w][rr] * (m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - big));
-            }
-            if (split) {
-                const int64_t to = part + n * 16 + rr;
-                *reinterpret_cast<f32x4*>(a.part_o + to * D + d) = y;
-                if (d == 0) {
-                    a.part_m[to] = big;
-                    a.part_l[to] = sum;
+                    for (int i = 0; i < 4; ++i) {
+                        const h2 y = as_h2(ph[n][i]) * d[i];
+                        hi[i] = as_u32(y);
+                        if constexpr (F32)
+                            lo[i] = as_u32(__builtin_elementwise_fma(as_h2(pl[n][i]), d[i],
+                                                                     __builtin_elementwise_fma(as_h2(ph[n][i]), d[i], -y)));
+                    }
+                    pt[n][0] = __builtin_bit_cast(h8, u32x4{hi[0], hi[1], hi[2], hi[3]});
+                    if constexpr (F32) pt[n][1] = __builtin_bit_cast(h8, u32x4{lo[0], lo[1], lo[2], lo[3]});
                 }
-            } else {
-                const int row = row0 + n * 16 + rr;
-                store4<F32>(a, s.f.first + row / a.G, h * a.G + row % a.G, D, d, y * (sum == 0.f ? 0.f : 1.f / sum));
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const h8 vv = vw.get(b, v);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int i = 0; i < TERMS; ++i) r[n].o[2 * b + v] = mfma(vv, pt[n][i], r[n].o[2 * b + v]);
+                }
+            }
+            load_v(rec, more);
+        }
+
+        // the waves' sums
+        const bool split = s.part >= 0;
+        const int64_t part = (int64_t)s.part * (NQ * 16);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            if (n * 16 >= nrows) break;
+            __syncthreads();
+            const float l = xor_sum(r[n].l);
+            if (g == 0) {
+                sh_m[wave][col] = r[n].m;
+                sh_l[wave][col] = l;
+            }
+            __syncthreads();
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sh_m[w][col]);
+            // (a wave that saw nothing counts 0, one whose scores are all NaN, NaN)
+            const float mine = r[n].m == -__builtin_inff() ? 0.f
+                               : __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(r[n].m - top), -ex.k);
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+                *reinterpret_cast<f32x4*>(&sh_o[wave][col][16 * i + 4 * g]) = r[n].o[i] * mine;
+            __syncthreads();
+            const int left = min(nrows - n * 16, 16);
+            for (int e = tid; e < left * (D / 4); e += THREADS) {
+                const int rr = e / (D / 4), d = e % (D / 4) * 4;
+                float big = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) big = fmaxf(big, sh_m[w][rr]);
+                f32x4 y = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    y += *reinterpret_cast<const f32x4*>(&sh_o[w][rr][d]);
+                    const float m = sh_m[w][rr];
+                    sum += sh_l[w][rr] * (m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - big));
+                }
+                if (split) {
+                    const int64_t to = part + n * 16 + rr;
+                    *reinterpret_cast<f32x4*>(a.part_o + to * D + d) = y;
+                    if (d == 0) {
+                        a.part_m[to] = big;
+                        a.part_l[to] = sum;
+                    }
+                } else {
+                    const int row = row0 + n * 16 + rr;
+                    store4<F32>(a, s.f.first + row / a.G, h * a.G + row % a.G, D, d, y * (sum == 0.f ? 0.f : 1.f / sum));
+                }
             }
         }
-    }
     });
 }
 
@@ -733,7 +752,7 @@ template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_joi
     const bool live = way < WAYS && row < cut.rows;
     // parts: the first is w's, its first segment or its last; then the first segments of the workgroups up to the item's end
     const int head = w * cut.step == cut.start ? 2 * w : 2 * w + 1;
-    const int chunks = (int)((cut.end - 1) / cut.step) - w + 1;
+    const int chunks = (int)min((cut.end - 1) / cut.step + 1, (int64_t)gridDim.y) - w;
     const auto part_at = [&](int c) { return (int64_t)(c == 0 ? head : 2 * (w + c)) * rq + r; };
     float m = -__builtin_inff(), l = 0.f;
     f32x4 y = 0.f;
@@ -797,13 +816,18 @@ struct Plan {
 Plan plan_of(const CacheShape& c, const AttnShape& a) {
     Plan p;
     const int64_t rows = a.max_q * (a.Hq / c.heads);
+    // A second group of 16 rows shares the first's work on a tile, which no more than 16 rows do not need. Above 128
+    // values it has no registers: 192 values, 4 trees of 60 tokens, bf16, 96 us with two groups and 58 with one;
+    // 256 values 79 and 81, 4 chains of 8 tokens 64 and 53 (in f32 the two groups gain a tenth to a fifth there).
     p.NQ = rows <= 16 || c.D > 128 ? 1 : 2;
     p.RQ = p.NQ * 16;
     const int64_t most = std::max<int64_t>(1, a.width * c.tiles);      // tiles of a sequence
     const int64_t items = a.B * ceil_div(rows, p.RQ) * c.heads;
     const int64_t card = 256 * waves_of((int)c.D / 32);                 // workgroups that run at once
     p.cut = most > WHOLE;
-    p.even = !p.cut || items <= card / 4;
+    // Equal parts of items (even) suit few; 128 of one token, 4000 long, 38 us against 32. With 64 the two are alike,
+    // and a call of few short items has one part for each only this way.
+    p.even = !p.cut || items <= card / 8;
     p.spare = p.cut && p.even ? card - items : 0;
     const int64_t least = step_min((int)p.RQ);
     const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * least), least) : 1);

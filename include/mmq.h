@@ -434,7 +434,7 @@ size_t mmq_cache_bytes(mmq_wtype t, int64_t pages, int64_t page, int64_t heads, 
  * slots [rows] (device, int32). A row whose slot is outside [0, pages * page) (-1, say) is not
  * written: of a tree of drafted tokens the accepted ones can be written to their places so. No byte of
  * another slot changes. Slots inside the range must differ from each other (where two are the same,
- * that slot's contents mean nothing). rows <= 2^24, rows * heads * D < 2^34. */
+ * that slot's contents mean nothing). 1 <= rows <= 2^24, rows * heads * D < 2^34. */
 mmq_status mmq_cache_write(mmq_otype o, const void* k, int64_t ldk, const void* v, int64_t ldv,
                            const int32_t* slots, int64_t rows, mmq_wtype tk, void* kcache, mmq_wtype tv,
                            void* vcache, int64_t pages, int64_t page, int64_t heads, int64_t D, void* stream);
