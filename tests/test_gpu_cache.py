@@ -524,3 +524,176 @@ def test_a_query_that_is_not_a_number_gives_none(env, n):
     assert torch.isnan(after[1, 2]).all()
     after[1, 2] = before[1, 2]
     assert torch.equal(after, before)
+
+
+def _lens(n, low, high, seed):
+    return tuple(int(x) for x in np.random.default_rng(seed).integers(low, high, n))
+
+
+# many items and long tables: the work is one range that workgroups cut anywhere
+CUT = [
+    dict(lens=_lens(40, 1, 1500, 1), news=(1,) * 40, D=64, heads=4, page=64),
+    dict(lens=_lens(12, 64, 1400, 2), news=_lens(12, 0, 21, 3), D=128, heads=8, G=2, dt="bf16", kt="q4_0", page=128),
+    dict(lens=_lens(12, 64, 1400, 2), news=_lens(12, 0, 21, 3), D=128, heads=6, G=3, vt="q4_0", tree=True),
+    dict(lens=_lens(9, 64, 1400, 4), news=_lens(9, 1, 65, 5), D=64, heads=3, G=2, dt="bf16", vt="q4_0", tree=True),
+    dict(lens=(1200,), news=(400,), D=64, heads=2, G=4),
+    dict(lens=(1200, 30, 950), news=(200, 30, 1), D=64, heads=2, G=4, dt="bf16", page=256),
+    dict(lens=tuple((i * 37) % 97 + 900 * (i in (7, 500)) for i in range(600)), news=tuple(i % 3 for i in range(600)), D=64,
+         heads=1, G=1),
+    dict(lens=(1100, 1000), news=(2, 20), D=192, heads=8, G=2),
+    dict(lens=(1100, 1000), news=(2, 20), D=256, heads=8, G=4, dt="bf16", kt="q4_0"),
+    dict(lens=(1100, 1000), news=(2, 1), D=256, heads=1, vt="q4_0"),
+    dict(lens=(1030,), news=(1,), D=192, heads=1, G=16, dt="bf16", kt="q4_0", vt="q4_0"),
+    dict(lens=(40,), news=(3,), D=64, width=200),                          # a long table of a short sequence
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=lambda c: f"{len(c['lens'])}of{max(c['lens'])}-D{c['D']}-heads{c.get('heads', 2)}-{c.get('dt', 'f32')}")
+def test_attention_cut_anywhere(env, case):
+    test_attention(env, case)
+
+
+def test_a_table_with_a_stride_and_an_unsigned_mask(env):
+    torch, mmq = env
+    c = Case(env, lens=(100, 64), news=(9, 12), tree=True, D=64, seed=16).device()
+    want = c.check()
+    wide = torch.full((2, c.width + 3), 7, dtype=torch.int32, device="cuda")
+    wide[:, :c.width] = c.td
+    c.td, c.md = wide[:, :c.width], c.md.view(torch.uint64)
+    assert np.array_equal(c.run().cpu().numpy().astype(np.float64).reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_scales_that_are_negative(env, dt):
+    """The quantiser makes none in q8_0, but a scale may have a sign: keys and values of both."""
+    c = Case(env, dt=dt, lens=(150, 1000), news=(3, 1), D=64, page=64, seed=17)
+    for side in "kv":
+        rec = c.host[side]
+        scales = rec[..., 64 * 32:].view(np.uint16)
+        scales ^= (c.r.integers(0, 2, scales.shape) << 15).astype(np.uint16)
+    c.device().check()
+
+
+def test_a_cache_of_more_than_4_gib(env):
+    """Pages below and above 2^32 bytes: what is written, read and attended to there is what a small cache
+    with the same pages gives, and nothing else changes."""
+    torch, mmq = env
+    heads, D, page, G = 8, 256, 256, 2
+    one = mmq.cache_bytes("q8_0", 1, page, heads, D)
+    pages = 2 ** 32 // one + 40
+    print(f"[case] cache of {pages} pages, {pages * one} bytes", flush=True)
+    big = [torch.zeros(mmq.cache_shape("q8_0", pages, page, heads, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    small = [torch.zeros(mmq.cache_shape("q8_0", 5, page, heads, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    at = torch.tensor([pages - 1, 3, 2 ** 32 // one, pages - 7, 2 ** 31 // one], device="cuda")
+    n = 5 * page - 11
+    x = torch.randn(2, n, heads, D, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    slots = (at[pos // page] * page + pos % page).int()
+    for rows in (slice(0, 300), slice(300, n)):             # one by one, and windows of rows
+        mmq.cache_write(x[0, rows], x[1, rows], slots[rows].clone(), *big)
+        mmq.cache_write(x[0, rows], x[1, rows], pos[rows].int(), *small)
+    for b, s in zip(big, small):
+        assert torch.equal(b[at], s)
+        b[at] = 0
+        assert not b.view(torch.int64).any()
+        b[at] = s
+    for rows in (slice(0, 300), slice(0, n)):
+        got, want = mmq.cache_read(slots[rows].clone(), *big), mmq.cache_read(pos[rows].int(), *small)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q = torch.randn(20, heads * G, D, device="cuda")
+    lens, starts = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    got = mmq.cache_attn(q, *big, at.int()[None], lens, starts, 20)
+    want = mmq.cache_attn(q, *small, torch.arange(5, dtype=torch.int32, device="cuda")[None], lens, starts, 20)
+    assert torch.equal(got, want)
+
+
+def test_two_calls_at_once(env):
+    """On two streams, each with a workspace of its own, and from two graphs: the bits of calls by themselves."""
+    torch, mmq = env
+    cases = [Case(env, lens=(3000, 1300), news=(1, 6), D=64, heads=4, page=64, seed=18).device(),
+             Case(env, dt="bf16", lens=(2500, 700, 90), news=(7, 2, 30), D=128, page=64, seed=19).device()]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graphs, held = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(c.run())
+        graphs.append(g)
+    for turn in range(4):
+        for h in held:
+            h.zero_()
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = []
+        for _ in range(5):
+            got = [c.run(stream=s) for c, s in zip(cases, streams)]
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for w, g, h in zip(want, got, held):
+            assert torch.equal(w, g) and torch.equal(w, h)
+
+
+@pytest.mark.parametrize("rows", [200, 2200])
+def test_rows_written_and_read_in_a_graph(env, rows):
+    """One by one and by windows: replayed with other rows and slots, as eager calls."""
+    torch, mmq = env
+    shape = mmq.cache_shape("q8_0", 80, 32, 8, 128)
+    caches = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    x = torch.zeros(2, rows, 8, 128, device="cuda")
+    slots = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    back = torch.zeros(2, rows, 8, 128, device="cuda")
+    def step(kc, vc, back):
+        mmq.cache_write(x[0], x[1], slots, kc, vc)
+        mmq.cache_read(slots, kc, vc, k=back[0], v=back[1])
+    slots.copy_(torch.arange(rows))
+    step(*caches[:2], back)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*caches[:2], back)
+    caches[2].copy_(caches[0])
+    caches[3].copy_(caches[1])
+    for turn in range(4):
+        x.copy_(torch.randn(x.shape, device="cuda"))
+        slots.copy_(torch.arange(rows) + 7 * turn if turn % 2 else torch.randperm(80 * 32)[:rows])
+        g.replay()
+        want = torch.zeros_like(back)
+        step(caches[2], caches[3], want)
+        torch.cuda.synchronize()
+        assert torch.equal(back, want) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+
+
+def test_attention_refusals_of_the_binding(env):
+    torch, mmq = env
+    c = Case(env, lens=(70, 40), news=(2, 3), tree=True, D=64, seed=21).device()
+    def refused(error, match, **kw):
+        a = dict(q=c.q, kcache=c.kc, vcache=c.vc, table=c.td, lens=c.ld, starts=c.sd, max_q=c.max_q, mask=c.md)
+        a.update(kw)
+        with pytest.raises(error, match=match):
+            mmq.cache_attn(**a)
+    refused(ValueError, "mask", mask=c.md.int())
+    refused(ValueError, "mask", mask=c.md[:4])
+    refused(ValueError, "out", out=torch.empty(4, 8, 64, device="cuda"))
+    refused(ValueError, "out", out=torch.empty(5, 8, 64, device="cuda", dtype=torch.bfloat16))
+    refused(ValueError, "heads", q=c.q[:, :3])
+    refused(ValueError, "q", q=c.q.transpose(1, 2))
+    refused(ValueError, "rows", q=c.q.half())
+    refused(ValueError, "table", table=c.td[0])
+    refused(ValueError, "table", table=c.td.long())
+    refused(ValueError, "table", table=c.td.t().contiguous().t())
+    refused(ValueError, "table", lens=c.ld[:1])             # lens says how many sequences there are
+    refused(ValueError, "starts", starts=c.sd[:2])
+    refused(ValueError, "cache", kcache=c.kc[:, :, :, :-34])
+    refused(ValueError, "cache", vcache=c.vc[:-1])
+    refused(ValueError, "type", vtype="q5_0")
+    refused(ValueError, "GPU", lens=c.ld.cpu())
+    refused(mmq.MMQError, "mmq_cache_attn", max_q=0)
+    refused(mmq.MMQError, "mmq_cache_attn", max_q=6)
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        refused(mmq.MMQError, "mmq_cache_attn", scale=scale)
+    wide = Case(env, lens=(1500,), news=(1,), D=64, seed=22).device()
+    with pytest.raises(mmq.MMQError):
+        wide.run(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
