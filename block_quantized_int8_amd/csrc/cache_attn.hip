@@ -21,7 +21,7 @@
 //
 // What bounds it, and what it reaches (8 heads of 128 values, 4 query heads for each, q8_0 unless said):
 //   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 61 us for 270 MB (4.4 TB/s);
-//     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch adds 5 us.
+//     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch takes 5 us.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
 //     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens 78 us (0.32 PFLOP/s), a chain of
@@ -738,38 +738,38 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     });
 }
 
-// Joins the parts of cut items. Workgroup (r, w): row r of the item that is cut where workgroup w's range ends,
+// Joins the parts of cut items. Workgroup (x, w): rows of the item that is cut where workgroup w's range ends,
 // if that is its first cut. A row's D/4 threads have four values each, and there are WAYS such groups of
-// threads, which take its parts in turn and are joined in LDS.
-template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
-    constexpr int D = NB * 32, PLACES = D / 4, WAYS = THREADS / PLACES, AT_ONCE = 8;
-    __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS][PLACES];
-    __shared__ float sh_m[WAYS], sh_l[WAYS];
+// threads. EACH: each has a row of its own, WAYS x on. Else the workgroup has row x, the groups take its
+// parts in turn and are joined in LDS.
+constexpr int ways_of(int NB) { return THREADS / (NB * 8); }
+template <bool F32, int NB, bool EACH> __global__ __launch_bounds__(THREADS) void cache_join_kernel(AttnArgs a, int rq) {
+    constexpr int D = NB * 32, PLACES = D / 4, WAYS = ways_of(NB), STEP = EACH ? 1 : WAYS, AT_ONCE = EACH ? 4 : 8;
     const int place = (int)threadIdx.x % PLACES, way = (int)threadIdx.x / PLACES, w = blockIdx.y;
     const Cut cut = a.cuts[w];
     if (cut.step == 0 || w * cut.step > cut.start) return;
-    const int r = blockIdx.x, row = cut.qg * rq + r;
-    const bool live = way < WAYS && row < cut.rows;
+    const int r = EACH ? blockIdx.x * WAYS + way : blockIdx.x, row = cut.qg * rq + r;
+    const bool live = way < WAYS && r < rq && row < cut.rows;
     // parts: the first is w's, its first segment or its last; then the first segments of the workgroups up to the item's end
     const int head = w * cut.step == cut.start ? 2 * w : 2 * w + 1;
     const int chunks = (int)min((cut.end - 1) / cut.step + 1, (int64_t)gridDim.y) - w;
     const auto part_at = [&](int c) { return (int64_t)(c == 0 ? head : 2 * (w + c)) * rq + r; };
     float m = -__builtin_inff(), l = 0.f;
     f32x4 y = 0.f;
-    for (int c0 = way; live && c0 < chunks; c0 += WAYS * AT_ONCE) {
+    for (int c0 = EACH ? 0 : way; live && c0 < chunks; c0 += STEP * AT_ONCE) {
         float pm[AT_ONCE], pl[AT_ONCE];
         f32x4 py[AT_ONCE];
         float top = m;
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t p = part_at(min(c0 + i * WAYS, chunks - 1));
+            const int64_t p = part_at(min(c0 + i * STEP, chunks - 1));
             pm[i] = a.part_m[p];
             pl[i] = a.part_l[p];
             py[i] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + place * 4);
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i)
-            if (c0 + i * WAYS < chunks) top = fmaxf(top, pm[i]);
+            if (c0 + i * STEP < chunks) top = fmaxf(top, pm[i]);
         const float base = top == -__builtin_inff() ? 0.f : top;
         const float fall = __builtin_amdgcn_exp2f(m - base);
         m = top;
@@ -777,33 +777,38 @@ template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_joi
         y *= fall;
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            if (c0 + i * WAYS >= chunks) break;
+            if (c0 + i * STEP >= chunks) break;
             const float f = __builtin_amdgcn_exp2f(pm[i] - base);
             l = fmaf(pl[i], f, l);
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = fmaf(py[i][j], f, y[j]);
         }
     }
-    if (live) sh_y[way][place] = y;
-    if (live && place == 0) {
-        sh_m[way] = m;
-        sh_l[way] = l;
+    if constexpr (!EACH) {
+        __shared__ __attribute__((aligned(16))) f32x4 sh_y[WAYS][PLACES];
+        __shared__ float sh_m[WAYS], sh_l[WAYS];
+        if (live) sh_y[way][place] = y;
+        if (live && place == 0) {
+            sh_m[way] = m;
+            sh_l[way] = l;
+        }
+        __syncthreads();
+        if (!live || way) return;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < WAYS; ++w) top = fmaxf(top, sh_m[w]);
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        l = 0.f;
+        y = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAYS; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sh_m[w] - base);
+            l = fmaf(sh_l[w], f, l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaf(sh_y[w][place][j], f, y[j]);
+        }
     }
-    __syncthreads();
-    if (!live || way) return;
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int w = 0; w < WAYS; ++w) top = fmaxf(top, sh_m[w]);
-    const float base = top == -__builtin_inff() ? 0.f : top;
-    l = 0.f;
-    y = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAYS; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sh_m[w] - base);
-        l = fmaf(sh_l[w], f, l);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = fmaf(sh_y[w][place][j], f, y[j]);
-    }
+    if (!live) return;
     store4<F32>(a, cut.first + row / a.G, cut.h * a.G + row % a.G, D, place * 4, y * (l == 0.f ? 0.f : 1.f / l));
 }
 
@@ -811,7 +816,7 @@ template <bool F32, int NB> __global__ __launch_bounds__(THREADS) void cache_joi
 struct Plan {
     int64_t NQ, RQ, blocks;
     int64_t spare;
-    bool even, cut;
+    bool even, cut, each;
 };
 Plan plan_of(const CacheShape& c, const AttnShape& a) {
     Plan p;
@@ -829,6 +834,9 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     // and a call of few short items has one part for each only this way.
     p.even = !p.cut || items <= card / 8;
     p.spare = p.cut && p.even ? card - items : 0;
+    // Many items have few parts each: 8 trees of 48 to 64 tokens, both launches, 85.5 us with a row a workgroup and
+    // 79.5 with WAYS. Few have many: one token of 131072 54.9, and 72.6 with WAYS.
+    p.each = !p.even;
     const int64_t least = step_min((int)p.RQ);
     const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * least), least) : 1);
     p.blocks = std::min(p.cut ? card : 2 * card, round_up(parts, 8));
@@ -927,8 +935,12 @@ hipError_t launch_cache_attn(mmq_otype o, const void* q, int64_t ldq, mmq_wtype 
         }
         if (p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
         const int64_t rows = std::min<int64_t>(p.RQ, s.max_q * a.G);
-        if (p.cut)
-            hipLaunchKernelGGL((cache_join_kernel<F, NB>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a, (int)p.RQ);
+        if (p.cut && p.each)
+            hipLaunchKernelGGL((cache_join_kernel<F, NB, true>), dim3((unsigned)ceil_div(rows, ways_of(NB)), (unsigned)p.blocks), threads,
+                               0, stream, a, (int)p.RQ);
+        else if (p.cut)
+            hipLaunchKernelGGL((cache_join_kernel<F, NB, false>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a,
+                               (int)p.RQ);
     });
     return hipGetLastError();
 }
