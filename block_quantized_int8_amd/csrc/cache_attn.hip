@@ -24,8 +24,8 @@
 //     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch takes 5 us.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
-//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens 78 us (0.32 PFLOP/s), a chain of
-//     512 behind 3584 105 us (0.3 PFLOP/s; f32, so twice the products).
+//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 73 us (0.37 PFLOP/s), a chain
+//     of 512 behind 3584, f32 with twice the products, 112 us (0.29 PFLOP/s).
 #include <algorithm>
 
 #include "cache.h"
@@ -824,6 +824,7 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     // A second group of 16 rows shares the first's work on a tile, which no more than 16 rows do not need. Above 128
     // values it has no registers: 192 values, 4 trees of 60 tokens, bf16, 96 us with two groups and 58 with one;
     // 256 values 79 and 81, 4 chains of 8 tokens 64 and 53 (in f32 the two groups gain a tenth to a fifth there).
+    // Four groups leave a SIMD one wave: 8 trees of 48 to 64 tokens 127 us, with two 79.5; 512 tokens 138 and 116.
     p.NQ = rows <= 16 || c.D > 128 ? 1 : 2;
     p.RQ = p.NQ * 16;
     const int64_t most = std::max<int64_t>(1, a.width * c.tiles);      // tiles of a sequence
