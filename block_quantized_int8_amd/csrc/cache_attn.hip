@@ -24,7 +24,7 @@
 //     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch takes 5 us.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
-//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 73 us (0.37 PFLOP/s), a chain
+//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 72 us (0.37 PFLOP/s), a chain
 //     of 512 behind 3584, f32 with twice the products, 112 us (0.29 PFLOP/s).
 #include <algorithm>
 
@@ -473,6 +473,15 @@ template <bool F32, typename R> __device__ inline void weights(const float (&sc)
     }
 }
 
+// A wave's products go before the other wave's softmax: 512 tokens behind 3488, bf16, 76.6 us and 73 so; 2048 behind 2048
+// 242 and 231.5; single tokens alike. (A wave alone on its SIMD has no other: 256 values, 156 us and 174 so.)
+template <bool SHARED> __device__ inline void products_first(bool yes) {
+    if constexpr (SHARED) {
+        if (yes) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
+    }
+}
+
 // What a wave knows of a tile's value scales: their exponent, and the f16 bits from which it must fall.
 struct Exponent {
     int k;
@@ -487,6 +496,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
     __shared__ float sh_m[WAVES][16], sh_l[WAVES][16];
     // f32 rows in twos: q's terms would take 64 registers that the main loop has not, and are the same in every wave
     constexpr bool Q_LDS = F32 && NQ == 2;
+    constexpr bool SHARED = waves_of(NB) > 1;
     __shared__ __attribute__((aligned(16))) h8 sh_q[Q_LDS ? NQ * TERMS * NB : 1][64];
     each_segment<NQ * 16>(a, [&](const Segment& s) __attribute__((always_inline)) {
         const int tid = thread_here(), lane = tid & 63, wave = scalar(tid >> 6), col = lane & 15, g = lane >> 4;
@@ -542,6 +552,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
             const uint32_t page = (uint32_t)table[(more ? t + WAVES : t) >> shift];
 
             // 1. the products of scores
+            products_first<SHARED>(true);
             float sc[NQ][8];
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -644,6 +655,8 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                 }
             }
 
+            products_first<SHARED>(false);
+
             // 2. p, from a maximum that is taken anew where a score is far above it
             uint32_t ph[NQ][4], pl[NQ][4];
 #pragma unroll
@@ -654,6 +667,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
             const _Float16 two_k = (_Float16)__builtin_amdgcn_ldexpf(1.f, ex.k);
 
             // 3. the products of values
+            products_first<SHARED>(true);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 h2 d[4];
@@ -683,6 +697,7 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                         for (int i = 0; i < TERMS; ++i) r[n].o[2 * b + v] = mfma(vv, pt[n][i], r[n].o[2 * b + v]);
                 }
             }
+            products_first<SHARED>(false);
             load_v(rec, more);
         }
 
