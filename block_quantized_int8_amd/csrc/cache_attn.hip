@@ -20,12 +20,12 @@
 // workspace, and a second launch joins them.
 //
 // What bounds it, and what it reaches (8 heads of 128 values, 4 query heads for each, q8_0 unless said):
-//   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 61 us for 270 MB (4.4 TB/s);
-//     one of 131072 tokens, bf16, values in q4_0, 44 us for 218 MB (4.9 TB/s); the second launch takes 5 us.
+//   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 58 us for 277 MB (4.8 TB/s);
+//     one of 131072 tokens, bf16, values in q4_0, 43 us for 218 MB (5.0 TB/s); the second launch takes 5 us.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
 //     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 72 us (0.37 PFLOP/s), a chain
-//     of 512 behind 3584, f32 with twice the products, 112 us (0.29 PFLOP/s).
+//     of 512 behind 3584, f32 with twice the products, 107 us (0.3 PFLOP/s).
 #include <algorithm>
 
 #include "cache.h"
