@@ -37,8 +37,9 @@ constexpr int WAVES = 4, THREADS = WAVES * 64;
 // Tiles of a workgroup's part at least: one a wave, or two where beginning costs more. 3 trees of 5 to 13 tokens
 // 17.8 us with 4 and 16.3 with 8, one token of 777 11.4 and 12.2.
 constexpr int step_min(int rq) { return rq == 16 ? 4 : 8; }
-// What beginning an item costs, in tiles. 64 sequences of 128 to 8192 tokens 78, 71, 69 and 71 us with 3, 6, 10 and 14.
-constexpr int BEGIN = 10;
+// What beginning an item costs, in tiles (a tile of two groups of rows takes about twice the time). 64 sequences of 128 to
+// 8192 tokens, one group, 83.5, 74, 68.5 and 72 us with 2, 5, 10 and 16; 8 trees, two groups, 81.5, 76, 78 and 79.
+constexpr int begin_cost(int rq) { return rq == 16 ? 10 : 5; }
 // Tiles of a table's row up to which items are not cut, so that there is no second launch: 32 tokens that see 700
 // each (22 tiles) 21.4 us with 16 and 15.5 with 24; one that sees 777 (25) 11.0 with 24 and 12.0 with 32.
 constexpr int64_t WHOLE = 24;
@@ -109,7 +110,7 @@ __device__ inline int seq_tiles(const AttnArgs& a, const Seq& s) {
 // from them by itself. An item that is cut leaves parts in the workspace. Two ways to count:
 //   even: an item costs 1 for each of its parts, which are equal and at most `share` tiles long. For
 //         items few enough that the parts' ends do not matter. (Short ones have one part: no second launch.)
-//   tiles: an item costs its tiles and BEGIN more, what beginning an item takes; workgroups end anywhere.
+//   tiles: an item costs its tiles and begin_cost more, what beginning an item takes; workgroups end anywhere.
 struct Found {
     int64_t start;                          // of the sequence
     int b, first, n, len, cost, groups;     // cost of an item; groups of rows
@@ -146,7 +147,7 @@ template <int RQ> struct Work {
     __device__ Seq seq(int i) const { return i == 0 ? own : seq_of(a, tid * per + i); }
     __device__ int cost(const Seq& s) const {
         const int tiles = seq_tiles(a, s);
-        return !a.even ? (tiles ? tiles + BEGIN : 0) : tiles <= share ? min(tiles, 1) : (tiles + share - 1) / share;
+        return !a.even ? (tiles ? tiles + begin_cost(RQ) : 0) : tiles <= share ? min(tiles, 1) : (tiles + share - 1) / share;
     }
     __device__ int groups(const Seq& s) const { return (min(s.n, a.max_q) * a.G + RQ - 1) / RQ; }
     // the sum of f over all items, and that over the sequences before the thread's
@@ -259,8 +260,8 @@ template <int RQ, typename F> __device__ inline void each_segment(const AttnArgs
                 s.t0 = (int)((int64_t)tiles * from / s.f.cost);
                 s.t1 = (int)((int64_t)tiles * to / s.f.cost);
             } else {
-                s.t0 = max(from - BEGIN, 0);
-                s.t1 = max(to - BEGIN, 0);
+                s.t0 = max(from - begin_cost(RQ), 0);
+                s.t1 = max(to - begin_cost(RQ), 0);
             }
             // the tiles that any of the rows can see
             const int seen = a.mask ? s.len : min(s.len, s.ctx + (s.row0 + s.nrows - 1) / a.G + 1);
@@ -854,7 +855,7 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     // 79.5 with WAYS. Few have many: one token of 131072 54.9, and 72.6 with WAYS.
     p.each = !p.even;
     const int64_t least = step_min((int)p.RQ);
-    const int64_t parts = items * (p.cut ? ceil_div(std::min(most + BEGIN, card * least), least) : 1);
+    const int64_t parts = items * (p.cut ? ceil_div(std::min(most + begin_cost((int)p.RQ), card * least), least) : 1);
     p.blocks = std::min(p.cut ? card : 2 * card, round_up(parts, 8));
     return p;
 }
