@@ -24,8 +24,8 @@
 //     one of 131072 tokens, bf16, values in q4_0, 43 us for 218 MB (5.0 TB/s); the second launch takes 5 us.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
-//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 72 us (0.37 PFLOP/s), a chain
-//     of 512 behind 3584, f32 with twice the products, 107 us (0.3 PFLOP/s).
+//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 71 us (0.38 PFLOP/s), a chain
+//     of 512 behind 3584, f32 with twice the products, 108 us (0.3 PFLOP/s).
 #include <algorithm>
 
 #include "cache.h"
@@ -953,8 +953,8 @@ hipError_t launch_cache_attn(mmq_otype o, const void* q, int64_t ldq, mmq_wtype 
         if (p.NQ == 1) hipLaunchKernelGGL((cache_attn_kernel<F, K, V, NB, 1>), grid, threads, 0, stream, a);
         const int64_t rows = std::min<int64_t>(p.RQ, s.max_q * a.G);
         if (p.cut && p.each)
-            hipLaunchKernelGGL((cache_join_kernel<F, NB, true>), dim3((unsigned)ceil_div(rows, ways_of(NB)), (unsigned)p.blocks), threads,
-                               0, stream, a, (int)p.RQ);
+            hipLaunchKernelGGL((cache_join_kernel<F, NB, true>), dim3((unsigned)ceil_div(rows, ways_of(NB)), (unsigned)p.blocks),
+                               threads, 0, stream, a, (int)p.RQ);
         else if (p.cut)
             hipLaunchKernelGGL((cache_join_kernel<F, NB, false>), dim3((unsigned)rows, (unsigned)p.blocks), threads, 0, stream, a,
                                (int)p.RQ);
