@@ -8,12 +8,16 @@
 //      scales in f32. q is held as f16 terms of q 2^e (e: the row's exponent, its largest value in
 //      [2^13, 2^14)): two for f32 rows, which leave 2^-22 of a value, one for bf16 rows, whose 8 bits
 //      it holds exactly down to 2^-30 of the row's largest.
-//   2. p = 2^(score - m), m the running maximum, sums of p in f32; 2^10 of headroom keeps small p away
+//   2. p = 2^(score - m), m the running maximum, sums of p in f32; 2^8 of headroom keeps small p away
 //      from f16's subnormals.
 //   3. O^T += V^T P^T. The scale of a token's block of values lies along the sum, so it goes into P:
 //      p d_v 2^k, for f32 rows in two f16 terms (the rounding of the first is in the second), for bf16
 //      rows in one, two roundings of 2^-11 of a term, where the result's own is 2^-8. k, the wave's
-//      running exponent, keeps the largest d_v 2^k in [1, 2).
+//      running exponent, keeps the largest d_v 2^k in [4, 8) and is never negative, so that d_v 2^k is exact
+//      in f16. Tiles with scales of 8 and more (values from 1016, or 64 in q4_0) come last, in a loop of their
+//      own, which makes p d_v 2^k in f32 and holds it in range by m: a token's score counts as higher by as
+//      much as its largest scale times 2^k is above 8. So a large value takes bits of a row's result only by
+//      its own weight there. (Inside the main loop, a branch around the products took 40 registers.)
 // A lane holds the tokens of S^T's rows that it needs as P^T's k: the cache's order of tokens makes
 // them the same (cache.h).
 // The waves' sums are joined in LDS. Work that several workgroups share leaves its parts in the
@@ -43,8 +47,11 @@ constexpr int begin_cost(int rq) { return rq == 16 ? 10 : 5; }
 // Tiles of a table's row up to which items are not cut, so that there is no second launch: 32 tokens that see 700
 // each (22 tiles) 21.4 us with 16 and 15.5 with 24; one that sees 777 (25) 11.0 with 24 and 12.0 with 32.
 constexpr int64_t WHOLE = 24;
-constexpr float P_BITS = 10.f;              // p is held times 2^10,
-constexpr float P_SLACK = 4.f;              // and the maximum may rise by 4 before it is taken anew
+// p is held times 2^P_BITS, the maximum may rise by P_SLACK before it is taken anew, and scales times 2^k are below
+// 2^D_BITS in the main loop: p d 2^k stays below 2^15. With 10, 2 and 3, 2048 tokens behind 2048 236 us and with 8, 4 and
+// 3 233.5; 8 trees 75.7 and 74.8. With 10, 3 and 2 ordinary values in q4_0 are large ones: 131072 tokens 61 us, and 49.5 so.
+constexpr float P_BITS = 8.f, P_SLACK = 4.f;
+constexpr int D_BITS = 3;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
@@ -440,13 +447,8 @@ __device__ inline void load_rows(const AttnArgs& a, int first, int h, int row, i
 // Three waves of 4 blocks and fewer spill as well: 64 sequences of one 86 us, with two 70.
 constexpr int waves_of(int NB) { return NB <= 6 ? 2 : 1; }
 
-// The weights p of a lane's 8 scores, as f16 terms, from a maximum that is taken anew where a score is
-// far above it; and their sum.
-template <bool F32, typename R> __device__ inline void weights(const float (&sc)[8], R& r, uint32_t (&ph)[4], uint32_t (&pl)[4]) {
-    float top = sc[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i]);
-    top *= r.c;
+// The maximum taken anew where a score is far above it. top: the lane's largest, times r.c.
+template <typename R> __device__ inline void raise_max(float top, R& r) {
     if (__any(top > r.m + P_SLACK)) {
         const float m1 = fmaxf(r.m, xor_max(top));
         const float base = m1 == -__builtin_inff() ? 0.f : m1;
@@ -457,20 +459,22 @@ template <bool F32, typename R> __device__ inline void weights(const float (&sc)
 #pragma unroll
         for (auto& o : r.o) o *= fall;
     }
-    float p[8];
+}
+// A lane's 8 weights, and their sum
+template <typename R> __device__ inline void weights(const float (&sc)[8], R& r, float (&p)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], r.c, r.off));
         r.l += p[i];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const h2 hi = {(_Float16)p[2 * i], (_Float16)p[2 * i + 1]};
-        ph[i] = as_u32(hi);
-        if constexpr (F32) {
-            const h2 lo = {(_Float16)(p[2 * i] - (float)hi[0]), (_Float16)(p[2 * i + 1] - (float)hi[1])};
-            pl[i] = as_u32(lo);
-        }
+}
+// Two numbers as f16 terms
+template <bool F32> __device__ inline void in_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    const h2 h = {(_Float16)x0, (_Float16)x1};
+    hi = as_u32(h);
+    if constexpr (F32) {
+        const h2 l = {(_Float16)(x0 - (float)h[0]), (_Float16)(x1 - (float)h[1])};
+        lo = as_u32(l);
     }
 }
 
@@ -483,11 +487,12 @@ template <bool SHARED> __device__ inline void products_first(bool yes) {
     }
 }
 
-// What a wave knows of a tile's value scales: their exponent, and the f16 bits from which it must fall.
+// What a wave knows of its tiles' value scales: their exponent, and the largest f16 bits that it suits.
 struct Exponent {
     int k;
     uint32_t limit;
 };
+constexpr uint32_t WIDE = (15 + D_BITS) << 10;              // 2^D_BITS as f16
 
 // F32: rows of f32 (two terms), or bf16 (one). NQ: groups of 16 rows of a workgroup.
 template <bool F32, bool K8, bool V8, int NB, int NQ>
@@ -527,34 +532,13 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
         };
         Keys<K8, NB> kw;
         Values<V8, NB> vw;
-        const auto load_k = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
+        const auto load_k = [&](uint64_t rec, bool there, int lane) __attribute__((always_inline)) {
             kw.load(Record(a.kc, rec, cache_record(K8, D), there), lane);
         };
-        const auto load_v = [&](uint64_t rec, bool there) __attribute__((always_inline)) {
+        const auto load_v = [&](uint64_t rec, bool there, int lane) __attribute__((always_inline)) {
             vw.load(Record(a.vc, rec, cache_record(V8, D), there), lane);
         };
-        // A tile's keys are loaded while the products of values of the one before run, its values while the
-        // next scores do: the registers are free by then. No such page: its tokens are not seen, and the
-        // first page stands in for it.
-        int t = t0 + wave;
-        bool ok = false;
-        uint64_t rec = 0;
-        if (t < t1) {
-            const uint32_t page = (uint32_t)table[t >> shift];
-            ok = page < (uint32_t)a.c.pages;
-            rec = record(t, ok ? page : 0);
-            load_k(rec, true);
-            load_v(rec, true);
-        }
-#pragma unroll 1
-        for (; t < t1; t += WAVES) {
-            const int limit = ok ? len : 0;
-            const bool more = t + WAVES < t1;
-            const uint32_t page = (uint32_t)table[(more ? t + WAVES : t) >> shift];
-
-            // 1. the products of scores
-            products_first<SHARED>(true);
-            float sc[NQ][8];
+        const auto scores = [&](int lane, float (&sc)[NQ][8]) __attribute__((always_inline)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -582,18 +566,10 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                     }
                 }
             }
-
-            // (the scores are finished before the loads, whose registers the products' operands leave)
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sc[n][i]));
-            ok = page < (uint32_t)a.c.pages;
-            rec = record(t + WAVES, ok ? page : 0);           // (not loaded from where there is none)
-            load_k(rec, more);
-
-            // tokens that a row does not see; scales of slots past the sequence are not read as numbers
-            if (CACHE_TILE * (t + 1) > min(ctx, limit)) {
+        };
+        // tokens that a row does not see; scales of slots past the sequence are not read as numbers
+        const auto hide = [&](int t, int limit, int g, float (&sc)[NQ][8]) __attribute__((always_inline)) {
+            if (__builtin_expect(CACHE_TILE * (t + 1) > min(ctx, limit), 0)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int pos = CACHE_TILE * t + 16 * (i >> 2) + 4 * g + (i & 3);
@@ -606,6 +582,51 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                     }
                 }
             }
+        };
+        const auto product = [&](int b, const h8 (&pt)[NQ][TERMS]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const h8 vv = vw.get(b, v);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < TERMS; ++i) r[n].o[2 * b + v] = mfma(vv, pt[n][i], r[n].o[2 * b + v]);
+            }
+        };
+        // A tile's keys are loaded while the products of values of the one before run, its values while the
+        // next scores do: the registers are free by then. No such page: its tokens are not seen, and the
+        // first page stands in for it.
+        int t = t0 + wave, left_out = t1;                       // left_out: the first tile with scales from 2^D_BITS on
+        bool ok = false;
+        uint64_t rec = 0;
+        if (t < t1) {
+            const uint32_t page = (uint32_t)table[t >> shift];
+            ok = page < (uint32_t)a.c.pages;
+            rec = record(t, ok ? page : 0);
+            load_k(rec, true, lane);
+            load_v(rec, true, lane);
+        }
+#pragma unroll 1
+        for (; t < t1; t += WAVES) {
+            const int limit = ok ? len : 0;
+            const bool more = t + WAVES < t1;
+            const uint32_t page = (uint32_t)table[(more ? t + WAVES : t) >> shift];
+
+            // 1. the products of scores
+            products_first<SHARED>(true);
+            float sc[NQ][8];
+            scores(lane, sc);
+
+            // (the scores are finished before the loads, whose registers the products' operands leave)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sc[n][i]));
+            ok = page < (uint32_t)a.c.pages;
+            rec = record(t + WAVES, ok ? page : 0);           // (not loaded from where there is none)
+            load_k(rec, more, lane);
+
+            hide(t, limit, g, sc);
 
             // The exponent k of the value scales. One that is not finite counts as 0, after the sums that it
             // goes into, those of the rows that see its token, are made NaN.
@@ -616,8 +637,8 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                 for (int i = 0; i < 4; ++i)
                     dtop = __builtin_elementwise_max(dtop, as_u16(V8 ? vw.d[b][i] : vw.d[b][i] & 0x7FFF7FFFu));
             uint32_t dmax = max(dtop[0], dtop[1]);              // (scales of q8_0 are not negative, or look large)
-            if (__any(dmax > ex.limit)) {
-                if (__any(dmax >= 0x7C00)) {
+            if (__builtin_expect(__any(dmax > ex.limit), 0)) {
+                if (__builtin_expect(__any(dmax >= 0x7C00), 0)) {
                     dmax = 0;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -642,17 +663,29 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                 dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 16));
                 dmax = max(dmax, (uint32_t)__shfl_xor((int)dmax, 32));
                 dmax = __builtin_amdgcn_readfirstlane(dmax);
-                if (dmax > ex.limit) {
-                    // the largest scale times 2^k in [1, 2), as far as 2^k is an f16
-                    const int k = min(15, 1 - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)dmax)));
+                // A tile with such scales is left for later: here none of it is seen. (Selects: a third path to the products,
+                // with zeros of its own, cost the main loop up to 27 registers, and bf16 rows in twos a quarter of their time.)
+                const bool wide = dmax >= WIDE;
+                left_out = wide ? min(left_out, t) : left_out;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vw.d[b][i] = wide ? 0 : vw.d[b][i];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sc[n][i] = wide ? -__builtin_inff() : sc[n][i];
+                if (!wide && dmax > ex.limit) {
+                    // the largest scale times 2^k in [4, 8), as far as 2^k is an f16
+                    const int k = min(15, D_BITS - __builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)dmax)));
                     const float fall = __builtin_amdgcn_ldexpf(1.f, k - ex.k);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
 #pragma unroll
                         for (int i = 0; i < 2 * NB; ++i) r[n].o[i] *= fall;
                     ex.k = k;
-                    // the largest f16 below 2^(1 - k)
-                    ex.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, -k)) | 0x3FF;
+                    // the largest f16 below 2^(D_BITS - k)
+                    ex.limit = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(1.f, D_BITS - 1 - k)) | 0x3FF;
                 }
             }
 
@@ -662,7 +695,13 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
             uint32_t ph[NQ][4], pl[NQ][4];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                weights<F32>(sc[n], r[n], ph[n], pl[n]);
+                float top = sc[n][0], p[8];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[n][i]);
+                raise_max(top * r[n].c, r[n]);
+                weights(sc[n], r[n], p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in_terms<F32>(p[2 * i], p[2 * i + 1], ph[n][i], pl[n][i]);
             }
 
             const _Float16 two_k = (_Float16)__builtin_amdgcn_ldexpf(1.f, ex.k);
@@ -689,17 +728,64 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
                     pt[n][0] = __builtin_bit_cast(h8, u32x4{hi[0], hi[1], hi[2], hi[3]});
                     if constexpr (F32) pt[n][1] = __builtin_bit_cast(h8, u32x4{lo[0], lo[1], lo[2], lo[3]});
                 }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const h8 vv = vw.get(b, v);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int i = 0; i < TERMS; ++i) r[n].o[2 * b + v] = mfma(vv, pt[n][i], r[n].o[2 * b + v]);
-                }
+                product(b, pt);
             }
             products_first<SHARED>(false);
-            load_v(rec, more);
+            load_v(rec, more, lane);
+        }
+
+        // The tiles left out, found by their scales again. Scales that are not finite have made their sums NaN above.
+#pragma unroll 1
+        for (t = left_out; __builtin_expect(t < t1, 0); t += WAVES) {
+            const uint32_t page = (uint32_t)table[t >> shift];
+            if (page >= (uint32_t)a.c.pages) continue;
+            const int lane = thread_here() & 63;
+            load_v(record(t, page), true, lane);
+            float sc[NQ][8] = {}, up[8];
+            hide(t, len, lane >> 4, sc);                                   // (for the scales)
+            uint32_t dmax = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t token = 0;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t d = (vw.d[b][i >> 1] >> (16 * (i & 1))) & 0x7FFF;
+                    if (d < 0x7C00) token = max(token, d);
+                    else vw.d[b][i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+                dmax = max(dmax, token);
+                up[i] = (float)max(__builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, (uint16_t)token)) + ex.k - D_BITS, 0);
+            }
+            if (!__any(dmax >= WIDE)) continue;
+            load_k(record(t, page), true, lane);
+            scores(lane, sc);
+            hide(t, len, lane >> 4, sc);
+            float p[NQ][8];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float top = fmaf(sc[n][0], r[n].c, up[0]);
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, fmaf(sc[n][i], r[n].c, up[i]));
+                raise_max(top, r[n]);
+                weights(sc[n], r[n], p[n]);
+            }
+            const float two_k = __builtin_amdgcn_ldexpf(1.f, ex.k);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                h8 pt[NQ][TERMS];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const h2 d = as_h2(vw.d[b][i]);
+                        in_terms<F32>(p[n][2 * i] * ((float)d[0] * two_k), p[n][2 * i + 1] * ((float)d[1] * two_k), hi[i], lo[i]);
+                    }
+                    pt[n][0] = __builtin_bit_cast(h8, u32x4{hi[0], hi[1], hi[2], hi[3]});
+                    if constexpr (F32) pt[n][1] = __builtin_bit_cast(h8, u32x4{lo[0], lo[1], lo[2], lo[3]});
+                }
+                product(b, pt);
+            }
         }
 
         // the waves' sums

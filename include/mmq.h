@@ -474,8 +474,10 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  *  workspace (device) >= mmq_cache_attn_workspace_bytes(...) bytes (NULL if that is 0); needs no
  *          initialisation. Two calls that overlap in time must not share one.
  * Numbers: whole numbers of the cache enter the products exactly; q in f32 rows, and softmax
- * weights times value scales, as two f16 terms (22 bits of the largest of a row; 35 bits below the
- * largest weight times the largest scale), in bf16 rows as one (q exactly, weights to 11 bits).
+ * weights times value scales, as two f16 terms (22 bits of the largest of a row), in bf16 rows as one
+ * (q exactly, weights to 11 bits). Weights times scales have no bits below 2^-33 of the row's
+ * largest product of a weight and its token's largest scale, where a scale below 8 counts as 8. A token
+ * that a row does not see costs it no bits.
  * Sums, maxima and scores are f32; the result is rounded once. It repeats bit for bit. Slots past
  * a sequence's length may hold anything; a scale that is not finite in a token that a row does not
  * see changes nothing for that row.

@@ -697,3 +697,134 @@ def test_attention_refusals_of_the_binding(env):
     wide = Case(env, lens=(1500,), news=(1,), D=64, seed=22).device()
     with pytest.raises(mmq.MMQError):
         wide.run(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def _put_values(c, slots, x):
+    cachemodel.write(c.host["v"], x.astype(np.float32), slots, c.vt, "v")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,peak", [("q8_0", 2e3), ("q8_0", 1e5), ("q8_0", 1e6), ("q8_0", 8e6), ("q4_0", 200.0), ("q4_0", 5e5)])
+@pytest.mark.parametrize("where", ["block", "before", "tree", "chain"])
+def test_a_large_value_scale_leaves_the_others_their_bits(env, where, kind, peak, dt):
+    """A row that sees one token (of weight 1; what else it sees is 2^-200 of it), with a block of values of `peak`
+    in that token, in a token before it that the same wave has had, or in one of the same tile that the row
+    does not see. Relative: as in test_a_row_that_sees_one_token_gets_its_values. Absolute: the products' f16 terms are
+    held to 2^-25 where the row's largest weight, times its token's scale over 4 where that is above one, is
+    at least 2^8, so 2^-33 max(1, D / 4) of a whole number q, with D the largest scale of the token it sees."""
+    torch, mmq = env
+    if where == "before":                       # tiles 0 and 4 are one wave's
+        c = Case(env, dt=dt, vt=kind, lens=(129,), news=(1,), D=64, seed=31)
+        k = np.full((129, 2, 64), -4.0, np.float32)
+        k[128] = 4.0
+        slots = c.table[0, np.arange(129) // 32] * 32 + np.arange(129) % 32
+        cachemodel.write(c.host["k"], k, slots, "q8_0", "k")
+        c.qh[:] = 4.0                           # scores -128 and 128
+        rows, large = [(0, 128)], 5
+    elif where == "chain":                      # row 0 sees token 0 alone
+        c = Case(env, dt=dt, vt=kind, lens=(20,), news=(20,), D=64, seed=32)
+        rows, large = [(0, 0)], 7
+    else:
+        c = Case(env, dt=dt, vt=kind, lens=(20,), news=(20,), tree=True, D=64, seed=33)
+        c.mask[:] = [1 << i for i in range(20)]
+        large = 7
+        rows = [(i, i) for i in range(20) if (i == large) == (where == "block")]
+    n = int(c.lens[0])
+    slots = c.table[0, np.arange(n) // 32] * 32 + np.arange(n) % 32
+    x = c.r.uniform(-3, 3, (n, 2, 64))
+    x[large, :, :32] *= peak / 3
+    x[large, :, 0] = peak
+    _put_values(c, slots, x)
+    got = c.device().run().float().cpu().numpy().astype(np.float64)
+    values = cachemodel.load(c.host["v"], kind, "v")
+    q, top = (127, 254.0) if kind == "q8_0" else (8, 16.0)
+    rel = 7 * 2.0 ** -23 if dt == "f32" else 2.0 ** -10 + 3 * 2.0 ** -23 + 2.0 ** -8
+    for row, pos in rows:
+        want = values[slots[pos]].repeat(4, 0)
+        D = np.abs(want).max() / (top / 2)
+        off = np.abs(got[row] - want) - rel * 1.01 * np.abs(want)
+        assert np.all(off <= q * 2.0 ** -33 * max(1.0, D / 4) * 1.01), (row, off.max())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("std", [1e-3, 1.0, 1e3, 3e4])
+def test_attention_within_the_absolute_bound_of_its_terms(env, std, kind, dt):
+    """Values of one size, large scales from 1e3 on (1e2 in q4_0); the bound of Case.want() with its absolute term,
+    N 2^-28 max|v|, as the terms have it: p's are held to 2^-25 where the largest weight is 2^8, and p d 2^k's to
+    2^-25 where the largest weight times 4 (or times 2^15 of a scale, k being at most 15) is 2^8, so to
+    N (2^-33 + 2^-35) max|v| + N 127 2^-48. There are two roundings of a term, the second 2^-21 in f32 rows: of the
+    two numbers of 2^-11 that are added."""
+    torch, mmq = env
+    c = Case(env, dt=dt, vt=kind, lens=(200, 450, 31), news=(2, 5, 1), D=64, seed=35)
+    for b, n in enumerate(c.lens):
+        slots = c.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32
+        x = c.r.standard_normal((n, 2, 64)) * std
+        x[::7] *= 3
+        _put_values(c, slots, x)
+    got = c.device().run().float().cpu().numpy().astype(np.float64)
+    want, bound = c.want()
+    k, v = (cachemodel.load(c.host[s], t, s) for s, t in (("k", c.kt), ("v", c.vt)))
+    with np.errstate(invalid="ignore"):
+        mag = cachemodel.attn(c.qh.astype(np.float64), k, v, c.table, c.lens, c.starts, c.page, c.pages, c.max_q, c.mask, c.scale)[1]
+    used = np.concatenate([c.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32 for b, n in enumerate(c.lens)])
+    vmax, N = np.abs(v[used]).max(), int(c.lens.max())
+    bound += N * ((2.0 ** -33 + 2.0 ** -35 - 2.0 ** -28) * vmax + 127 * 2.0 ** -48)
+    bound += mag * (2.0 ** -21 if dt == "f32" else 2.0 ** -11) * 1.01
+    off = np.abs(got - want)
+    print(f"[case]   error at most {(off / bound).max():.4f} of the bound", flush=True)
+    assert np.all(off <= bound)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,news,D,kind", [(300, 1, 64, "q8_0"), (640, 5, 128, "q4_0"), (1900, 1, 64, "q8_0"), (900, 12, 128, "q8_0"),
+                                           (500, 3, 192, "q4_0"), (700, 2, 256, "q8_0")])
+def test_equal_scores_over_scales_of_all_sizes(env, n, news, D, kind, dt):
+    """q = 0, and blocks of values from 1e-3 to 1e6 (1e5 in q4_0) beside and after each other, the last one
+    ordinary. Weights are 1 / N, so what the terms do not hold, N (2^-33 + 2^-35) max|v| of the largest weight,
+    is 1.25 2^-33 max|v| here."""
+    torch, mmq = env
+    c = Case(env, dt=dt, vt=kind, lens=(n,), news=(news,), D=D, page=64, seed=36)
+    c.qh[:] = 0
+    slots = c.table[0, np.arange(n) // 64] * 64 + np.arange(n) % 64
+    size = 10.0 ** c.r.uniform(-3, 6 if kind == "q8_0" else 5, (n, 2, D // 32, 1))
+    size[c.r.random(n) < 0.7] = 1.0
+    size[:, :, -1] = 1.0                            # a block of ordinary values in every token
+    _put_values(c, slots, (c.r.standard_normal((n, 2, D // 32, 32)) * size).reshape(n, 2, D))
+    got = c.device().run().float().cpu().numpy().astype(np.float64)
+    v = cachemodel.load(c.host["v"], kind, "v")[slots]
+    for i in range(news):
+        seen = v[:n - news + i + 1]
+        want, mag = seen.mean(0).repeat(4, 0), np.abs(seen).mean(0).repeat(4, 0)
+        # sums over n + 32 additions, weights that are powers of two exactly; terms of 2^-22 and 2^-21, or 2^-11 twice
+        bound = mag * (4 * U24 * (n + 32) + (3 * 2.0 ** -22 if dt == "f32" else 2.0 ** -10)) * 1.01 + 1.25 * 2.0 ** -33 * np.abs(seen).max()
+        bound += np.abs(want) * (U24 if dt == "f32" else 2.0 ** -8)
+        off = np.abs(got[i] - want)
+        print(f"[case]   error at most {(off / bound).max():.4f} of the bound", flush=True)
+        assert np.all(off <= bound)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_large_and_infinite_scales_in_one_tile(env, dt):
+    """Each row sees its own token, one of them with values up to 1e6, one with infinite scales (head 0), which row 5
+    sees besides its own: rows of the infinite one are not finite, all others as if they were alone."""
+    torch, mmq = env
+    c = Case(env, dt=dt, lens=(20,), news=(20,), tree=True, D=64, seed=37)
+    c.mask[:] = [1 << i for i in range(20)]
+    c.mask[5] |= np.uint64(1 << 3)
+    slots = c.table[0, np.arange(20) // 32] * 32 + np.arange(20) % 32
+    x = c.r.uniform(-3, 3, (20, 2, 64))
+    x[2, :, 7] = 1e6
+    _put_values(c, slots, x)
+    values = cachemodel.load(c.host["v"], "q8_0", "v")[slots]
+    t = int(slots[3]) % 32
+    for b in range(2):
+        at = 64 * 32 + 2 * (((t % 16) // 4 * 2 + b) * 8 + 4 * (t // 16) + t % 4)
+        c.host["v"][slots[3] // 32, 0, 0, at:at + 2] = np.frombuffer(np.uint16(0x7C00).tobytes(), np.uint8)
+    got = c.device().run().float().cpu().numpy().astype(np.float64)
+    assert not np.isfinite(got[[3, 5], :4]).any() and np.isfinite(got[[3, 5], 4:]).all()
+    rel = 7 * 2.0 ** -23 if dt == "f32" else 2.0 ** -10 + 3 * 2.0 ** -23 + 2.0 ** -8
+    for row in (i for i in range(20) if i not in (3, 5)):
+        want = values[row].repeat(4, 0)
+        D = np.abs(want).max() / 127
+        assert np.all(np.abs(got[row] - want) <= rel * 1.01 * np.abs(want) + 127 * 2.0 ** -33 * max(1.0, D / 4) * 1.01), row
