@@ -447,10 +447,11 @@ __device__ inline void load_rows(const AttnArgs& a, int first, int h, int row, i
 // Three waves of 4 blocks and fewer spill as well: 64 sequences of one 86 us, with two 70.
 constexpr int waves_of(int NB) { return NB <= 6 ? 2 : 1; }
 
-// The maximum taken anew where a score is far above it. top: the lane's largest, times r.c.
+// A row's maximum taken anew where a score is far above it, and there alone: its bits do not depend on the other rows
+// of the products. top: the lane's largest, times r.c.
 template <typename R> __device__ inline void raise_max(float top, R& r) {
     if (__any(top > r.m + P_SLACK)) {
-        const float m1 = fmaxf(r.m, xor_max(top));
+        const float above = xor_max(top), m1 = above > r.m + P_SLACK ? above : r.m;
         const float base = m1 == -__builtin_inff() ? 0.f : m1;
         const float fall = __builtin_amdgcn_exp2f(r.m - base);
         r.m = m1;

@@ -478,9 +478,9 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  * (q exactly, weights to 11 bits). Weights times scales have no bits below 2^-33 of the row's
  * largest product of a weight and its token's largest scale, where a scale below 8 counts as 8. A token
  * that a row does not see costs it no bits.
- * Sums, maxima and scores are f32; the result is rounded once. It repeats bit for bit. Slots past
- * a sequence's length may hold anything; a scale that is not finite in a token that a row does not
- * see changes nothing for that row.
+ * Sums, maxima and scores are f32; the result is rounded once. It repeats bit for bit, whatever the
+ * queries of other rows are. Slots past a sequence's length may hold anything; a scale that is not
+ * finite in a token that a row does not see changes nothing for that row.
  * Limits (MMQ_EINVAL): rows <= 2^24, 1 <= B <= 4096, 1 <= max_q <= rows, width <= 2^22, and
  * ceil(max_q * G / 16) * heads < 2^20. */
 mmq_status mmq_cache_attn(mmq_otype o, const void* q, int64_t ldq, int64_t rows, int64_t heads_q, mmq_wtype tk,

@@ -828,3 +828,26 @@ def test_large_and_infinite_scales_in_one_tile(env, dt):
         want = values[row].repeat(4, 0)
         D = np.abs(want).max() / 127
         assert np.all(np.abs(got[row] - want) <= rel * 1.01 * np.abs(want) + 127 * 2.0 ** -33 * max(1.0, D / 4) * 1.01), row
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D,news,n", [(64, 3, 700), (128, 8, 650), (256, 3, 700)])
+def test_a_row_keeps_its_bits_whatever_its_neighbours_are(env, D, news, n, dt):
+    """Several tiles a wave, so that running maxima are taken anew: a neighbour in the same products whose scores
+    rise along the sequence, are not numbers, or are all alike, and the other rows bit for bit the same."""
+    torch, mmq = env
+    c = Case(env, dt=dt, lens=(n,), news=(news,), D=D, page=64, seed=34)
+    slots = c.table[0, np.arange(n) // 64] * 64 + np.arange(n) % 64
+    k = c.r.standard_normal((n, 2, D)).astype(np.float32)
+    k[:, :, 7] = np.linspace(0, 4, n)[:, None]
+    cachemodel.write(c.host["k"], k, slots, "q8_0", "k")
+    c.device().q[:, :, 7] = 0.0
+    runs = []
+    for neighbour in (0.0, 200.0, float("nan")):
+        c.q[1, 2] = 0.0
+        c.q[1, 2, 7] = neighbour
+        runs.append(c.run())
+    assert torch.isnan(runs[2][1, 2]).all()
+    for got in runs[1:]:
+        got[1, 2] = runs[0][1, 2]
+        assert torch.equal(got, runs[0])
