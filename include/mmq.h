@@ -466,8 +466,9 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  *          tokens past width * page, are not seen. Pages may be shared by sequences.
  *  lens    (device) int32 [B]; a negative length is 0
  *  starts  (device) int32 [B + 1], rising, in [0, rows]; a sequence whose starts are not has no
- *          rows. Rows outside every sequence are left untouched; a row of two sequences holds the
- *          result of one of them.
+ *          rows. Rows outside every sequence are left untouched. Where starts fall, a row can belong to two
+ *          sequences: each of its values is then one of the two results, not the same one for all
+ *          values nor in every call.
  *  max_q   the largest n: rows of a sequence past its max_q are left untouched
  *  mask    (device) uint64 [rows] or NULL
  *  scale   finite and > 0 (D^-0.5, as a rule)
@@ -478,9 +479,9 @@ size_t mmq_cache_attn_workspace_bytes(int64_t rows, int64_t heads_q, int64_t pag
  * (q exactly, weights to 11 bits). Weights times scales have no bits below 2^-33 of the row's
  * largest product of a weight and its token's largest scale, where a scale below 8 counts as 8. A token
  * that a row does not see costs it no bits.
- * Sums, maxima and scores are f32; the result is rounded once. It repeats bit for bit, whatever the
- * queries of other rows are. Slots past a sequence's length may hold anything; a scale that is not
- * finite in a token that a row does not see changes nothing for that row.
+ * Sums, maxima and scores are f32; the result is rounded once. Rows of one sequence repeat bit for
+ * bit, whatever the queries of other rows are. Slots past a sequence's length may hold anything; a
+ * scale that is not finite in a token that a row does not see changes nothing for that row.
  * Limits (MMQ_EINVAL): rows <= 2^24, 1 <= B <= 4096, 1 <= max_q <= rows, width <= 2^22, and
  * ceil(max_q * G / 16) * heads < 2^20. */
 mmq_status mmq_cache_attn(mmq_otype o, const void* q, int64_t ldq, int64_t rows, int64_t heads_q, mmq_wtype tk,
