@@ -613,7 +613,7 @@ def _cache_dims(kshape, vshape, ktype, vtype):
         return None
     pages, heads, tiles, rec = kshape
     D = rec // CACHE_BLOCK[ktype]
-    if rec != D * CACHE_BLOCK[ktype] or vshape != (pages, heads, tiles, D * CACHE_BLOCK[vtype]):
+    if heads == 0 or D == 0 or rec != D * CACHE_BLOCK[ktype] or vshape != (pages, heads, tiles, D * CACHE_BLOCK[vtype]):
         return None
     return WTYPE[ktype], WTYPE[vtype], pages, 32 * tiles, heads, D
 

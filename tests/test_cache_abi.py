@@ -186,3 +186,12 @@ def test_binding_strides(mmq):
     for t in (x.transpose(0, 1), x[:, ::2], x[:, :, ::2], x.double(), x[0], x[:, :, :63]):
         with pytest.raises(ValueError):
             mmq._heads_ld("f", "k", t, 12, 64, f32)
+
+
+def test_caches_without_heads_or_values_are_refused(mmq):
+    """A ValueError as for other shapes, before anything is divided by them."""
+    import torch
+    for shape in ((2, 0, 2, 34 * 64), (2, 4, 2, 0), (2, 0, 2, 0)):
+        cache = torch.zeros(shape, dtype=torch.uint8)
+        with pytest.raises(ValueError, match="cache_shape"):
+            mmq._caches("f", cache, cache, "q8_0", "q8_0")
