@@ -746,15 +746,26 @@ def test_a_large_value_scale_leaves_the_others_their_bits(env, where, kind, peak
         assert np.all(off <= q * 2.0 ** -33 * max(1.0, D / 4) * 1.01), (row, off.max())
 
 
+def _as_held(c):
+    """Case.want() with its absolute term, N 2^-28 max|v|, as the products' terms have it: p's are held to 2^-25 where
+    the largest weight is 2^8, and p d 2^k's to 2^-25 where the largest weight times 4 (or times 2^15 of a scale, k
+    being at most 15) is 2^8, so to N (2^-33 + 2^-35) max|v| + N 127 2^-48. There are two roundings of a term, the
+    second 2^-21 in f32 rows: of the two numbers of 2^-11 that are added."""
+    want, bound = c.want()
+    k, v = (cachemodel.load(c.host[s], t, s) for s, t in (("k", c.kt), ("v", c.vt)))
+    with np.errstate(invalid="ignore"):
+        mag = cachemodel.attn(c.qh.astype(np.float64), k, v, c.table, c.lens, c.starts, c.page, c.pages, c.max_q, c.mask, c.scale)[1]
+    used = np.concatenate([c.table[b, np.arange(n) // c.page] * c.page + np.arange(n) % c.page for b, n in enumerate(c.lens)])
+    vmax, N = np.abs(v[used]).max(), int(c.lens.max())
+    bound += N * ((2.0 ** -33 + 2.0 ** -35 - 2.0 ** -28) * vmax + 127 * 2.0 ** -48)
+    return want, bound + mag * (2.0 ** -21 if c.dt == "f32" else 2.0 ** -11) * 1.01
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
 @pytest.mark.parametrize("std", [1e-3, 1.0, 1e3, 3e4])
 def test_attention_within_the_absolute_bound_of_its_terms(env, std, kind, dt):
-    """Values of one size, large scales from 1e3 on (1e2 in q4_0); the bound of Case.want() with its absolute term,
-    N 2^-28 max|v|, as the terms have it: p's are held to 2^-25 where the largest weight is 2^8, and p d 2^k's to
-    2^-25 where the largest weight times 4 (or times 2^15 of a scale, k being at most 15) is 2^8, so to
-    N (2^-33 + 2^-35) max|v| + N 127 2^-48. There are two roundings of a term, the second 2^-21 in f32 rows: of the
-    two numbers of 2^-11 that are added."""
+    """Values of one size, large scales from 1e3 on (1e2 in q4_0)."""
     torch, mmq = env
     c = Case(env, dt=dt, vt=kind, lens=(200, 450, 31), news=(2, 5, 1), D=64, seed=35)
     for b, n in enumerate(c.lens):
@@ -763,14 +774,7 @@ def test_attention_within_the_absolute_bound_of_its_terms(env, std, kind, dt):
         x[::7] *= 3
         _put_values(c, slots, x)
     got = c.device().run().float().cpu().numpy().astype(np.float64)
-    want, bound = c.want()
-    k, v = (cachemodel.load(c.host[s], t, s) for s, t in (("k", c.kt), ("v", c.vt)))
-    with np.errstate(invalid="ignore"):
-        mag = cachemodel.attn(c.qh.astype(np.float64), k, v, c.table, c.lens, c.starts, c.page, c.pages, c.max_q, c.mask, c.scale)[1]
-    used = np.concatenate([c.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32 for b, n in enumerate(c.lens)])
-    vmax, N = np.abs(v[used]).max(), int(c.lens.max())
-    bound += N * ((2.0 ** -33 + 2.0 ** -35 - 2.0 ** -28) * vmax + 127 * 2.0 ** -48)
-    bound += mag * (2.0 ** -21 if dt == "f32" else 2.0 ** -11) * 1.01
+    want, bound = _as_held(c)
     off = np.abs(got - want)
     print(f"[case]   error at most {(off / bound).max():.4f} of the bound", flush=True)
     assert np.all(off <= bound)
@@ -851,3 +855,73 @@ def test_a_row_keeps_its_bits_whatever_its_neighbours_are(env, D, news, n, dt):
     for got in runs[1:]:
         got[1, 2] = runs[0][1, 2]
         assert torch.equal(got, runs[0])
+
+
+# items cut anywhere whose join has several rows a workgroup, for heads whose rows do not fill one (192) and for those
+# of one wave a SIMD (256, more than 32 items)
+CUT_WIDE = [
+    dict(lens=_lens(12, 64, 1400, 6), news=_lens(12, 1, 21, 7), D=192, heads=8, G=2),
+    dict(lens=_lens(12, 64, 1400, 6), news=_lens(12, 1, 21, 7), D=192, heads=8, G=2, dt="bf16", kt="q4_0", page=128),
+    dict(lens=_lens(9, 64, 1400, 8), news=_lens(9, 1, 30, 9), D=192, heads=6, G=3, vt="q4_0", tree=True),
+    dict(lens=(1100, 1000), news=(2, 20), D=256, heads=8, G=4),
+    dict(lens=_lens(12, 64, 1400, 10), news=(1,) * 12, D=256, heads=4, G=3, vt="q4_0"),
+]
+
+
+@pytest.mark.parametrize("case", CUT_WIDE, ids=lambda c: f"{len(c['lens'])}of{max(c['lens'])}-D{c['D']}-heads{c.get('heads', 2)}-{c.get('dt', 'f32')}")
+def test_attention_cut_anywhere_in_wide_heads(env, case):
+    test_attention(env, case)
+
+
+@pytest.mark.parametrize("case", [
+    dict(lens=(20011, 9000), news=(1, 3), D=64, heads=1, G=2, page=256),
+    dict(lens=(33000,), news=(2,), D=128, heads=1, G=1, page=64, dt="bf16", vt="q4_0"),
+    dict(lens=_lens(36, 4000, 9000, 11), news=(1,) * 36, D=64, heads=2, G=1, kt="q4_0"),
+], ids=lambda c: f"{len(c['lens'])}of{max(c['lens'])}")
+def test_attention_over_long_sequences(env, case):
+    c = Case(env, **case).device()
+    want, bound = _as_held(c)
+    off = np.abs(c.run().float().cpu().numpy().astype(np.float64) - want)
+    print(f"[case]   error at most {(off / bound).max():.4f} of the bound", flush=True)
+    assert np.all(off <= bound)
+
+
+@pytest.mark.parametrize("n,news,kind", [(33001, 1, "q8_0"), (131071, 1, "q4_0"), (16385, 5, "q8_0")])
+def test_equal_scores_give_the_mean_of_long_sequences(env, n, news, kind):
+    """As test_equal_scores_give_the_mean: whole numbers below 2^24 in all, so every token counts, or the sum is off."""
+    torch, mmq = env
+    c = Case(env, vt=kind, lens=(n,), news=(news,), D=64, page=128, seed=38)
+    top = 127 if kind == "q8_0" else 7
+    x = c.r.integers(-top, top + 1, (n, 2, 64)).astype(np.float32)
+    x[:, :, ::32] = 127.0 if kind == "q8_0" else -8.0          # every block's scale is 1
+    slots = c.table[0, np.arange(n) // 128] * 128 + np.arange(n) % 128
+    cachemodel.write(c.host["v"], x, slots, kind, "v")
+    c.device().q.zero_()
+    got = c.run().cpu().numpy().astype(np.float64)
+    for i in range(news):
+        seen = n - news + i + 1
+        want = x[:seen].astype(np.float64).sum(0).repeat(4, 0) / seen
+        assert np.all(np.abs(got[i] - want) <= np.abs(want) * 2 * U24 * 1.01)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [9, 1700])
+def test_rows_of_odd_strides(env, dt, rows):
+    """Queries, keys and values whose rows lie an odd number of elements apart: the bits of contiguous ones."""
+    torch, mmq = env
+    heads, D, page, dtype = 8, 128, 64, _dtype(torch, dt)
+    x = torch.randn(3, rows, heads * D, device="cuda").to(dtype)
+    q, k, v = (torch.zeros(rows * (heads * D + s) + 8, dtype=dtype, device="cuda")[:rows * (heads * D + s)].view(rows, -1)[:, :heads * D]
+               for s in (1, 3, 5))
+    for to, of in zip((q, k, v), x):
+        to.copy_(of)
+    shape = mmq.cache_shape("q8_0", rows // page + 2, page, heads, D)
+    slots = torch.arange(5, 5 + rows, dtype=torch.int32, device="cuda")
+    caches = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    mmq.cache_write(k, v, slots, caches[0], caches[1])
+    mmq.cache_write(x[1], x[2], slots, caches[2], caches[3])
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    table = torch.arange(rows // page + 2, dtype=torch.int32, device="cuda")[None]
+    lens, starts = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([5 + rows], [0, 9]))
+    got, want = (mmq.cache_attn(t[:9], caches[0], caches[1], table, lens, starts, 9) for t in (q, x[0]))
+    assert q.stride(0) % 2 == 1 and torch.equal(got, want)
