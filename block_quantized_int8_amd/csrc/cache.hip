@@ -12,8 +12,10 @@
 // Many rows go by windows of 32 or 64 through LDS images of the two or three tiles that consecutive
 // slots can touch, so that memory sees whole 16-byte pieces there; rows of other tiles go one by one.
 //
-// Memory bounds many rows: 32768 of 8 heads of 128 values are read from q8_0 as bf16 in 35.6 us (5.8 TB/s of both
-// sides); 2048 of them written from f32 in 8.5 us (2.5 TB/s, and a launch). Few rows are a launch: one 2.9 us.
+// Memory bounds many rows: 32768 of 8 heads of 128 values are read from q8_0 as bf16 in 35 us (5.9 TB/s of both
+// sides), written from f32 in 70 us (4.9 TB/s); 8192 of them written in 19.5 us (4.4), 2048 in 8.4 us (2.5 TB/s, and a
+// launch). Few rows are a launch: one 2.8 us. Rows that lie anywhere cost several times that: 32768 written in 226 us and
+// read as f32 in 99 (in order 72 and 55), where one by one would be 182 and 128; the host does not know the slots.
 #include <algorithm>
 
 #include "cache.h"
@@ -376,7 +378,8 @@ __device__ inline void read_window(const RowsArgs& a, const Window<R>& w, uint8_
         // (two calls: one pointer to either would make its loads ones that do not know which memory)
         if (j >= 0) x = read_piece<T, Q8, VALUE, true>(images + j * in_image(rec), D, t, v >> 5, v & 31);
         else x = read_piece<T, Q8, VALUE, false>(cache + record_of(a, slot, w.head) * rec, D, t, v >> 5, v & 31);
-        // past the caches: 32768 rows of 8 x 128 bf16 values 58.2 us, and 35.7 so
+        // Past the caches: 32768 rows of 8 x 128 values in bf16 56 us, and 35.5 so, in f32 79 and 55. With a kernel behind it
+        // that reads the rows, 103 and 99, and 173 and 169.5; fewer rows are found in the caches then: 8192 in f32 45 and 48.5.
         __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any*>(out + (w.row0 + r) * ld));
     }
 }

@@ -12,24 +12,29 @@
 //      from f16's subnormals.
 //   3. O^T += V^T P^T. The scale of a token's block of values lies along the sum, so it goes into P:
 //      p d_v 2^k, for f32 rows in two f16 terms (the rounding of the first is in the second), for bf16
-//      rows in one, two roundings of 2^-11 of a term, where the result's own is 2^-8. k, the wave's
-//      running exponent, keeps the largest d_v 2^k in [4, 8) and is never negative, so that d_v 2^k is exact
-//      in f16. Tiles with scales of 8 and more (values from 1016, or 64 in q4_0) come last, in a loop of their
-//      own, which makes p d_v 2^k in f32 and holds it in range by m: a token's score counts as higher by as
-//      much as its largest scale times 2^k is above 8. So a large value takes bits of a row's result only by
-//      its own weight there. (Inside the main loop, a branch around the products took 40 registers.)
+//      rows in one, two roundings of 2^-11 of a term, where the result's own is 2^-8: errors are 1.004 to
+//      1.02 times those of the result's rounding alone. (Two terms leave that alone there too, and take 88
+//      us for 73 of 8 trees, 286 for 235 of 2048 tokens behind 2048, 50 for 47 of 64 single tokens in q4_0.)
+//      k, the wave's running exponent, keeps the largest d_v 2^k in [4, 8) and is never negative, so that
+//      d_v 2^k is exact in f16. Tiles with scales of 8 and more (values from 1016, or 64 in q4_0) come last, in
+//      a loop of their own, which makes p d_v 2^k in f32 and holds it in range by m: a token's score counts
+//      as higher by as much as its largest scale times 2^k is above 8. So a large value takes bits of a row's
+//      result only by its own weight there. (Inside the main loop, a branch around the products took 40 registers.)
 // A lane holds the tokens of S^T's rows that it needs as P^T's k: the cache's order of tokens makes
 // them the same (cache.h).
 // The waves' sums are joined in LDS. Work that several workgroups share leaves its parts in the
 // workspace, and a second launch joins them.
 //
-// What bounds it, and what it reaches (8 heads of 128 values, 4 query heads for each, q8_0 unless said):
-//   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 58 us for 277 MB (4.8 TB/s);
+// What bounds it, and what it reaches (8 heads of 128 values, 4 query heads for each, q8_0 unless said; kernels' times in
+// a profiler's trace):
+//   - one new token a sequence: memory. 64 sequences of 128 to 8192 tokens, f32, 58.5 us for 277 MB (4.7 TB/s);
 //     one of 131072 tokens, bf16, values in q4_0, 43 us for 218 MB (5.0 TB/s); the second launch takes 5 us.
+//     With keys and values in q4_0 vector instructions (24 us in bf16, 29 in f32) hide behind the loads (28 us) in
+//     part only: the 64 sequences 43.5 us in bf16, 50 in f32 for 146 MB.
 //   - many rows: the vector unit, whose time and the matrix core's add up here. A wave's tile costs some 180
 //     instructions whatever its rows (8-bit numbers made f16, scales), and for each 16 rows 130 (bf16)
-//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 71 us (0.38 PFLOP/s), a chain
-//     of 512 behind 3584, f32 with twice the products, 108 us (0.3 PFLOP/s).
+//     or 180 (f32) and 16 or 32 products: 8 trees of 48 to 64 tokens, bf16, 72 us (0.37 PFLOP/s), a chain
+//     of 512 behind 3584, f32 with twice the products, 109 us (0.3 PFLOP/s).
 #include <algorithm>
 
 #include "cache.h"
@@ -116,7 +121,9 @@ __device__ inline int seq_tiles(const AttnArgs& a, const Seq& s) {
 // Each workgroup takes an equal part of the range, whatever the sequences' lengths, and finds its place
 // from them by itself. An item that is cut leaves parts in the workspace. Two ways to count:
 //   even: an item costs 1 for each of its parts, which are equal and at most `share` tiles long. For
-//         items few enough that the parts' ends do not matter. (Short ones have one part: no second launch.)
+//         items few enough that the parts' ends do not matter. (An item of one part is finished by its workgroup. The
+//         second launch is made all the same, wherever the table is wide enough for cuts: the host does not know the
+//         lengths. It finds nothing to join then.)
 //   tiles: an item costs its tiles and begin_cost more, what beginning an item takes; workgroups end anywhere.
 struct Found {
     int64_t start;                          // of the sequence
@@ -441,10 +448,16 @@ __device__ inline void load_rows(const AttnArgs& a, int first, int h, int row, i
     r.c = fmaxf(__builtin_amdgcn_ldexpf(a.scale * 1.44269504088896340736f, -e), 1e-37f);
 }
 
-// Waves of a SIMD that the registers are dealt out for, and so workgroups of a compute unit. 8 blocks of values need
-// the 512 registers of one wave: f32, 4 trees of 60 tokens 100 us, with two waves, which spill, 211. 6 blocks
-// with one wave or two: 512 tokens behind 1500 128 and 101 us (though 32 single tokens of 8000 161 and 182).
-// Three waves of 4 blocks and fewer spill as well: 64 sequences of one 86 us, with two 70.
+// Waves of a SIMD that the registers are dealt out for, and so workgroups of a compute unit.
+//   - 8 blocks of values need the 512 registers of one wave: f32, 4 trees of 60 tokens 100 us, with two waves, which
+//     spill, 211.
+//   - 6 blocks, with one wave or two (with which the f32 forms of q8_0 keys or values and the bf16 form of both spill 20
+//     to 104 bytes, none on the main loop's usual path): 512 tokens behind 1488, f32, 121 and 87 us, 8 trees 218 and 167, 64
+//     single tokens in q4_0 90 and 68; but in q8_0 95 and 103, and 32 of 8000 149 and 171.
+//   - 4 blocks, with three waves, which spill 12 to 480 bytes, or two: 64 single tokens, f32, 88 and 63 us, 8 trees 241 and
+//     104. (In q4_0 and bf16 46 and 47.)
+//   - 2 blocks, with three waves, of which three forms spill 20 to 36 bytes, or two: 512 tokens behind 1488 47 and 39 us, one
+//     single token of 65536 23 and 22; but 64 single tokens in q4_0 and bf16 31.5 and 34.
 constexpr int waves_of(int NB) { return NB <= 6 ? 2 : 1; }
 
 // A row's maximum taken anew where a score is far above it, and there alone: its bits do not depend on the other rows
@@ -934,8 +947,9 @@ Plan plan_of(const CacheShape& c, const AttnShape& a) {
     const int64_t items = a.B * ceil_div(rows, p.RQ) * c.heads;
     const int64_t card = 256 * waves_of((int)c.D / 32);                 // workgroups that run at once
     p.cut = most > WHOLE;
-    // Equal parts of items (even) suit few; 128 of one token, 4000 long, 38 us against 32. With 64 the two are alike,
-    // and a call of few short items has one part for each only this way.
+    // Equal parts of items (even) suit few, up to 64 (32 for heads of 256): 64 of one token, 8000 long, 35 us against 37 cut
+    // by tiles, 500 to 8000 long 21 against 25; 32 of 256 values 38 against 41. 128, 8000 long, 63 against 59, and 64 of 256
+    // values 66 against 62.5. A call of few short items has one part for each only this way.
     p.even = !p.cut || items <= card / 8;
     p.spare = p.cut && p.even ? card - items : 0;
     // Many items have few parts each: 8 trees of 48 to 64 tokens, both launches, 85.5 us with a row a workgroup and
