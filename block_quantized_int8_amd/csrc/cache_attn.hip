@@ -482,6 +482,13 @@ template <typename R> __device__ inline void weights(const float (&sc)[8], R& r,
         r.l += p[i];
     }
 }
+// A product as the f32 that it is rounded to. Without it, the compiler makes a term's f16 from the product's factors, with
+// one rounding, where the term is subtracted, and from their f32, with two, where it is used: where those differ, the
+// second term is the first's error no more (one in some thousands, then 2^-11 of the term).
+__device__ inline float rounded(float x) {
+    asm("" : "+v"(x));
+    return x;
+}
 // Two numbers as f16 terms
 template <bool F32> __device__ inline void in_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
     const h2 h = {(_Float16)x0, (_Float16)x1};
@@ -793,7 +800,8 @@ __global__ __launch_bounds__(THREADS, waves_of(NB)) void cache_attn_kernel(AttnA
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const h2 d = as_h2(vw.d[b][i]);
-                        in_terms<F32>(p[n][2 * i] * ((float)d[0] * two_k), p[n][2 * i + 1] * ((float)d[1] * two_k), hi[i], lo[i]);
+                        in_terms<F32>(rounded(p[n][2 * i] * ((float)d[0] * two_k)), rounded(p[n][2 * i + 1] * ((float)d[1] * two_k)),
+                                      hi[i], lo[i]);
                     }
                     pt[n][0] = __builtin_bit_cast(h8, u32x4{hi[0], hi[1], hi[2], hi[3]});
                     if constexpr (F32) pt[n][1] = __builtin_bit_cast(h8, u32x4{lo[0], lo[1], lo[2], lo[3]});

@@ -925,3 +925,21 @@ def test_rows_of_odd_strides(env, dt, rows):
     lens, starts = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([5 + rows], [0, 9]))
     got, want = (mmq.cache_attn(t[:9], caches[0], caches[1], table, lens, starts, 9) for t in (q, x[0]))
     assert q.stride(0) % 2 == 1 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D,kind", [(64, "q8_0"), (128, "q4_0"), (192, "q8_0")])
+def test_small_scores_over_large_scales(env, D, kind, dt):
+    """Weights of all sorts near 1 / N times scales from 8 on, with scores so small that the bound is a few 2^-16: of
+    some 100000 products of a weight and a scale, each has its two terms."""
+    torch, mmq = env
+    c = Case(env, dt=dt, vt=kind, lens=(64,), news=(64,), D=D, heads=2, G=8, seed=39)
+    c.qh *= np.float32(2.0 ** -6)
+    slots = c.table[0, np.arange(64) // 32] * 32 + np.arange(64) % 32
+    size = 10.0 ** c.r.uniform(2, 6 if kind == "q8_0" else 4.9, (64, 2, D // 32, 1))
+    _put_values(c, slots, (c.r.standard_normal((64, 2, D // 32, 32)) * size).reshape(64, 2, D))
+    got = c.device().run().float().cpu().numpy().astype(np.float64)
+    want, bound = _as_held(c)
+    off = np.abs(got - want)
+    print(f"[case]   error at most {(off / bound).max():.4f} of the bound", flush=True)
+    assert np.all(off <= bound)
